@@ -1,5 +1,5 @@
-"""Thin Python binding of liblora_sgmv.so (the C ABI in include/lora_sgmv.h and
-include/lora_pool.h).
+"""Thin Python binding of liblora_sgmv.so (the C ABI in include/lora_sgmv.h,
+include/lora_pool.h and include/lora_train.h).
 
 Argument marshalling only: every step of the LoRA path runs in the library's
 CUDA kernels.  PyTorch supplies device memory and the current stream.  There is
@@ -36,6 +36,19 @@ LORA_SEG_GROUP = 0
 LORA_SEG_CONTIGUOUS = 1
 LORA_FIXED_SCRATCH_MAX_TOKENS = 16384
 LORA_MAX_PROJ = 4
+LORA_DERR_BAD_LABEL = 16
+LORA_DERR_BAD_SEQ = 32
+LORA_DERR_NONFINITE = 64
+LORA_LOGITS_BF16 = 0
+LORA_LOGITS_F32 = 1
+LORA_PREF_SIGMOID = 0
+LORA_PREF_HINGE = 1
+LORA_PREF_IPO = 2
+LORA_PREF_AVERAGE = 1
+LORA_STATE_F32 = 0
+LORA_STATE_E4M3 = 1
+LORA_ADAMW_BLOCK = 64
+LORA_ADAMW_ZERO_GRAD = 1
 
 EXPORTED = (
     "lora_segments_buffer_bytes",
@@ -69,6 +82,14 @@ EXPORTED = (
     "lora_pool_load",
     "lora_pool_evict",
     "lora_pool_mgr_stats",
+    "lora_token_logprobs",
+    "lora_preference_workspace_bytes",
+    "lora_preference_loss",
+    "lora_policy_loss",
+    "lora_adamw_init",
+    "lora_grad_sumsq_workspace_bytes",
+    "lora_grad_sumsq",
+    "lora_adamw_step",
 )
 
 
@@ -103,6 +124,28 @@ class lora_segments_t(ctypes.Structure):
                 ("short_units", ctypes.c_void_p), ("long_units", ctypes.c_void_p),
                 ("scratch", ctypes.c_void_p), ("h_scratch", ctypes.c_void_p),
                 ("k_partials", ctypes.c_void_p)]
+
+
+class lora_pref_opts_t(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("flags", ctypes.c_uint32), ("beta", ctypes.c_float),
+                ("label_smoothing", ctypes.c_float), ("margin", ctypes.c_float), ("grad_scale", ctypes.c_float)]
+
+
+class lora_policy_opts_t(ctypes.Structure):
+    _fields_ = [("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float),
+                ("grad_scale", ctypes.c_float)]
+
+
+class lora_train_proj_t(ctypes.Structure):
+    _fields_ = [("view", lora_pool_view_t), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class lora_adamw_hyper_t(ctypes.Structure):
+    _fields_ = [("step", ctypes.c_int32), ("lr", ctypes.c_float), ("beta1", ctypes.c_float),
+                ("beta2", ctypes.c_float), ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("max_norm", ctypes.c_float), ("grad_scale", ctypes.c_float)]
 
 
 class LoraError(RuntimeError):
@@ -186,6 +229,25 @@ def lib():
         L.lora_pool_evict.argtypes = [vp, i32, view_p, vp]
         L.lora_pool_mgr_stats.restype = i32
         L.lora_pool_mgr_stats.argtypes = [vp, ctypes.POINTER(lora_pool_stats_t)]
+        u32, proj_p = ctypes.c_uint32, ctypes.POINTER(lora_train_proj_t)
+        L.lora_token_logprobs.restype = i32
+        L.lora_token_logprobs.argtypes = [vp, i64, i32, vp, i32, i32, vp, vp, vp, vp]
+        L.lora_preference_workspace_bytes.restype = sz
+        L.lora_preference_workspace_bytes.argtypes = [i32, i32]
+        L.lora_preference_loss.restype = i32
+        L.lora_preference_loss.argtypes = [vp, i64, i32, vp, vp, vp, i32, i32, i32, ctypes.POINTER(lora_pref_opts_t),
+                                           vp, vp, vp, i64, vp, sz, vp, vp]
+        L.lora_policy_loss.restype = i32
+        L.lora_policy_loss.argtypes = [vp, i64, i32, vp, vp, vp, vp, vp, i32, i32, ctypes.POINTER(lora_policy_opts_t),
+                                       vp, vp, vp, vp, i64, vp, vp]
+        L.lora_adamw_init.restype = i32
+        L.lora_adamw_init.argtypes = [proj_p, i32, i32, vp, i32, vp, vp]
+        L.lora_grad_sumsq_workspace_bytes.restype = sz
+        L.lora_grad_sumsq_workspace_bytes.argtypes = [proj_p, i32, i32]
+        L.lora_grad_sumsq.restype = i32
+        L.lora_grad_sumsq.argtypes = [proj_p, i32, vp, i32, i32, vp, vp, sz, vp, vp]
+        L.lora_adamw_step.restype = i32
+        L.lora_adamw_step.argtypes = [proj_p, i32, i32, vp, i32, vp, vp, u32, vp, vp]
         _lib = L
     return _lib
 
@@ -567,3 +629,191 @@ class PoolManager:
 
     def evict(self, adapter: int, view: PoolView, stream=None):
         lora_pool_evict(self.h, adapter, view, stream)
+
+
+# ------------------------------------------------- training: losses on logits --
+
+def _logits(t: torch.Tensor):
+    """(pointer, row stride, dtype code) of a [T, V] matrix of logits."""
+    if t.dtype == torch.bfloat16:
+        code = LORA_LOGITS_BF16
+    elif t.dtype == torch.float32:
+        code = LORA_LOGITS_F32
+    else:
+        raise ValueError("expected bfloat16 or float32 logits")
+    # a matrix of one row may have any stride there
+    return _ptr(t), max(_ld(t), int(t.shape[1])), code
+
+
+def _rows(t: Optional[torch.Tensor], n: int, dtype, what: str):
+    """Pointer of a contiguous vector of n elements of a type, or of none."""
+    if t is not None and (t.numel() != n or t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError("%s: expected %d contiguous elements of %s" % (what, n, dtype))
+    return _ptr(t)
+
+
+def _grad_of(logits: torch.Tensor, dlogits: Optional[torch.Tensor]):
+    if dlogits is None:
+        return ctypes.c_void_p(0), 0
+    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
+        raise ValueError("dlogits: expected the shape and type of the logits")
+    p, ld, _ = _logits(dlogits)
+    return p, ld
+
+
+def lora_token_logprobs(logits: torch.Tensor, labels: torch.Tensor, logp: torch.Tensor,
+                        lse: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None):
+    """logp[t] = logits[t, labels[t]] - lse[t]; logits [T, V] bf16 or fp32, labels int32 [T] (< 0: not counted)."""
+    p, ld, code = _logits(logits)
+    T, V = logits.shape
+    f32 = torch.float32
+    _check(lib().lora_token_logprobs(p, ld, code, _rows(labels, T, torch.int32, "labels"), T, V,
+                                     _rows(logp, T, f32, "logp"), _rows(lse, T, f32, "lse"), _ptr(err),
+                                     _stream(stream)), "lora_token_logprobs")
+
+
+def preference_workspace(T: int, n_pairs: int, device="cuda") -> torch.Tensor:
+    """A workspace for lora_preference_loss over T rows and n_pairs pairs."""
+    return torch.empty(int(lib().lora_preference_workspace_bytes(T, n_pairs)), dtype=torch.uint8, device=device)
+
+
+def lora_preference_loss(logits: torch.Tensor, labels: torch.Tensor, seq_indptr: torch.Tensor, loss: torch.Tensor,
+                         seq_logp: Optional[torch.Tensor], dlogits: Optional[torch.Tensor], workspace: torch.Tensor,
+                         ref_logp: Optional[torch.Tensor] = None, kind: int = LORA_PREF_SIGMOID, beta: float = 0.1,
+                         label_smoothing: float = 0.0, margin: float = 0.0, average: bool = False,
+                         grad_scale: float = 1.0, err: Optional[torch.Tensor] = None, stream=None):
+    """Paired preference loss and its gradient (see include/lora_train.h): sequence s is rows
+    seq_indptr[s] .. seq_indptr[s + 1], pair p sequences 2p (chosen) and 2p + 1 (rejected).
+    dlogits may be the logits (the gradient takes their place) or None."""
+    p, ld, code = _logits(logits)
+    T, V = logits.shape
+    n = int(loss.numel())
+    f32 = torch.float32
+    opts = lora_pref_opts_t(kind, LORA_PREF_AVERAGE if average else 0, beta, label_smoothing, margin, grad_scale)
+    dp, ldd = _grad_of(logits, dlogits)
+    _check(lib().lora_preference_loss(p, ld, code, _rows(labels, T, torch.int32, "labels"),
+                                      _rows(ref_logp, T, f32, "ref_logp"),
+                                      _rows(seq_indptr, 2 * n + 1, torch.int32, "seq_indptr"), n, T, V,
+                                      ctypes.byref(opts), _rows(loss, n, f32, "loss"),
+                                      _rows(seq_logp, 2 * n, f32, "seq_logp"), dp, ldd, _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)),
+           "lora_preference_loss")
+
+
+def lora_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tensor, advantage: torch.Tensor,
+                     logp: torch.Tensor, loss: torch.Tensor, kl: Optional[torch.Tensor],
+                     dlogits: Optional[torch.Tensor], ref_logp: Optional[torch.Tensor] = None,
+                     weight: Optional[torch.Tensor] = None, clip_low: float = 0.2, clip_high: float = 0.2,
+                     kl_coef: float = 0.0, grad_scale: float = 1.0, err: Optional[torch.Tensor] = None, stream=None):
+    """Clipped policy loss with a KL term, per row, and its gradient (see include/lora_train.h).
+    dlogits may be the logits (the gradient takes their place) or None."""
+    p, ld, code = _logits(logits)
+    T, V = logits.shape
+    f32 = torch.float32
+    opts = lora_policy_opts_t(clip_low, clip_high, kl_coef, grad_scale)
+    dp, ldd = _grad_of(logits, dlogits)
+    _check(lib().lora_policy_loss(p, ld, code, _rows(labels, T, torch.int32, "labels"),
+                                  _rows(old_logp, T, f32, "old_logp"), _rows(ref_logp, T, f32, "ref_logp"),
+                                  _rows(advantage, T, f32, "advantage"), _rows(weight, T, f32, "weight"), T, V,
+                                  ctypes.byref(opts), _rows(logp, T, f32, "logp"), _rows(loss, T, f32, "loss"),
+                                  _rows(kl, T, f32, "kl"), dp, ldd, _ptr(err), _stream(stream)), "lora_policy_loss")
+
+
+# --------------------------------------------------- training: optimizer step --
+
+class TrainProj:
+    """One projection's training state beside its pool: gradients, moments and optional fp32
+    weights, all laid out like the pool (lora_train_proj_t).  fp32 moments, or e4m3 codes
+    (float8_e4m3fn or uint8) with bf16 scales."""
+
+    def __init__(self, view: PoolView, grad: torch.Tensor, m: torch.Tensor, v: torch.Tensor,
+                 master: Optional[torch.Tensor] = None, m_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None):
+        n = view.c.n_pages * view.c.page_elems
+        self.state = LORA_STATE_F32 if m_scale is None else LORA_STATE_E4M3
+        size = 4 if self.state == LORA_STATE_F32 else 1
+        for name, t, count, width in (("grad", grad, n, 4), ("m", m, n, size), ("v", v, n, size),
+                                      ("master", master, n, 4), ("m_scale", m_scale, n // LORA_ADAMW_BLOCK, 2),
+                                      ("v_scale", v_scale, n // LORA_ADAMW_BLOCK, 2)):
+            if t is None:
+                continue
+            if t.numel() < count or t.element_size() != width or not t.is_contiguous():
+                raise ValueError("%s: expected %d contiguous elements of %d bytes" % (name, count, width))
+        self.view, self.grad, self.m, self.v = view, grad, m, v
+        self.master, self.m_scale, self.v_scale = master, m_scale, v_scale
+        self.c = lora_train_proj_t(view.c, *(_ptr(t).value for t in (grad, master, m, v, m_scale, v_scale)))
+
+    @classmethod
+    def zeros(cls, view: PoolView, state: int = LORA_STATE_F32, master: bool = False):
+        """Zeroed state for a view (run lora_adamw_init for the adapters that train: it fills master)."""
+        dev = view.pool.device
+        n = view.c.n_pages * view.c.page_elems
+        grad = torch.zeros(n, dtype=torch.float32, device=dev)
+        w = torch.zeros(n, dtype=torch.float32, device=dev) if master else None
+        if state == LORA_STATE_F32:
+            return cls(view, grad, torch.zeros_like(grad), torch.zeros_like(grad), master=w)
+        m, v = (torch.zeros(n, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2))
+        ms, vs = (torch.zeros(n // LORA_ADAMW_BLOCK, dtype=torch.bfloat16, device=dev) for _ in range(2))
+        return cls(view, grad, m, v, master=w, m_scale=ms, v_scale=vs)
+
+
+class TrainSet:
+    """The projections whose adapters step together (lora_train_proj_t array)."""
+
+    def __init__(self, projs):
+        self.projs = list(projs)
+        if not self.projs or any(p.state != self.projs[0].state for p in self.projs):
+            raise ValueError("expected projections with moments of one kind")
+        self.state = self.projs[0].state
+        self.n = len(self.projs)
+        self.n_adapters = int(self.projs[0].view.c.n_adapters)
+        self.c = (lora_train_proj_t * self.n)(*(p.c for p in self.projs))
+
+    def sumsq_workspace(self, n_ids: int) -> torch.Tensor:
+        """A workspace for lora_grad_sumsq over n_ids adapters."""
+        n = int(lib().lora_grad_sumsq_workspace_bytes(self.c, self.n, n_ids))
+        return torch.empty(n, dtype=torch.uint8, device=self.projs[0].grad.device)
+
+
+def adamw_hyper(n_adapters: int, step=1, lr=1e-4, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, max_norm=0.0,
+                grad_scale=1.0, device="cuda") -> torch.Tensor:
+    """A device array of n_adapters lora_adamw_hyper_t as fp32 [n_adapters, 8] (column 0 holds the
+    step's int32 bits: view(torch.int32)[:, 0]); each argument is a value or one value per adapter."""
+    h = np.zeros((n_adapters, 8), dtype=np.float32)
+    h.view(np.int32)[:, 0] = step
+    for k, value in enumerate((lr, beta1, beta2, eps, weight_decay, max_norm, grad_scale)):
+        h[:, 1 + k] = value
+    return torch.from_numpy(h).to(device)
+
+
+def _ids(ids: torch.Tensor):
+    n = int(ids.numel())
+    return _rows(ids, n, torch.int32, "ids"), n
+
+
+def lora_adamw_init(train: TrainSet, ids: torch.Tensor, err: Optional[torch.Tensor] = None, stream=None):
+    """Zero the listed adapters' gradients and moments; master takes the pool's weights."""
+    p, n = _ids(ids)
+    _check(lib().lora_adamw_init(train.c, train.n, train.state, p, n, _ptr(err), _stream(stream)), "lora_adamw_init")
+
+
+def lora_grad_sumsq(train: TrainSet, ids: torch.Tensor, sumsq: torch.Tensor, workspace: torch.Tensor,
+                    accumulate: bool = False, err: Optional[torch.Tensor] = None, stream=None):
+    """sumsq[i] = (accumulate: +=) the sum of squares of adapter i's gradients, for the listed ids."""
+    p, n = _ids(ids)
+    _check(lib().lora_grad_sumsq(train.c, train.n, p, n, 1 if accumulate else 0,
+                                 _rows(sumsq, train.n_adapters, torch.float32, "sumsq"), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)),
+           "lora_grad_sumsq")
+
+
+def lora_adamw_step(train: TrainSet, ids: torch.Tensor, hyper: torch.Tensor, sumsq: Optional[torch.Tensor] = None,
+                    zero_grad: bool = False, err: Optional[torch.Tensor] = None, stream=None):
+    """One AdamW step of the listed adapters in place (see include/lora_train.h); hyper: see adamw_hyper."""
+    p, n = _ids(ids)
+    if hyper.numel() * hyper.element_size() != 32 * train.n_adapters or not hyper.is_contiguous():
+        raise ValueError("hyper: expected %d settings of 32 bytes" % train.n_adapters)
+    _check(lib().lora_adamw_step(train.c, train.n, train.state, p, n, _ptr(hyper),
+                                 _rows(sumsq, train.n_adapters, torch.float32, "sumsq"),
+                                 LORA_ADAMW_ZERO_GRAD if zero_grad else 0, _ptr(err), _stream(stream)),
+           "lora_adamw_step")

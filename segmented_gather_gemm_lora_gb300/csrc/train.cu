@@ -1,0 +1,516 @@
+// Optimizer step of adapter training (lora_train.h): AdamW over the elements of
+// the listed adapters, in their pages, and the gradient norms it clips by.
+//
+// Work is cut into chunks of kChunk consecutive elements of one matrix (A or B)
+// of one projection of one listed adapter; a CTA takes one chunk.  The grid is
+// sized by max_rank (the host does not know the ranks); CTAs past the adapter's
+// rank end at once.
+#include <algorithm>
+#include <cstring>
+
+#include "common.cuh"
+#include "internal.h"
+#include "lora_train.h"
+
+namespace lora {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kGroup = 8;                     // consecutive elements a thread takes: one page each (d % 8 == 0, pages >= 64)
+constexpr int kChunk = kThreads * kGroup;     // elements of a chunk of the step
+constexpr int kSumGroups = 4;                 // groups a thread sums
+constexpr int kSumChunk = kChunk * kSumGroups;
+constexpr int kMaxProj = 16;                  // projections of one launch (kernel parameters below 4 KB)
+constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
+constexpr int kBlockLanes = LORA_ADAMW_BLOCK / kGroup;  // lanes that share a block's scale
+
+struct DevProj {
+  DevView v;
+  float* grad;
+  float* master;
+  void* m;
+  void* r;  // second moments
+  uint16_t* m_scale;
+  uint16_t* r_scale;
+  int chunk0;   // first chunk of the projection in the launch
+  int chunks_a;  // chunks of A at max_rank
+};
+
+struct TrainArgs {
+  DevProj p[kMaxProj];
+  int n_proj;
+  const int32_t* ids;
+  const lora_adamw_hyper_t* hyper;
+  const float* sumsq;
+  float* partial;       // [n_ids][partial_stride]
+  int partial_stride;
+  int partial0;
+  int zero_grad;
+  int32_t* err;
+};
+static_assert(sizeof(TrainArgs) <= 4096, "kernel parameters");
+
+// A chunk's place: which adapter, projection and matrix, and its elements.
+struct Place {
+  int ad;
+  int g;
+  long long e0, size;  // first element; elements of the matrix
+  long long slot0;     // page-list slot of the matrix
+  bool lead;           // the CTA that reports the adapter's errors
+  bool live;           // the chunk holds elements of a good adapter
+};
+
+// Resolve blockIdx into a Place; the whole CTA gets the same answer.
+__device__ __forceinline__ Place find_place(const TrainArgs& a, int chunk) {
+  Place q;
+  const int e = blockIdx.y, c = blockIdx.x;
+  q.ad = a.ids[e];
+  // an id listed before is passed over: its elements have one writer
+  int twice = 0;
+  for (int k = threadIdx.x; k < e; k += blockDim.x) twice |= a.ids[k] == q.ad;
+  q.g = 0;
+  while (q.g + 1 < a.n_proj && c >= a.p[q.g + 1].chunk0) ++q.g;
+  const DevProj& p = a.p[q.g];
+  const int cg = c - p.chunk0;
+  q.lead = cg == 0;
+  const bool is_b = cg >= p.chunks_a;
+  q.e0 = (long long)(is_b ? cg - p.chunks_a : cg) * chunk;
+  const lora_adapter_desc_t d = adapter_desc(p.v, q.ad);
+  q.size = (long long)d.rank * (is_b ? p.v.d_out : p.v.d_in);
+  q.slot0 = is_b ? d.b_page0 : d.a_page0;
+  int bad = 0;
+  if (q.ad < 0 || q.ad >= p.v.n_adapters) bad = LORA_DERR_BAD_ADAPTER;
+  else if (d.rank < 1 || d.rank > p.v.max_rank) bad = LORA_DERR_BAD_RANK;
+  if (__syncthreads_or(twice)) bad = LORA_DERR_BAD_ADAPTER;
+  if (bad && q.lead && threadIdx.x == 0) report(a.err, bad);
+  q.live = !bad && q.e0 < q.size;
+  return q;
+}
+
+// Pool position of element e of the place's matrix, or -1 off the pool.
+__device__ __forceinline__ long long pool_pos(const DevView& v, const Place& q, long long e) {
+  const long long slot = q.slot0 + (e >> v.page_shift);
+  if (slot < 0 || slot >= v.n_page_list) return -1;
+  const long long page = v.page_list[slot];
+  if (page < 0 || page >= v.n_pages) return -1;
+  return (page << v.page_shift) + (e & ((1LL << v.page_shift) - 1));
+}
+
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// Eight e4m3 codes as fp32, and back (to nearest, ties to even, saturating).
+__device__ __forceinline__ void decode8(uint2 c, float (&f)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint16_t two = (uint16_t)((k < 2 ? c.x : c.y) >> (16 * (k & 1)));
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+    asm("{\n\t.reg .f16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+        : "=f"(f[2 * k]), "=f"(f[2 * k + 1])
+        : "r"(h));
+  }
+}
+__device__ __forceinline__ uint2 encode8(const float (&f)[8]) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint16_t two;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(f[2 * k + 1]), "f"(f[2 * k]));
+    w[k >> 1] |= (uint32_t)two << (16 * (k & 1));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// The scale of a block of 64 whose elements the eight lanes around this one hold.
+__device__ __forceinline__ uint16_t block_scale(const float (&x)[8]) {
+  float top = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
+#pragma unroll
+  for (int s = 1; s < kBlockLanes; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  return __bfloat16_as_ushort(__float2bfloat16_rn(top < kTiny ? 0.f : top / 448.f));
+}
+
+__device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+// AdamW.  Bound by memory: per element 24 bytes (fp32 moments), 30 (and fp32
+// weights), 12 (8-bit moments), 4 more to clear the gradient; one pass, each
+// byte moved once.  A thread's eight elements lie on one page, a block's 64 in
+// eight neighbouring lanes, so a block's scale takes three shuffles.
+template <bool kE4M3>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ TrainArgs a) {
+  pdl_wait_then_release();
+  const Place q = find_place(a, kChunk);
+  if (!q.live) return;
+  const DevProj& p = a.p[q.g];
+  const lora_adamw_hyper_t h = a.hyper[q.ad];
+  if (h.step < 1) return;
+  float gs = h.grad_scale;
+  if (a.sumsq != nullptr) {
+    const float ss = a.sumsq[q.ad];
+    if (!(ss < __int_as_float(0x7f800000))) {
+      if (q.lead && threadIdx.x == 0) report(a.err, LORA_DERR_NONFINITE);
+      return;
+    }
+    if (h.max_norm > 0.f) gs *= fminf(1.f, h.max_norm / (sqrtf(ss) * fabsf(gs) + 1e-6f));
+  }
+  // 1 - beta^t = -expm1(t log1p(beta - 1)): beta - 1 is exact, nothing cancels
+  const float c1 = -expm1f((float)h.step * log1pf(h.beta1 - 1.f));
+  const float c2 = -expm1f((float)h.step * log1pf(h.beta2 - 1.f));
+  const float size = h.lr / c1, iroot = 1.f / sqrtf(c2), decay = 1.f - h.lr * h.weight_decay;
+  const float n1 = 1.f - h.beta1, n2 = 1.f - h.beta2;
+
+  const long long e = q.e0 + (long long)threadIdx.x * kGroup;
+  long long pos = -1;
+  if (e < q.size) {
+    pos = pool_pos(p.v, q, e);
+    if (pos < 0) report(a.err, LORA_DERR_BAD_PAGE);
+  }
+  const bool on = pos >= 0;
+  if (!kE4M3 && !on) return;
+  float g[8] = {}, m[8] = {}, r[8] = {}, w[8] = {};
+  uint16_t* const pool = const_cast<uint16_t*>(p.v.pool);
+  if (on) {
+    load8(p.grad + pos, g);
+    if (kE4M3) {
+      const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.m) + pos);
+      const uint2 cr = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.r) + pos);
+      const float sm = bf16_value(p.m_scale[pos / LORA_ADAMW_BLOCK]), sr = bf16_value(p.r_scale[pos / LORA_ADAMW_BLOCK]);
+      decode8(cm, m);
+      decode8(cr, r);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        m[k] *= sm;
+        r[k] *= sr;
+        r[k] *= r[k];
+      }
+    } else {
+      load8(static_cast<const float*>(p.m) + pos, m);
+      load8(static_cast<const float*>(p.r) + pos, r);
+    }
+    if (p.master != nullptr) load8(p.master + pos, w);
+    else unpack8(*reinterpret_cast<const uint4*>(pool + pos), w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      g[k] *= gs;
+      m[k] = h.beta1 * m[k] + n1 * g[k];
+      r[k] = h.beta2 * r[k] + n2 * (g[k] * g[k]);
+    }
+    if (!kE4M3) {
+      store8(static_cast<float*>(p.m) + pos, m);
+      store8(static_cast<float*>(p.r) + pos, r);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      r[k] = sqrtf(r[k]);
+      w[k] = fmaf(w[k], decay, -size * (m[k] / fmaf(r[k], iroot, h.eps)));
+    }
+    if (p.master != nullptr) store8(p.master + pos, w);
+    uint4 b;
+    b.x = pack_bf16x2(w[0], w[1]);
+    b.y = pack_bf16x2(w[2], w[3]);
+    b.z = pack_bf16x2(w[4], w[5]);
+    b.w = pack_bf16x2(w[6], w[7]);
+    *reinterpret_cast<uint4*>(pool + pos) = b;
+    if (a.zero_grad) {
+      const float zero[8] = {};
+      store8(p.grad + pos, zero);
+    }
+  }
+  if (kE4M3) {  // lanes without elements hold zeros, which no scale sees
+    const uint16_t bm = block_scale(m), br = block_scale(r);
+    if (!on) return;
+    const float sm = bf16_value(bm), sr = bf16_value(br);
+    const float im = sm > 0.f ? 1.f / sm : 0.f, ir = sr > 0.f ? 1.f / sr : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      m[k] *= im;
+      r[k] *= ir;
+      if (r[k] > 0.f) r[k] = fmaxf(r[k], 0.001953125f);  // 2^-9, the smallest code
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m) + pos) = encode8(m);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.r) + pos) = encode8(r);
+    if (threadIdx.x % kBlockLanes == 0) {
+      p.m_scale[pos / LORA_ADAMW_BLOCK] = bm;
+      p.r_scale[pos / LORA_ADAMW_BLOCK] = br;
+    }
+  }
+}
+
+template <bool kE4M3>
+__global__ void __launch_bounds__(kThreads) adamw_init_kernel(const __grid_constant__ TrainArgs a) {
+  pdl_wait_then_release();
+  const Place q = find_place(a, kChunk);
+  if (!q.live) return;
+  const DevProj& p = a.p[q.g];
+  const long long e = q.e0 + (long long)threadIdx.x * kGroup;
+  if (e >= q.size) return;
+  const long long pos = pool_pos(p.v, q, e);
+  if (pos < 0) {
+    report(a.err, LORA_DERR_BAD_PAGE);
+    return;
+  }
+  const float zero[8] = {};
+  store8(p.grad + pos, zero);
+  if (kE4M3) {
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m) + pos) = make_uint2(0, 0);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.r) + pos) = make_uint2(0, 0);
+    if (threadIdx.x % kBlockLanes == 0) {
+      p.m_scale[pos / LORA_ADAMW_BLOCK] = 0;
+      p.r_scale[pos / LORA_ADAMW_BLOCK] = 0;
+    }
+  } else {
+    store8(static_cast<float*>(p.m) + pos, zero);
+    store8(static_cast<float*>(p.r) + pos, zero);
+  }
+  if (p.master != nullptr) {
+    float w[8];
+    unpack8(*reinterpret_cast<const uint4*>(p.v.pool + pos), w);
+    store8(p.master + pos, w);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ T block_sum(T x, T* sh) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
+  __syncthreads();
+  T t = 0;
+#pragma unroll
+  for (int k = 0; k < kThreads / 32; ++k) t += sh[k];
+  return t;
+}
+
+// Sum of squares of one chunk of gradients (4 bytes an element, read once) into
+// its own slot of the workspace: the order of the sum is the same in every run.
+__global__ void __launch_bounds__(kThreads) sumsq_kernel(const __grid_constant__ TrainArgs a) {
+  __shared__ float sh[kThreads / 32];
+  pdl_wait_then_release();
+  const Place q = find_place(a, kSumChunk);
+  float s = 0.f;
+  if (q.live) {
+    const DevProj& p = a.p[q.g];
+#pragma unroll
+    for (int j = 0; j < kSumGroups; ++j) {
+      const long long e = q.e0 + (long long)(j * kThreads + threadIdx.x) * kGroup;
+      if (e >= q.size) break;
+      const long long pos = pool_pos(p.v, q, e);
+      if (pos < 0) {
+        report(a.err, LORA_DERR_BAD_PAGE);
+        continue;
+      }
+      float g[8];
+      load8(p.grad + pos, g);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += g[k] * g[k];
+    }
+  }
+  const float t = block_sum(s, sh);
+  if (threadIdx.x == 0) a.partial[(long long)blockIdx.y * a.partial_stride + a.partial0 + blockIdx.x] = t;
+}
+
+struct FinishArgs {
+  const int32_t* ids;
+  int n_adapters;
+  const float* partial;
+  int stride;
+  int accumulate;
+  float* sumsq;
+};
+
+// One CTA an adapter: its chunks' sums, in double, in chunk order by thread.
+__global__ void __launch_bounds__(kThreads) sumsq_finish_kernel(const __grid_constant__ FinishArgs a) {
+  __shared__ double sh[kThreads / 32];
+  pdl_wait_then_release();
+  const int e = blockIdx.x;
+  const int ad = a.ids[e];
+  int twice = 0;
+  for (int k = threadIdx.x; k < e; k += kThreads) twice |= a.ids[k] == ad;
+  if (__syncthreads_or(twice) || ad < 0 || ad >= a.n_adapters) return;
+  double s = 0;
+  for (int k = threadIdx.x; k < a.stride; k += kThreads) s += a.partial[(long long)e * a.stride + k];
+  s = block_sum(s, sh);
+  if (threadIdx.x == 0) a.sumsq[ad] = (float)(a.accumulate ? s + a.sumsq[ad] : s);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Chunks of `chunk` elements of a projection's A and of its B at max_rank.
+long long chunks_of(long long max_rank, long long d, int chunk) { return (max_rank * d + chunk - 1) / chunk; }
+
+lora_status_t check_list(const lora_train_proj_t* projs, int n_proj, const int32_t* ids, int n_ids) {
+  if (projs == nullptr || n_proj < 1 || n_ids < 0) return LORA_ERR_INVALID_ARG;
+  if (n_ids > LORA_MAX_ADAPTERS) return LORA_ERR_UNSUPPORTED;
+  if (n_ids > 0 && ids == nullptr) return LORA_ERR_INVALID_ARG;
+  for (int g = 0; g < n_proj; ++g) {
+    const lora_status_t st = validate_view(&projs[g].view);
+    if (st != LORA_OK) return st;
+    if (projs[g].view.n_adapters != projs[0].view.n_adapters) return LORA_ERR_INVALID_ARG;
+    if (projs[g].grad == nullptr || !aligned16(projs[g].grad)) return LORA_ERR_INVALID_ARG;
+  }
+  return LORA_OK;
+}
+
+bool overlap(const void* a, long long abytes, const void* b, long long bbytes) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
+}
+
+lora_status_t check_state(const lora_train_proj_t* projs, int n_proj, int state) {
+  if (state != LORA_STATE_F32 && state != LORA_STATE_E4M3) return LORA_ERR_INVALID_ARG;
+  for (int g = 0; g < n_proj; ++g) {
+    const lora_train_proj_t& p = projs[g];
+    if (p.m == nullptr || p.v == nullptr || !aligned16(p.m) || !aligned16(p.v) || !aligned16(p.master))
+      return LORA_ERR_INVALID_ARG;
+    const bool scales = p.m_scale != nullptr && p.v_scale != nullptr;
+    if (state == LORA_STATE_E4M3 ? !scales || ((reinterpret_cast<uintptr_t>(p.m_scale) | reinterpret_cast<uintptr_t>(p.v_scale)) & 1u)
+                                 : p.m_scale != nullptr || p.v_scale != nullptr)
+      return LORA_ERR_INVALID_ARG;
+    const long long n = p.view.n_pages * p.view.page_elems, mb = state == LORA_STATE_E4M3 ? n : 4 * n;
+    const long long sb = n / LORA_ADAMW_BLOCK * 2;
+    const struct {
+      const void* at;
+      long long bytes;
+    } w[7] = {{p.view.pool, 2 * n}, {p.grad, 4 * n}, {p.master, 4 * n}, {p.m, mb}, {p.v, mb}, {p.m_scale, sb}, {p.v_scale, sb}};
+    for (int i = 0; i < 7; ++i)
+      for (int k = 0; k < i; ++k)
+        if (overlap(w[i].at, w[i].bytes, w[k].at, w[k].bytes)) return LORA_ERR_INVALID_ARG;
+  }
+  return LORA_OK;
+}
+
+// Fill the projections [g0, g0 + n) of a launch; the number of its chunks.
+long long fill(TrainArgs* a, const lora_train_proj_t* projs, int g0, int n, int chunk) {
+  long long at = 0;
+  a->n_proj = n;
+  for (int k = 0; k < n; ++k) {
+    const lora_train_proj_t& s = projs[g0 + k];
+    DevProj& d = a->p[k];
+    make_dev_view(&s.view, &d.v);
+    d.grad = s.grad;
+    d.master = s.master;
+    d.m = s.m;
+    d.r = s.v;
+    d.m_scale = static_cast<uint16_t*>(s.m_scale);
+    d.r_scale = static_cast<uint16_t*>(s.v_scale);
+    d.chunk0 = (int)at;
+    d.chunks_a = (int)chunks_of(s.view.max_rank, s.view.d_in, chunk);
+    at += d.chunks_a + chunks_of(s.view.max_rank, s.view.d_out, chunk);
+    if (at > 0x7fffffffLL) return -1;
+  }
+  return at;
+}
+
+lora_status_t launch_over(const void* func, TrainArgs* a, const lora_train_proj_t* projs, int n_proj, int n_ids, int chunk,
+                          cudaStream_t s) {
+  for (int g0 = 0; g0 < n_proj; g0 += kMaxProj) {
+    const long long chunks = fill(a, projs, g0, std::min(kMaxProj, n_proj - g0), chunk);
+    if (chunks < 0) return LORA_ERR_UNSUPPORTED;
+    if (launch_pdl(func, dim3((unsigned)chunks, (unsigned)n_ids), dim3(kThreads), 0, s, 0, a) != cudaSuccess)
+      return LORA_ERR_CUDA;
+    a->partial0 += (int)chunks;
+  }
+  return LORA_OK;
+}
+
+// Chunks of all projections in the sum; -1 above what a launch can count.
+long long sum_chunks(const lora_train_proj_t* projs, int n_proj) {
+  long long at = 0;
+  for (int g = 0; g < n_proj; ++g)
+    at += chunks_of(projs[g].view.max_rank, projs[g].view.d_in, kSumChunk) +
+          chunks_of(projs[g].view.max_rank, projs[g].view.d_out, kSumChunk);
+  return at > 0x7fffffffLL ? -1 : at;
+}
+
+}  // namespace
+
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" {
+
+lora_status_t lora_adamw_init(const lora_train_proj_t* projs, int32_t n_proj, int32_t state, const int32_t* ids,
+                              int32_t n_ids, int32_t* dev_err, lora_stream_t stream) {
+  lora_status_t st = check_list(projs, n_proj, ids, n_ids);
+  if (st != LORA_OK || (st = check_state(projs, n_proj, state)) != LORA_OK || n_ids == 0) return st;
+  TrainArgs a;
+  memset(&a, 0, sizeof(a));
+  a.ids = ids;
+  a.err = dev_err;
+  return launch_over(state == LORA_STATE_E4M3 ? (const void*)adamw_init_kernel<true> : (const void*)adamw_init_kernel<false>,
+                     &a, projs, n_proj, n_ids, kChunk, (cudaStream_t)stream);
+}
+
+size_t lora_grad_sumsq_workspace_bytes(const lora_train_proj_t* projs, int32_t n_proj, int32_t n_ids) {
+  if (projs == nullptr || n_proj < 1 || n_ids < 0 || n_ids > LORA_MAX_ADAPTERS) return 0;
+  for (int g = 0; g < n_proj; ++g)
+    if (validate_view(&projs[g].view) != LORA_OK) return 0;
+  const long long n = sum_chunks(projs, n_proj);
+  return n < 0 ? 0 : (size_t)(((long long)n_ids * n * 4 + 16) / 16 * 16);
+}
+
+lora_status_t lora_grad_sumsq(const lora_train_proj_t* projs, int32_t n_proj, const int32_t* ids, int32_t n_ids,
+                              int32_t accumulate, float* sumsq, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_err, lora_stream_t stream) {
+  lora_status_t st = check_list(projs, n_proj, ids, n_ids);
+  if (st != LORA_OK) return st;
+  if (sumsq == nullptr || (reinterpret_cast<uintptr_t>(sumsq) & 3u) != 0) return LORA_ERR_INVALID_ARG;
+  if (n_ids == 0) return LORA_OK;
+  if (workspace == nullptr || !aligned16(workspace)) return LORA_ERR_INVALID_ARG;
+  const long long n = sum_chunks(projs, n_proj);
+  if (n < 0) return LORA_ERR_UNSUPPORTED;
+  if (workspace_bytes < lora_grad_sumsq_workspace_bytes(projs, n_proj, n_ids)) return LORA_ERR_WORKSPACE;
+  TrainArgs a;
+  memset(&a, 0, sizeof(a));
+  a.ids = ids;
+  a.err = dev_err;
+  a.partial = static_cast<float*>(workspace);
+  a.partial_stride = (int)n;
+  st = launch_over((const void*)sumsq_kernel, &a, projs, n_proj, n_ids, kSumChunk, (cudaStream_t)stream);
+  if (st != LORA_OK) return st;
+  FinishArgs f;
+  memset(&f, 0, sizeof(f));
+  f.ids = ids;
+  f.n_adapters = projs[0].view.n_adapters;
+  f.partial = a.partial;
+  f.stride = (int)n;
+  f.accumulate = accumulate ? 1 : 0;
+  f.sumsq = sumsq;
+  return launch_pdl((const void*)sumsq_finish_kernel, dim3((unsigned)n_ids), dim3(kThreads), 0, (cudaStream_t)stream, 0,
+                    &f) == cudaSuccess
+             ? LORA_OK
+             : LORA_ERR_CUDA;
+}
+
+lora_status_t lora_adamw_step(const lora_train_proj_t* projs, int32_t n_proj, int32_t state, const int32_t* ids,
+                              int32_t n_ids, const lora_adamw_hyper_t* hyper, const float* sumsq, uint32_t flags,
+                              int32_t* dev_err, lora_stream_t stream) {
+  if (flags & ~(uint32_t)LORA_ADAMW_ZERO_GRAD) return LORA_ERR_INVALID_ARG;
+  lora_status_t st = check_list(projs, n_proj, ids, n_ids);
+  if (st != LORA_OK || (st = check_state(projs, n_proj, state)) != LORA_OK) return st;
+  if (hyper == nullptr || (reinterpret_cast<uintptr_t>(hyper) & 3u) != 0 || (reinterpret_cast<uintptr_t>(sumsq) & 3u) != 0)
+    return LORA_ERR_INVALID_ARG;
+  if (n_ids == 0) return LORA_OK;
+  TrainArgs a;
+  memset(&a, 0, sizeof(a));
+  a.ids = ids;
+  a.hyper = hyper;
+  a.sumsq = sumsq;
+  a.zero_grad = (flags & LORA_ADAMW_ZERO_GRAD) ? 1 : 0;
+  a.err = dev_err;
+  return launch_over(state == LORA_STATE_E4M3 ? (const void*)adamw_kernel<true> : (const void*)adamw_kernel<false>, &a,
+                     projs, n_proj, n_ids, kChunk, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,8 +1,8 @@
 // Optimizer step of adapter training (lora_train.h): AdamW over the elements of
 // the listed adapters, in their pages, and the gradient norms it clips by.
 //
-// Work is cut into chunks of kChunk consecutive elements of one matrix (A or B)
-// of one projection of one listed adapter; a CTA takes one chunk.  The grid is
+// Work is cut into chunks of consecutive elements of one matrix (A or B) of one
+// projection of one listed adapter; a CTA takes one chunk, span by span.  The grid is
 // sized by max_rank (the host does not know the ranks); CTAs past the adapter's
 // rank end at once.
 #include <algorithm>
@@ -18,9 +18,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kGroup = 8;                     // consecutive elements a thread takes: one page each (d % 8 == 0, pages >= 64)
-constexpr int kChunk = kThreads * kGroup;     // elements of a chunk of the step
-constexpr int kSumGroups = 4;                 // groups a thread sums
-constexpr int kSumChunk = kChunk * kSumGroups;
+constexpr int kSpan = kThreads * kGroup;      // elements the CTA takes at once
+constexpr int kSumGroups = 4;                 // spans of a chunk of the sum
+constexpr int kSumChunk = kSpan * kSumGroups;
 constexpr int kMaxProj = 16;                  // projections of one launch (kernel parameters below 4 KB)
 constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
 constexpr int kBlockLanes = LORA_ADAMW_BLOCK / kGroup;  // lanes that share a block's scale
@@ -47,6 +47,7 @@ struct TrainArgs {
   int partial_stride;
   int partial0;
   int zero_grad;
+  int spans;  // spans of a chunk
   int32_t* err;
 };
 static_assert(sizeof(TrainArgs) <= 4096, "kernel parameters");
@@ -62,8 +63,9 @@ struct Place {
 };
 
 // Resolve blockIdx into a Place; the whole CTA gets the same answer.
-__device__ __forceinline__ Place find_place(const TrainArgs& a, int chunk) {
+__device__ __forceinline__ Place find_place(const TrainArgs& a) {
   Place q;
+  const int chunk = a.spans * kSpan;
   const int e = blockIdx.y, c = blockIdx.x;
   q.ad = a.ids[e];
   // an id listed before is passed over: its elements have one writer
@@ -142,106 +144,143 @@ __device__ __forceinline__ uint16_t block_scale(const float (&x)[8]) {
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 
+__device__ __forceinline__ float sqrt_fast(float x) {  // 2^-23 relative
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {  // one unit
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// What the step takes from an adapter's settings, worked out by one thread.
+struct StepShared {
+  float gs, b1, n1, b2, n2, size, iroot, eps, decay;
+  int skip;
+};
+
 // AdamW.  Bound by memory: per element 24 bytes (fp32 moments), 30 (and fp32
 // weights), 12 (8-bit moments), 4 more to clear the gradient; one pass, each
 // byte moved once.  A thread's eight elements lie on one page, a block's 64 in
-// eight neighbouring lanes, so a block's scale takes three shuffles.
+// eight neighbouring lanes, so a block's scale takes three shuffles.  Roots and
+// quotients are the hardware's approximations (2^-22 of an update, which is
+// itself a small part of a weight): with 8-bit moments the IEEE forms' extra
+// instructions, not memory, set the time.
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ TrainArgs a) {
+  __shared__ StepShared sh;
   pdl_wait_then_release();
-  const Place q = find_place(a, kChunk);
+  const Place q = find_place(a);
   if (!q.live) return;
   const DevProj& p = a.p[q.g];
-  const lora_adamw_hyper_t h = a.hyper[q.ad];
-  if (h.step < 1) return;
-  float gs = h.grad_scale;
-  if (a.sumsq != nullptr) {
-    const float ss = a.sumsq[q.ad];
-    if (!(ss < __int_as_float(0x7f800000))) {
-      if (q.lead && threadIdx.x == 0) report(a.err, LORA_DERR_NONFINITE);
-      return;
+  if (threadIdx.x == 0) {
+    const lora_adamw_hyper_t h = a.hyper[q.ad];
+    float gs = h.grad_scale;
+    sh.skip = h.step < 1;
+    if (a.sumsq != nullptr) {
+      const float ss = a.sumsq[q.ad];
+      if (!(ss < __int_as_float(0x7f800000))) {
+        if (q.lead && !sh.skip) report(a.err, LORA_DERR_NONFINITE);
+        sh.skip = 1;
+      } else if (h.max_norm > 0.f) {
+        gs *= fminf(1.f, h.max_norm / (sqrtf(ss) * fabsf(gs) + 1e-6f));
+      }
     }
-    if (h.max_norm > 0.f) gs *= fminf(1.f, h.max_norm / (sqrtf(ss) * fabsf(gs) + 1e-6f));
+    // 1 - beta^t = -expm1(t log1p(beta - 1)): beta - 1 is exact, nothing cancels
+    const float c1 = -expm1f((float)h.step * log1pf(h.beta1 - 1.f));
+    const float c2 = -expm1f((float)h.step * log1pf(h.beta2 - 1.f));
+    sh.gs = gs;
+    sh.b1 = h.beta1;
+    sh.n1 = 1.f - h.beta1;
+    sh.b2 = h.beta2;
+    sh.n2 = 1.f - h.beta2;
+    sh.size = h.lr / c1;
+    sh.iroot = 1.f / sqrtf(c2);
+    sh.eps = h.eps;
+    sh.decay = 1.f - h.lr * h.weight_decay;
   }
-  // 1 - beta^t = -expm1(t log1p(beta - 1)): beta - 1 is exact, nothing cancels
-  const float c1 = -expm1f((float)h.step * log1pf(h.beta1 - 1.f));
-  const float c2 = -expm1f((float)h.step * log1pf(h.beta2 - 1.f));
-  const float size = h.lr / c1, iroot = 1.f / sqrtf(c2), decay = 1.f - h.lr * h.weight_decay;
-  const float n1 = 1.f - h.beta1, n2 = 1.f - h.beta2;
-
-  const long long e = q.e0 + (long long)threadIdx.x * kGroup;
-  long long pos = -1;
-  if (e < q.size) {
-    pos = pool_pos(p.v, q, e);
-    if (pos < 0) report(a.err, LORA_DERR_BAD_PAGE);
-  }
-  const bool on = pos >= 0;
-  if (!kE4M3 && !on) return;
-  float g[8] = {}, m[8] = {}, r[8] = {}, w[8] = {};
+  __syncthreads();
+  if (sh.skip) return;
+  const float gs = sh.gs, b1 = sh.b1, n1 = sh.n1, b2 = sh.b2, n2 = sh.n2;
+  const float size = sh.size, iroot = sh.iroot, eps = sh.eps, decay = sh.decay;
   uint16_t* const pool = const_cast<uint16_t*>(p.v.pool);
-  if (on) {
-    load8(p.grad + pos, g);
-    if (kE4M3) {
-      const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.m) + pos);
-      const uint2 cr = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.r) + pos);
-      const float sm = bf16_value(p.m_scale[pos / LORA_ADAMW_BLOCK]), sr = bf16_value(p.r_scale[pos / LORA_ADAMW_BLOCK]);
-      decode8(cm, m);
-      decode8(cr, r);
+  for (int j = 0; j < a.spans; ++j) {
+    if (q.e0 + (long long)j * kSpan >= q.size) break;
+    const long long e = q.e0 + (long long)(j * kThreads + threadIdx.x) * kGroup;
+    long long pos = -1;
+    if (e < q.size) {
+      pos = pool_pos(p.v, q, e);
+      if (pos < 0) report(a.err, LORA_DERR_BAD_PAGE);
+    }
+    const bool on = pos >= 0;
+    float m[8] = {}, r[8] = {};
+    if (on) {
+      float g[8], w[8];
+      load8(p.grad + pos, g);
+      if (kE4M3) {
+        const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.m) + pos);
+        const uint2 cr = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.r) + pos);
+        const float sm = bf16_value(p.m_scale[pos / LORA_ADAMW_BLOCK]), sr = bf16_value(p.r_scale[pos / LORA_ADAMW_BLOCK]);
+        decode8(cm, m);
+        decode8(cr, r);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          m[k] *= sm;
+          r[k] *= sr;
+          r[k] *= r[k];
+        }
+      } else {
+        load8(static_cast<const float*>(p.m) + pos, m);
+        load8(static_cast<const float*>(p.r) + pos, r);
+      }
+      if (p.master != nullptr) load8(p.master + pos, w);
+      else unpack8(*reinterpret_cast<const uint4*>(pool + pos), w);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        m[k] *= sm;
-        r[k] *= sr;
-        r[k] *= r[k];
+        g[k] *= gs;
+        m[k] = b1 * m[k] + n1 * g[k];
+        r[k] = b2 * r[k] + n2 * (g[k] * g[k]);
       }
-    } else {
-      load8(static_cast<const float*>(p.m) + pos, m);
-      load8(static_cast<const float*>(p.r) + pos, r);
-    }
-    if (p.master != nullptr) load8(p.master + pos, w);
-    else unpack8(*reinterpret_cast<const uint4*>(pool + pos), w);
+      if (!kE4M3) {
+        store8(static_cast<float*>(p.m) + pos, m);
+        store8(static_cast<float*>(p.r) + pos, r);
+      }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      g[k] *= gs;
-      m[k] = h.beta1 * m[k] + n1 * g[k];
-      r[k] = h.beta2 * r[k] + n2 * (g[k] * g[k]);
+      for (int k = 0; k < 8; ++k) {
+        r[k] = sqrt_fast(r[k]);
+        w[k] = fmaf(w[k], decay, -size * (m[k] * rcp_fast(fmaf(r[k], iroot, eps))));
+      }
+      if (p.master != nullptr) store8(p.master + pos, w);
+      uint4 b;
+      b.x = pack_bf16x2(w[0], w[1]);
+      b.y = pack_bf16x2(w[2], w[3]);
+      b.z = pack_bf16x2(w[4], w[5]);
+      b.w = pack_bf16x2(w[6], w[7]);
+      *reinterpret_cast<uint4*>(pool + pos) = b;
+      if (a.zero_grad) {
+        const float zero[8] = {};
+        store8(p.grad + pos, zero);
+      }
     }
-    if (!kE4M3) {
-      store8(static_cast<float*>(p.m) + pos, m);
-      store8(static_cast<float*>(p.r) + pos, r);
-    }
+    if (kE4M3) {  // lanes without elements hold zeros, which no scale sees
+      const uint16_t bm = block_scale(m), br = block_scale(r);
+      if (!on) continue;
+      const float sm = bf16_value(bm), sr = bf16_value(br);
+      const float im = sm > 0.f ? rcp_fast(sm) : 0.f, ir = sr > 0.f ? rcp_fast(sr) : 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      r[k] = sqrtf(r[k]);
-      w[k] = fmaf(w[k], decay, -size * (m[k] / fmaf(r[k], iroot, h.eps)));
-    }
-    if (p.master != nullptr) store8(p.master + pos, w);
-    uint4 b;
-    b.x = pack_bf16x2(w[0], w[1]);
-    b.y = pack_bf16x2(w[2], w[3]);
-    b.z = pack_bf16x2(w[4], w[5]);
-    b.w = pack_bf16x2(w[6], w[7]);
-    *reinterpret_cast<uint4*>(pool + pos) = b;
-    if (a.zero_grad) {
-      const float zero[8] = {};
-      store8(p.grad + pos, zero);
-    }
-  }
-  if (kE4M3) {  // lanes without elements hold zeros, which no scale sees
-    const uint16_t bm = block_scale(m), br = block_scale(r);
-    if (!on) return;
-    const float sm = bf16_value(bm), sr = bf16_value(br);
-    const float im = sm > 0.f ? 1.f / sm : 0.f, ir = sr > 0.f ? 1.f / sr : 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      m[k] *= im;
-      r[k] *= ir;
-      if (r[k] > 0.f) r[k] = fmaxf(r[k], 0.001953125f);  // 2^-9, the smallest code
-    }
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m) + pos) = encode8(m);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.r) + pos) = encode8(r);
-    if (threadIdx.x % kBlockLanes == 0) {
-      p.m_scale[pos / LORA_ADAMW_BLOCK] = bm;
-      p.r_scale[pos / LORA_ADAMW_BLOCK] = br;
+      for (int k = 0; k < 8; ++k) {
+        m[k] *= im;
+        r[k] *= ir;
+        if (r[k] > 0.f) r[k] = fmaxf(r[k], 0.001953125f);  // 2^-9, the smallest code
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m) + pos) = encode8(m);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.r) + pos) = encode8(r);
+      if (threadIdx.x % kBlockLanes == 0) {
+        p.m_scale[pos / LORA_ADAMW_BLOCK] = bm;
+        p.r_scale[pos / LORA_ADAMW_BLOCK] = br;
+      }
     }
   }
 }
@@ -249,33 +288,35 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads) adamw_init_kernel(const __grid_constant__ TrainArgs a) {
   pdl_wait_then_release();
-  const Place q = find_place(a, kChunk);
+  const Place q = find_place(a);
   if (!q.live) return;
   const DevProj& p = a.p[q.g];
-  const long long e = q.e0 + (long long)threadIdx.x * kGroup;
-  if (e >= q.size) return;
-  const long long pos = pool_pos(p.v, q, e);
-  if (pos < 0) {
-    report(a.err, LORA_DERR_BAD_PAGE);
-    return;
-  }
-  const float zero[8] = {};
-  store8(p.grad + pos, zero);
-  if (kE4M3) {
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m) + pos) = make_uint2(0, 0);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.r) + pos) = make_uint2(0, 0);
-    if (threadIdx.x % kBlockLanes == 0) {
-      p.m_scale[pos / LORA_ADAMW_BLOCK] = 0;
-      p.r_scale[pos / LORA_ADAMW_BLOCK] = 0;
+  for (int j = 0; j < a.spans; ++j) {
+    const long long e = q.e0 + (long long)(j * kThreads + threadIdx.x) * kGroup;
+    if (e >= q.size) return;
+    const long long pos = pool_pos(p.v, q, e);
+    if (pos < 0) {
+      report(a.err, LORA_DERR_BAD_PAGE);
+      continue;
     }
-  } else {
-    store8(static_cast<float*>(p.m) + pos, zero);
-    store8(static_cast<float*>(p.r) + pos, zero);
-  }
-  if (p.master != nullptr) {
-    float w[8];
-    unpack8(*reinterpret_cast<const uint4*>(p.v.pool + pos), w);
-    store8(p.master + pos, w);
+    const float zero[8] = {};
+    store8(p.grad + pos, zero);
+    if (kE4M3) {
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m) + pos) = make_uint2(0, 0);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.r) + pos) = make_uint2(0, 0);
+      if (threadIdx.x % kBlockLanes == 0) {
+        p.m_scale[pos / LORA_ADAMW_BLOCK] = 0;
+        p.r_scale[pos / LORA_ADAMW_BLOCK] = 0;
+      }
+    } else {
+      store8(static_cast<float*>(p.m) + pos, zero);
+      store8(static_cast<float*>(p.r) + pos, zero);
+    }
+    if (p.master != nullptr) {
+      float w[8];
+      unpack8(*reinterpret_cast<const uint4*>(p.v.pool + pos), w);
+      store8(p.master + pos, w);
+    }
   }
 }
 
@@ -296,23 +337,25 @@ __device__ __forceinline__ T block_sum(T x, T* sh) {
 __global__ void __launch_bounds__(kThreads) sumsq_kernel(const __grid_constant__ TrainArgs a) {
   __shared__ float sh[kThreads / 32];
   pdl_wait_then_release();
-  const Place q = find_place(a, kSumChunk);
+  const Place q = find_place(a);
   float s = 0.f;
   if (q.live) {
     const DevProj& p = a.p[q.g];
+    long long pos[kSumGroups];  // all first, then all loads: a thread has its 128 bytes in flight
 #pragma unroll
     for (int j = 0; j < kSumGroups; ++j) {
       const long long e = q.e0 + (long long)(j * kThreads + threadIdx.x) * kGroup;
-      if (e >= q.size) break;
-      const long long pos = pool_pos(p.v, q, e);
-      if (pos < 0) {
-        report(a.err, LORA_DERR_BAD_PAGE);
-        continue;
-      }
-      float g[8];
-      load8(p.grad + pos, g);
+      pos[j] = e < q.size ? pool_pos(p.v, q, e) : -2;
+    }
+    float g[kSumGroups][8] = {};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s += g[k] * g[k];
+    for (int j = 0; j < kSumGroups; ++j)
+      if (pos[j] >= 0) load8(p.grad + pos[j], g[j]);
+#pragma unroll
+    for (int j = 0; j < kSumGroups; ++j) {
+      if (pos[j] == -1) report(a.err, LORA_DERR_BAD_PAGE);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += g[j][k] * g[j][k];
     }
   }
   const float t = block_sum(s, sh);
@@ -411,16 +454,26 @@ long long fill(TrainArgs* a, const lora_train_proj_t* projs, int g0, int n, int 
   return at;
 }
 
-lora_status_t launch_over(const void* func, TrainArgs* a, const lora_train_proj_t* projs, int n_proj, int n_ids, int chunk,
+lora_status_t launch_over(const void* func, TrainArgs* a, const lora_train_proj_t* projs, int n_proj, int n_ids, int spans,
                           cudaStream_t s) {
+  a->spans = spans;
   for (int g0 = 0; g0 < n_proj; g0 += kMaxProj) {
-    const long long chunks = fill(a, projs, g0, std::min(kMaxProj, n_proj - g0), chunk);
+    const long long chunks = fill(a, projs, g0, std::min(kMaxProj, n_proj - g0), spans * kSpan);
     if (chunks < 0) return LORA_ERR_UNSUPPORTED;
     if (launch_pdl(func, dim3((unsigned)chunks, (unsigned)n_ids), dim3(kThreads), 0, s, 0, a) != cudaSuccess)
       return LORA_ERR_CUDA;
     a->partial0 += (int)chunks;
   }
   return LORA_OK;
+}
+
+// Spans of a chunk: four, which spreads a CTA's start over 8192 elements, once
+// the launch still has several CTAs for every place on the GPU.
+int step_spans(const lora_train_proj_t* projs, int n_proj, int n_ids) {
+  long long chunks = 0;
+  for (int g = 0; g < n_proj; ++g)
+    chunks += chunks_of(projs[g].view.max_rank, (long long)projs[g].view.d_in + projs[g].view.d_out, 4 * kSpan);
+  return chunks * n_ids >= 16LL * sm_count() ? 4 : 1;
 }
 
 // Chunks of all projections in the sum; -1 above what a launch can count.
@@ -449,7 +502,7 @@ lora_status_t lora_adamw_init(const lora_train_proj_t* projs, int32_t n_proj, in
   a.ids = ids;
   a.err = dev_err;
   return launch_over(state == LORA_STATE_E4M3 ? (const void*)adamw_init_kernel<true> : (const void*)adamw_init_kernel<false>,
-                     &a, projs, n_proj, n_ids, kChunk, (cudaStream_t)stream);
+                     &a, projs, n_proj, n_ids, step_spans(projs, n_proj, n_ids), (cudaStream_t)stream);
 }
 
 size_t lora_grad_sumsq_workspace_bytes(const lora_train_proj_t* projs, int32_t n_proj, int32_t n_ids) {
@@ -477,7 +530,7 @@ lora_status_t lora_grad_sumsq(const lora_train_proj_t* projs, int32_t n_proj, co
   a.err = dev_err;
   a.partial = static_cast<float*>(workspace);
   a.partial_stride = (int)n;
-  st = launch_over((const void*)sumsq_kernel, &a, projs, n_proj, n_ids, kSumChunk, (cudaStream_t)stream);
+  st = launch_over((const void*)sumsq_kernel, &a, projs, n_proj, n_ids, kSumGroups, (cudaStream_t)stream);
   if (st != LORA_OK) return st;
   FinishArgs f;
   memset(&f, 0, sizeof(f));
@@ -510,7 +563,7 @@ lora_status_t lora_adamw_step(const lora_train_proj_t* projs, int32_t n_proj, in
   a.zero_grad = (flags & LORA_ADAMW_ZERO_GRAD) ? 1 : 0;
   a.err = dev_err;
   return launch_over(state == LORA_STATE_E4M3 ? (const void*)adamw_kernel<true> : (const void*)adamw_kernel<false>, &a,
-                     projs, n_proj, n_ids, kChunk, (cudaStream_t)stream);
+                     projs, n_proj, n_ids, step_spans(projs, n_proj, n_ids), (cudaStream_t)stream);
 }
 
 }  // extern "C"

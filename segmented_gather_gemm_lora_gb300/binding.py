@@ -266,8 +266,8 @@ def _check(status: int, what: str):
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without building a torch.cuda.Stream around it
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -634,41 +634,49 @@ class PoolManager:
 # ------------------------------------------------- training: losses on logits --
 
 def _logits(t: torch.Tensor):
-    """(pointer, row stride, dtype code) of a [T, V] matrix of logits."""
-    if t.dtype == torch.bfloat16:
-        code = LORA_LOGITS_BF16
-    elif t.dtype == torch.float32:
-        code = LORA_LOGITS_F32
-    else:
+    """(address, row stride, dtype code, T, V) of a [T, V] matrix of logits."""
+    code = _LOGITS_CODE.get(t.dtype)
+    if code is None:
         raise ValueError("expected bfloat16 or float32 logits")
-    # a matrix of one row may have any stride there
-    return _ptr(t), max(_ld(t), int(t.shape[1])), code
+    T, V = t.shape
+    ld, one = t.stride()
+    if one != 1 and V > 1:
+        raise ValueError("expected a 2-D row-major tensor with unit column stride")
+    return t.data_ptr(), max(ld, V), code, T, V  # a matrix of one row may have any stride there
 
 
-def _rows(t: Optional[torch.Tensor], n: int, dtype, what: str):
-    """Pointer of a contiguous vector of n elements of a type, or of none."""
-    if t is not None and (t.numel() != n or t.dtype != dtype or not t.is_contiguous()):
+_LOGITS_CODE = {torch.bfloat16: LORA_LOGITS_BF16, torch.float32: LORA_LOGITS_F32}
+
+
+def _rows(t: Optional[torch.Tensor], n: int, dtype, what: str) -> int:
+    """Address of a contiguous vector of n elements of a type, 0 of none.  (Addresses as plain
+    integers: these calls are short, and a ctypes object for each argument costs as much as a check.)"""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError("%s: expected %d contiguous elements of %s" % (what, n, dtype))
-    return _ptr(t)
+    return t.data_ptr()
+
+
+def _addr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _grad_of(logits: torch.Tensor, dlogits: Optional[torch.Tensor]):
     if dlogits is None:
-        return ctypes.c_void_p(0), 0
-    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
+        return 0, 0
+    if dlogits is not logits and (dlogits.shape != logits.shape or dlogits.dtype is not logits.dtype):
         raise ValueError("dlogits: expected the shape and type of the logits")
-    p, ld, _ = _logits(dlogits)
-    return p, ld
+    return _logits(dlogits)[:2]
 
 
 def lora_token_logprobs(logits: torch.Tensor, labels: torch.Tensor, logp: torch.Tensor,
                         lse: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None):
     """logp[t] = logits[t, labels[t]] - lse[t]; logits [T, V] bf16 or fp32, labels int32 [T] (< 0: not counted)."""
-    p, ld, code = _logits(logits)
-    T, V = logits.shape
+    p, ld, code, T, V = _logits(logits)
     f32 = torch.float32
     _check(lib().lora_token_logprobs(p, ld, code, _rows(labels, T, torch.int32, "labels"), T, V,
-                                     _rows(logp, T, f32, "logp"), _rows(lse, T, f32, "lse"), _ptr(err),
+                                     _rows(logp, T, f32, "logp"), _rows(lse, T, f32, "lse"), _addr(err),
                                      _stream(stream)), "lora_token_logprobs")
 
 
@@ -685,8 +693,7 @@ def lora_preference_loss(logits: torch.Tensor, labels: torch.Tensor, seq_indptr:
     """Paired preference loss and its gradient (see include/lora_train.h): sequence s is rows
     seq_indptr[s] .. seq_indptr[s + 1], pair p sequences 2p (chosen) and 2p + 1 (rejected).
     dlogits may be the logits (the gradient takes their place) or None."""
-    p, ld, code = _logits(logits)
-    T, V = logits.shape
+    p, ld, code, T, V = _logits(logits)
     n = int(loss.numel())
     f32 = torch.float32
     opts = lora_pref_opts_t(kind, LORA_PREF_AVERAGE if average else 0, beta, label_smoothing, margin, grad_scale)
@@ -695,8 +702,8 @@ def lora_preference_loss(logits: torch.Tensor, labels: torch.Tensor, seq_indptr:
                                       _rows(ref_logp, T, f32, "ref_logp"),
                                       _rows(seq_indptr, 2 * n + 1, torch.int32, "seq_indptr"), n, T, V,
                                       ctypes.byref(opts), _rows(loss, n, f32, "loss"),
-                                      _rows(seq_logp, 2 * n, f32, "seq_logp"), dp, ldd, _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)),
+                                      _rows(seq_logp, 2 * n, f32, "seq_logp"), dp, ldd, _addr(workspace),
+                                      workspace.numel() * workspace.element_size(), _addr(err), _stream(stream)),
            "lora_preference_loss")
 
 
@@ -707,8 +714,7 @@ def lora_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch
                      kl_coef: float = 0.0, grad_scale: float = 1.0, err: Optional[torch.Tensor] = None, stream=None):
     """Clipped policy loss with a KL term, per row, and its gradient (see include/lora_train.h).
     dlogits may be the logits (the gradient takes their place) or None."""
-    p, ld, code = _logits(logits)
-    T, V = logits.shape
+    p, ld, code, T, V = _logits(logits)
     f32 = torch.float32
     opts = lora_policy_opts_t(clip_low, clip_high, kl_coef, grad_scale)
     dp, ldd = _grad_of(logits, dlogits)
@@ -716,7 +722,7 @@ def lora_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch
                                   _rows(old_logp, T, f32, "old_logp"), _rows(ref_logp, T, f32, "ref_logp"),
                                   _rows(advantage, T, f32, "advantage"), _rows(weight, T, f32, "weight"), T, V,
                                   ctypes.byref(opts), _rows(logp, T, f32, "logp"), _rows(loss, T, f32, "loss"),
-                                  _rows(kl, T, f32, "kl"), dp, ldd, _ptr(err), _stream(stream)), "lora_policy_loss")
+                                  _rows(kl, T, f32, "kl"), dp, ldd, _addr(err), _stream(stream)), "lora_policy_loss")
 
 
 # --------------------------------------------------- training: optimizer step --
@@ -741,7 +747,7 @@ class TrainProj:
                 raise ValueError("%s: expected %d contiguous elements of %d bytes" % (name, count, width))
         self.view, self.grad, self.m, self.v = view, grad, m, v
         self.master, self.m_scale, self.v_scale = master, m_scale, v_scale
-        self.c = lora_train_proj_t(view.c, *(_ptr(t).value for t in (grad, master, m, v, m_scale, v_scale)))
+        self.c = lora_train_proj_t(view.c, *(_addr(t) or None for t in (grad, master, m, v, m_scale, v_scale)))
 
     @classmethod
     def zeros(cls, view: PoolView, state: int = LORA_STATE_F32, master: bool = False):
@@ -794,7 +800,7 @@ def _ids(ids: torch.Tensor):
 def lora_adamw_init(train: TrainSet, ids: torch.Tensor, err: Optional[torch.Tensor] = None, stream=None):
     """Zero the listed adapters' gradients and moments; master takes the pool's weights."""
     p, n = _ids(ids)
-    _check(lib().lora_adamw_init(train.c, train.n, train.state, p, n, _ptr(err), _stream(stream)), "lora_adamw_init")
+    _check(lib().lora_adamw_init(train.c, train.n, train.state, p, n, _addr(err), _stream(stream)), "lora_adamw_init")
 
 
 def lora_grad_sumsq(train: TrainSet, ids: torch.Tensor, sumsq: torch.Tensor, workspace: torch.Tensor,
@@ -802,8 +808,8 @@ def lora_grad_sumsq(train: TrainSet, ids: torch.Tensor, sumsq: torch.Tensor, wor
     """sumsq[i] = (accumulate: +=) the sum of squares of adapter i's gradients, for the listed ids."""
     p, n = _ids(ids)
     _check(lib().lora_grad_sumsq(train.c, train.n, p, n, 1 if accumulate else 0,
-                                 _rows(sumsq, train.n_adapters, torch.float32, "sumsq"), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)),
+                                 _rows(sumsq, train.n_adapters, torch.float32, "sumsq"), _addr(workspace),
+                                 workspace.numel() * workspace.element_size(), _addr(err), _stream(stream)),
            "lora_grad_sumsq")
 
 
@@ -813,7 +819,7 @@ def lora_adamw_step(train: TrainSet, ids: torch.Tensor, hyper: torch.Tensor, sum
     p, n = _ids(ids)
     if hyper.numel() * hyper.element_size() != 32 * train.n_adapters or not hyper.is_contiguous():
         raise ValueError("hyper: expected %d settings of 32 bytes" % train.n_adapters)
-    _check(lib().lora_adamw_step(train.c, train.n, train.state, p, n, _ptr(hyper),
+    _check(lib().lora_adamw_step(train.c, train.n, train.state, p, n, _addr(hyper),
                                  _rows(sumsq, train.n_adapters, torch.float32, "sumsq"),
-                                 LORA_ADAMW_ZERO_GRAD if zero_grad else 0, _ptr(err), _stream(stream)),
+                                 LORA_ADAMW_ZERO_GRAD if zero_grad else 0, _addr(err), _stream(stream)),
            "lora_adamw_step")

@@ -71,14 +71,15 @@ size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 cudaError_t ensure_smem_attr(const void* func, size_t bytes) {
   // A few kernels, each raised once per device to its largest request.
-  static std::atomic<size_t> cache[8][kMaxDevices];
-  static std::atomic<const void*> funcs[8];
+  constexpr int kSlots = 24;
+  static std::atomic<size_t> cache[kSlots][kMaxDevices];
+  static std::atomic<const void*> funcs[kSlots];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   int slot = -1;
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < kSlots; ++i) {
     const void* f = funcs[i].load();
     if (f == func) { slot = i; break; }
     if (f == nullptr) {

@@ -342,7 +342,8 @@ def test_rows_past_32_bits():
     args = [dev(np.zeros(3)), dev(np.ones(3))]
     logp, loss = torch.empty(3, device="cuda"), torch.empty(3, device="cuda")
     d = torch.empty(3, V, dtype=torch.bfloat16, device="cuda")
-    c = x.contiguous()
+    c = torch.empty(3, 704, dtype=torch.bfloat16, device="cuda")[:, :V]  # rows aligned as those of x
+    c.copy_(x)
     B.lora_policy_loss(x, lab, *args, logp, loss, None, d)
     logp2, loss2, d2 = torch.empty_like(logp), torch.empty_like(loss), torch.empty_like(d)
     B.lora_policy_loss(c, lab, *args, logp2, loss2, None, d2)
@@ -371,3 +372,52 @@ def test_other_stream_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip((logp, loss, d), want))
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 500009), ("f32", 262147), ("bf16", 303110), ("f32", 151940)])
+def test_rows_longer_than_a_clusters_shared_memory(dtype, V):
+    """The longest rows that are staged in shared memory, and rows that are not."""
+    rng = np.random.default_rng(V)
+    flat, x, x64 = make_logits(rng, 2, V, V + 3, dtype, 1, masked=False)
+    lab = np.array([V - 1, 17], dtype=np.int32)
+    want, lse = R.logprobs(x64, lab)
+    logp, loss, d = torch.empty(2, device="cuda"), torch.empty(2, device="cuda"), torch.empty_like(x)
+    old = dev(want)
+    B.lora_policy_loss(x, dev(lab, np.int32), old, dev([1.0, -1.0]), logp, loss, None, d)
+    close(logp.cpu().numpy(), want, 2 * ATOL, "logp")  # twice as many terms a thread
+    coef = np.array([-1.0, 1.0])
+    bound = grad_bound(x64, lse, lab, coef, np.full(2, 3e-5), dtype)
+    close(d.double().cpu().numpy(), R.softmax_grad(x64, lab, lse, coef), bound, "gradient")
+    B.lora_policy_loss(x, dev(lab, np.int32), old, dev([1.0, -1.0]), logp, loss, None, x)
+    assert torch.equal(x, d)
+
+
+def test_timeout_leaves_the_outputs():
+    """With the timeout probe armed every row gives up after about a millisecond, sets its bit and writes
+    nothing; the next calls are right."""
+    x = torch.randn(6, 9000, device="cuda")
+    lab = torch.zeros(6, dtype=torch.int32, device="cuda")
+    f = torch.zeros(6, device="cuda")
+    logp, loss, pair = (torch.full((6,), GUARD, device="cuda") for _ in range(3))
+    d, ws, err = torch.full_like(x, GUARD), B.preference_workspace(6, 1), new_err()
+    indptr = dev([0, 3, 6], np.int32)
+
+    def calls():
+        B.lora_token_logprobs(x, lab, logp, err=err)
+        B.lora_policy_loss(x, lab, f, f, logp, loss, None, d, err=err)
+        B.lora_preference_loss(x, lab, indptr, pair[:1], None, d, ws, err=err)
+
+    try:
+        B.debug_wait_probe(2_000_000)
+        calls()
+        torch.cuda.synchronize()
+    finally:
+        B.debug_wait_probe(0)
+    assert int(err) == B.LORA_DERR_TIMEOUT
+    assert bool((logp == GUARD).all()) and bool((loss == GUARD).all()) and bool((d == GUARD).all())
+    assert float(pair[0]) == GUARD
+    err.zero_()
+    calls()
+    assert int(err) == 0
+    want = torch.log_softmax(x.double(), 1)[:, 0]
+    assert float((logp.double() - want).abs().max()) <= ATOL

@@ -40,8 +40,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float exp_of(float d) { return ex2(fmaf(d, kLog2e, d * kLog2eLo)); }
-
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pair_of(float a, float b) {
   uint64_t r;
@@ -140,6 +138,9 @@ struct Elem<float> {
 };
 
 // A running sum of exponentials: its maximum m, and s = sum of exp(x - base(m)).
+// Terms take the hardware's 2^x.  The few rescalings use expf: 2^x is 5e-8 low on
+// average, which a rescaling would put on the whole sum, and a loss adds logp over
+// hundreds of rows.
 struct Sum {
   float m, s;
 };
@@ -149,7 +150,7 @@ __device__ __forceinline__ Sum join(const Sum& x, const Sum& y) {
   Sum r;
   r.m = fmaxf(x.m, y.m);
   const float base = base_of(r.m);
-  r.s = x.s * exp_of(x.m - base) + y.s * exp_of(y.m - base);
+  r.s = x.s * expf(x.m - base) + y.s * expf(y.m - base);
   return r;
 }
 
@@ -212,7 +213,8 @@ __device__ __forceinline__ Sum add_vectors(Sum t, const uint4 (&r)[N]) {
   }
   float a, b;
   split(part, a, b);
-  return Sum{m, t.s * exp_of(t.m - base) + (a + b)};
+  if (m != t.m) t.s *= expf(t.m - base);
+  return Sum{m, t.s + (a + b)};
 }
 
 // One element x, joined to t.
@@ -251,7 +253,7 @@ __device__ __forceinline__ Sum warp_sum(Sum t) {
   float m = t.m;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  float s = t.s * exp_of(t.m - base_of(m));
+  float s = t.s * expf(t.m - base_of(m));
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
   return Sum{m, s};
@@ -496,13 +498,14 @@ __global__ void __launch_bounds__(kThreads) row_sum_kernel(const __grid_constant
   if (lead) put_sum(a, t, x, r);
 }
 
-// The gradient rows from the rows' sums and coefficients.
+// The gradient rows from the rows' sums and coefficients, last rows first: those
+// that the sums read last are still in L2.
 template <typename E>
 __global__ void __launch_bounds__(kThreads) row_grad_kernel(const __grid_constant__ RowArgs a) {
   const int n = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
   pdl_wait_then_release();
   if (a.probe > 0) return;  // the sums of this call reported it
-  const int t = (int)cluster_id_x();
+  const int t = a.T - 1 - (int)cluster_id_x();
   const Cut<E> c = cut_row(static_cast<const E*>(a.logits) + (long long)t * a.ld, a.V, rank, n);
   const Grad g = pair_grad(a, t, row_label(a, t, false));
   write_grad<E, kThreads>(c, static_cast<E*>(a.dlogits) + (long long)t * a.ldd, a.V, g);

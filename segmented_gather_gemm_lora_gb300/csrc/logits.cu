@@ -192,14 +192,11 @@ struct RowShared {
   Sum part[kMaxCluster * kWarps];
 };
 
-// The sum of the elements of some vectors, joined to t (a sum of its own first:
-// the running sum takes one addition).
+// The sum of exp(x - base) over some vectors.
 template <typename E, int N>
-__device__ __forceinline__ Sum add_vectors(Sum t, const uint4 (&r)[N]) {
+__device__ __forceinline__ float exp_sum(const uint4 (&r)[N], float base) {
   constexpr int kPairs = Elem<E>::kPairs;
-  const uint64_t hi = pair_of(kLog2e, kLog2e), lo = pair_of(kLog2eLo, kLog2eLo);
-  const float m = fmaxf(t.m, Elem<E>::top(r)), base = base_of(m);
-  const uint64_t nb = pair_of(-base, -base);
+  const uint64_t hi = pair_of(kLog2e, kLog2e), lo = pair_of(kLog2eLo, kLog2eLo), nb = pair_of(-base, -base);
   uint64_t part = pair_of(0.f, 0.f);
 #pragma unroll
   for (int u = 0; u < N; ++u) {
@@ -213,8 +210,16 @@ __device__ __forceinline__ Sum add_vectors(Sum t, const uint4 (&r)[N]) {
   }
   float a, b;
   split(part, a, b);
+  return a + b;
+}
+
+// Some vectors joined to t (their sum first: the running sum takes one addition).
+template <typename E, int N>
+__device__ __forceinline__ Sum add_vectors(Sum t, const uint4 (&r)[N]) {
+  const float m = fmaxf(t.m, Elem<E>::top(r)), base = base_of(m);
+  const float s = exp_sum<E>(r, base);
   if (m != t.m) t.s *= expf(t.m - base);
-  return Sum{m, t.s + (a + b)};
+  return Sum{m, t.s + s};
 }
 
 // One element x, joined to t.
@@ -249,14 +254,19 @@ __device__ __forceinline__ void cluster_started(int n) {
 }
 
 // The sum of the lanes' sums: the maximum first, then one rescaling a lane.
-__device__ __forceinline__ Sum warp_sum(Sum t) {
-  float m = t.m;
+__device__ __forceinline__ float warp_max(float m) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  float s = t.s * expf(t.m - base_of(m));
+  return m;
+}
+__device__ __forceinline__ float warp_add(float s) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  return Sum{m, s};
+  return s;
+}
+__device__ __forceinline__ Sum warp_sum(const Sum& t) {
+  const float m = warp_max(t.m);
+  return Sum{m, warp_add(t.s * expf(t.m - base_of(m)))};
 }
 
 // The row's sum over the cluster (which has arrived by cluster_started): each
@@ -697,14 +707,24 @@ __global__ void __launch_bounds__(held_threads(kG), (kVec > 8 ? 512 : 768) / hel
     }
     Sum s{-INF_F, 0.f};
     if (kKind != kRowGrad) {
+      // the warp's maximum first: its sums need no rescaling
+      float m = e >= 0 ? fmaxf(xe, -INF_F) : -INF_F;
 #pragma unroll
       for (int u = 0; u < kVec; u += 4)
         if (u * kG < nv) {
           const uint4 four[4] = {r[u], r[u + 1], r[u + 2], r[u + 3]};
-          s = add_vectors<E>(s, four);
+          m = fmaxf(m, Elem<E>::top(four));
         }
-      if (e >= 0) s = add_one(s, xe);
-      s = warp_sum(s);
+      m = warp_max(m);
+      const float base = base_of(m);
+      float add = e >= 0 ? ex2(fmaf(xe - base, kLog2e, (xe - base) * kLog2eLo)) : 0.f;
+#pragma unroll
+      for (int u = 0; u < kVec; u += 4)
+        if (u * kG < nv) {
+          const uint4 four[4] = {r[u], r[u + 1], r[u + 2], r[u + 3]};
+          add += exp_sum<E>(four, base);
+        }
+      s = Sum{m, warp_add(add)};
       if (kG > 32 && !dead) {
         const uint32_t bar = smem_u32(&sh.sums[buf]);
         if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * kW * sizeof(float4)));

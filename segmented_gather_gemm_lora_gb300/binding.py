@@ -9,6 +9,7 @@ no fallback: if the library cannot be built or loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import numpy as np
@@ -658,6 +659,12 @@ def _rows(t: Optional[torch.Tensor], n: int, dtype, what: str) -> int:
     return t.data_ptr()
 
 
+@functools.lru_cache(maxsize=64)
+def _opts(kind, *values):
+    """A structure of options by reference: a training run passes the same few again and again."""
+    return ctypes.byref(kind(*values))
+
+
 def _addr(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -696,12 +703,12 @@ def lora_preference_loss(logits: torch.Tensor, labels: torch.Tensor, seq_indptr:
     p, ld, code, T, V = _logits(logits)
     n = int(loss.numel())
     f32 = torch.float32
-    opts = lora_pref_opts_t(kind, LORA_PREF_AVERAGE if average else 0, beta, label_smoothing, margin, grad_scale)
+    opts = _opts(lora_pref_opts_t, kind, LORA_PREF_AVERAGE if average else 0, beta, label_smoothing, margin, grad_scale)
     dp, ldd = _grad_of(logits, dlogits)
     _check(lib().lora_preference_loss(p, ld, code, _rows(labels, T, torch.int32, "labels"),
                                       _rows(ref_logp, T, f32, "ref_logp"),
                                       _rows(seq_indptr, 2 * n + 1, torch.int32, "seq_indptr"), n, T, V,
-                                      ctypes.byref(opts), _rows(loss, n, f32, "loss"),
+                                      opts, _rows(loss, n, f32, "loss"),
                                       _rows(seq_logp, 2 * n, f32, "seq_logp"), dp, ldd, _addr(workspace),
                                       workspace.numel() * workspace.element_size(), _addr(err), _stream(stream)),
            "lora_preference_loss")
@@ -716,12 +723,12 @@ def lora_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch
     dlogits may be the logits (the gradient takes their place) or None."""
     p, ld, code, T, V = _logits(logits)
     f32 = torch.float32
-    opts = lora_policy_opts_t(clip_low, clip_high, kl_coef, grad_scale)
+    opts = _opts(lora_policy_opts_t, clip_low, clip_high, kl_coef, grad_scale)
     dp, ldd = _grad_of(logits, dlogits)
     _check(lib().lora_policy_loss(p, ld, code, _rows(labels, T, torch.int32, "labels"),
                                   _rows(old_logp, T, f32, "old_logp"), _rows(ref_logp, T, f32, "ref_logp"),
                                   _rows(advantage, T, f32, "advantage"), _rows(weight, T, f32, "weight"), T, V,
-                                  ctypes.byref(opts), _rows(logp, T, f32, "logp"), _rows(loss, T, f32, "loss"),
+                                  opts, _rows(logp, T, f32, "logp"), _rows(loss, T, f32, "loss"),
                                   _rows(kl, T, f32, "kl"), dp, ldd, _addr(err), _stream(stream)), "lora_policy_loss")
 
 

@@ -21,6 +21,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "lora_train.h"
+#include "pairs.cuh"
 
 namespace lora {
 
@@ -40,31 +41,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pair_of(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void split(uint64_t p, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // One element and a 16-byte vector of a row's type.
 template <typename E>
 struct Elem;
@@ -775,24 +751,6 @@ struct PairArgs {
   int32_t* err;
   int probed;  // the timeout probe is armed: the rows have no sums
 };
-
-// An fp32 sum with what its rounding left out (hi + lo, |lo| within half a unit of
-// hi): sums of hundreds of terms as exact as in doubles, which the GPU adds two a
-// clock an SM.
-struct Pair32 {
-  float hi, lo;
-};
-__device__ __forceinline__ Pair32 two_sum(float a, float b) {
-  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
-  return Pair32{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
-}
-__device__ __forceinline__ Pair32 add_pair(const Pair32& x, const Pair32& y) {
-  const Pair32 h = two_sum(x.hi, y.hi);
-  // an infinite or NaN sum has nothing left out
-  const float lo = fabsf(h.hi) < INF_F ? h.lo + (x.lo + y.lo) : 0.f;
-  const float s = __fadd_rn(h.hi, lo);
-  return Pair32{s, fabsf(s) < INF_F ? __fsub_rn(lo, __fsub_rn(s, h.hi)) : 0.f};
-}
 
 // What a pair takes from one sequence's rows.
 struct PairSums {

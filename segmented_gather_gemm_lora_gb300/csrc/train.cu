@@ -11,12 +11,13 @@
 #include "common.cuh"
 #include "internal.h"
 #include "lora_train.h"
+#include "pairs.cuh"
 
 namespace lora {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kGroup = 8;                     // consecutive elements a thread takes: one page each (d % 8 == 0, pages >= 64)
 constexpr int kSpan = kThreads * kGroup;      // elements the CTA takes at once
 constexpr int kSumGroups = 4;                 // spans of a chunk of the sum
@@ -56,21 +57,21 @@ static_assert(sizeof(TrainArgs) <= 4096, "kernel parameters");
 struct Place {
   int ad;
   int g;
-  long long e0, size;  // first element; elements of the matrix
+  long long e0, size;  // first element; elements of the matrix (0: of no good adapter)
   long long slot0;     // page-list slot of the matrix
   bool lead;           // the CTA that reports the adapter's errors
-  bool live;           // the chunk holds elements of a good adapter
+  int bad;
+  int twice;           // this thread saw the id earlier in the list
 };
 
-// Resolve blockIdx into a Place; the whole CTA gets the same answer.
+// Resolve blockIdx into a Place.  The threads still have to agree on `twice` (an
+// id listed before is passed over: its elements have one writer), so that loads
+// can be under way by then.
 __device__ __forceinline__ Place find_place(const TrainArgs& a) {
   Place q;
   const int chunk = a.spans * kSpan;
   const int e = blockIdx.y, c = blockIdx.x;
   q.ad = a.ids[e];
-  // an id listed before is passed over: its elements have one writer
-  int twice = 0;
-  for (int k = threadIdx.x; k < e; k += blockDim.x) twice |= a.ids[k] == q.ad;
   q.g = 0;
   while (q.g + 1 < a.n_proj && c >= a.p[q.g + 1].chunk0) ++q.g;
   const DevProj& p = a.p[q.g];
@@ -79,15 +80,19 @@ __device__ __forceinline__ Place find_place(const TrainArgs& a) {
   const bool is_b = cg >= p.chunks_a;
   q.e0 = (long long)(is_b ? cg - p.chunks_a : cg) * chunk;
   const lora_adapter_desc_t d = adapter_desc(p.v, q.ad);
-  q.size = (long long)d.rank * (is_b ? p.v.d_out : p.v.d_in);
+  q.twice = 0;
+  for (int k = threadIdx.x; k < e; k += blockDim.x) q.twice |= a.ids[k] == q.ad;
   q.slot0 = is_b ? d.b_page0 : d.a_page0;
-  int bad = 0;
-  if (q.ad < 0 || q.ad >= p.v.n_adapters) bad = LORA_DERR_BAD_ADAPTER;
-  else if (d.rank < 1 || d.rank > p.v.max_rank) bad = LORA_DERR_BAD_RANK;
-  if (__syncthreads_or(twice)) bad = LORA_DERR_BAD_ADAPTER;
-  if (bad && q.lead && threadIdx.x == 0) report(a.err, bad);
-  q.live = !bad && q.e0 < q.size;
+  q.bad = q.ad < 0 || q.ad >= p.v.n_adapters ? LORA_DERR_BAD_ADAPTER : d.rank < 1 || d.rank > p.v.max_rank ? LORA_DERR_BAD_RANK : 0;
+  q.size = q.bad ? 0 : (long long)d.rank * (is_b ? p.v.d_out : p.v.d_in);
   return q;
+}
+
+// Whether the chunk holds elements of a good adapter, the same in every thread.
+__device__ __forceinline__ bool agree(const TrainArgs& a, Place& q) {
+  if (__syncthreads_or(q.twice)) q.bad = LORA_DERR_BAD_ADAPTER;
+  if (q.bad && q.lead && threadIdx.x == 0) report(a.err, q.bad);
+  return !q.bad && q.e0 < q.size;
 }
 
 // Pool position of element e of the place's matrix, or -1 off the pool.
@@ -99,59 +104,88 @@ __device__ __forceinline__ long long pool_pos(const DevView& v, const Place& q, 
   return (page << v.page_shift) + (e & ((1LL << v.page_shift) - 1));
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+// Eight elements as four pairs.
+struct Eight {
+  uint64_t p[4];
+};
+__device__ __forceinline__ Eight from_f32(const float4& a, const float4& b) {
+  return Eight{{pair_of(a.x, a.y), pair_of(a.z, a.w), pair_of(b.x, b.y), pair_of(b.z, b.w)}};
 }
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+__device__ __forceinline__ Eight from_bf16(const uint4& v) {
+  return Eight{{pair_of(bf_lo(v.x), bf_hi(v.x)), pair_of(bf_lo(v.y), bf_hi(v.y)), pair_of(bf_lo(v.z), bf_hi(v.z)),
+                pair_of(bf_lo(v.w), bf_hi(v.w))}};
+}
+__device__ __forceinline__ void store8(float* p, const Eight& x) {
+  float f[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) split(x.p[k], f[2 * k], f[2 * k + 1]);
   reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
+__device__ __forceinline__ uint4 to_bf16(const Eight& x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float a, b;
+    split(x.p[k], a, b);
+    w[k] = pack_bf16x2(a, b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 // Eight e4m3 codes as fp32, and back (to nearest, ties to even, saturating).
-__device__ __forceinline__ void decode8(uint2 c, float (&f)[8]) {
+__device__ __forceinline__ Eight from_e4m3(const uint2& c) {
+  Eight x;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint16_t two = (uint16_t)((k < 2 ? c.x : c.y) >> (16 * (k & 1)));
     uint32_t h;
+    float a, b;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
-    asm("{\n\t.reg .f16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
-        : "=f"(f[2 * k]), "=f"(f[2 * k + 1])
-        : "r"(h));
+    asm("{\n\t.reg .f16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}" : "=f"(a), "=f"(b) : "r"(h));
+    x.p[k] = pair_of(a, b);
   }
+  return x;
 }
-__device__ __forceinline__ uint2 encode8(const float (&f)[8]) {
+__device__ __forceinline__ uint2 to_e4m3(const Eight& x) {
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
+    float a, b;
     uint16_t two;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(f[2 * k + 1]), "f"(f[2 * k]));
+    split(x.p[k], a, b);
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(b), "f"(a));
     w[k >> 1] |= (uint32_t)two << (16 * (k & 1));
   }
   return make_uint2(w[0], w[1]);
 }
 
 // The scale of a block of 64 whose elements the eight lanes around this one hold.
-__device__ __forceinline__ uint16_t block_scale(const float (&x)[8]) {
+__device__ __forceinline__ uint16_t block_scale(const Eight& x) {
   float top = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
+  for (int k = 0; k < 4; ++k) {
+    float a, b;
+    split(x.p[k], a, b);
+    top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
+  }
 #pragma unroll
   for (int s = 1; s < kBlockLanes; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  return __bfloat16_as_ushort(__float2bfloat16_rn(top < kTiny ? 0.f : top / 448.f));
+  return __bfloat16_as_ushort(__float2bfloat16_rn(top < kTiny ? 0.f : top * (1.f / 448.f)));
 }
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 
-__device__ __forceinline__ float sqrt_fast(float x) {  // 2^-23 relative
+template <bool kFlush>  // 2^-23 relative; kFlush: denormal arguments count as zero (fewer instructions)
+__device__ __forceinline__ float sqrt_fast(float x) {
   float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  if (kFlush) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  else asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float rcp_fast(float x) {  // one unit
   float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // of normal values: a root is 0 or above 2^-75
   return y;
 }
 
@@ -161,21 +195,59 @@ struct StepShared {
   int skip;
 };
 
+// What a thread reads of its eight elements.
+template <bool kE4M3>
+struct Raw {
+  float4 g[2], m[kE4M3 ? 1 : 2], r[kE4M3 ? 1 : 2];  // e4m3: the codes in m[0].x, .y (r alike)
+  uint4 w[2];                                        // bf16 in w[0], or fp32
+  uint32_t scales;
+};
+template <bool kE4M3>
+__device__ __forceinline__ Raw<kE4M3> read_raw(const DevProj& p, long long pos) {
+  Raw<kE4M3> x;
+  x.g[0] = reinterpret_cast<const float4*>(p.grad + pos)[0];
+  x.g[1] = reinterpret_cast<const float4*>(p.grad + pos)[1];
+  if (kE4M3) {
+    const float2 m = *reinterpret_cast<const float2*>(static_cast<const uint8_t*>(p.m) + pos);
+    const float2 r = *reinterpret_cast<const float2*>(static_cast<const uint8_t*>(p.r) + pos);
+    x.m[0] = make_float4(m.x, m.y, 0.f, 0.f);
+    x.r[0] = make_float4(r.x, r.y, 0.f, 0.f);
+    x.scales = p.m_scale[pos / LORA_ADAMW_BLOCK] | (uint32_t)p.r_scale[pos / LORA_ADAMW_BLOCK] << 16;
+  } else {
+#pragma unroll
+    for (int k = 0; k < (kE4M3 ? 1 : 2); ++k) {
+      x.m[k] = reinterpret_cast<const float4*>(static_cast<const float*>(p.m) + pos)[k];
+      x.r[k] = reinterpret_cast<const float4*>(static_cast<const float*>(p.r) + pos)[k];
+    }
+  }
+  if (p.master != nullptr) {
+    x.w[0] = reinterpret_cast<const uint4*>(p.master + pos)[0];
+    x.w[1] = reinterpret_cast<const uint4*>(p.master + pos)[1];
+  } else {
+    x.w[0] = *reinterpret_cast<const uint4*>(p.v.pool + pos);
+  }
+  return x;
+}
+
 // AdamW.  Bound by memory: per element 24 bytes (fp32 moments), 30 (and fp32
 // weights), 12 (8-bit moments), 4 more to clear the gradient; one pass, each
 // byte moved once.  A thread's eight elements lie on one page, a block's 64 in
 // eight neighbouring lanes, so a block's scale takes three shuffles.  Roots and
 // quotients are the hardware's approximations (2^-22 of an update, which is
-// itself a small part of a weight): with 8-bit moments the IEEE forms' extra
-// instructions, not memory, set the time.
+// itself a small part of a weight) and products work on pairs: with 8-bit moments
+// the IEEE forms' extra instructions, not memory, set the time.
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ TrainArgs a) {
   __shared__ StepShared sh;
   pdl_wait_then_release();
-  const Place q = find_place(a);
-  if (!q.live) return;
+  Place q = find_place(a);
   const DevProj& p = a.p[q.g];
-  if (threadIdx.x == 0) {
+  // the pool position of this thread's eight elements of span j, -1 for none
+  auto place = [&](int j) -> long long {
+    const long long e = q.e0 + (long long)(j * kThreads + threadIdx.x) * kGroup;
+    return j < a.spans && e < q.size ? pool_pos(p.v, q, e) : -2;
+  };
+  if (threadIdx.x == 0 && q.size > 0) {
     const lora_adamw_hyper_t h = a.hyper[q.ad];
     float gs = h.grad_scale;
     sh.skip = h.step < 1;
@@ -201,85 +273,77 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     sh.eps = h.eps;
     sh.decay = 1.f - h.lr * h.weight_decay;
   }
-  __syncthreads();
-  if (sh.skip) return;
-  const float gs = sh.gs, b1 = sh.b1, n1 = sh.n1, b2 = sh.b2, n2 = sh.n2;
-  const float size = sh.size, iroot = sh.iroot, eps = sh.eps, decay = sh.decay;
+  if (!agree(a, q) || sh.skip) return;
+  const uint64_t gs = pair_of(sh.gs, sh.gs), b1 = pair_of(sh.b1, sh.b1), n1 = pair_of(sh.n1, sh.n1);
+  const uint64_t b2 = pair_of(sh.b2, sh.b2), n2 = pair_of(sh.n2, sh.n2), down = pair_of(-sh.size, -sh.size);
+  const uint64_t iroot = pair_of(sh.iroot, sh.iroot), eps = pair_of(sh.eps, sh.eps), decay = pair_of(sh.decay, sh.decay);
   uint16_t* const pool = const_cast<uint16_t*>(p.v.pool);
-  for (int j = 0; j < a.spans; ++j) {
-    if (q.e0 + (long long)j * kSpan >= q.size) break;
-    const long long e = q.e0 + (long long)(j * kThreads + threadIdx.x) * kGroup;
-    long long pos = -1;
-    if (e < q.size) {
-      pos = pool_pos(p.v, q, e);
-      if (pos < 0) report(a.err, LORA_DERR_BAD_PAGE);
-    }
-    const bool on = pos >= 0;
-    float m[8] = {}, r[8] = {};
-    if (on) {
-      float g[8], w[8];
-      load8(p.grad + pos, g);
+  for (int j = 0; j < a.spans && q.e0 + (long long)j * kSpan < q.size; ++j) {
+    const long long pos = place(j);
+    Raw<kE4M3> x{};
+    if (pos >= 0) x = read_raw<kE4M3>(p, pos);
+    if (pos == -1) report(a.err, LORA_DERR_BAD_PAGE);
+    Eight m{}, r{};
+    if (pos >= 0) {
+      const Eight g = from_f32(x.g[0], x.g[1]);
+      Eight w = p.master != nullptr ? from_f32(*reinterpret_cast<const float4*>(&x.w[0]), *reinterpret_cast<const float4*>(&x.w[1]))
+                                    : from_bf16(x.w[0]);
       if (kE4M3) {
-        const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.m) + pos);
-        const uint2 cr = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.r) + pos);
-        const float sm = bf16_value(p.m_scale[pos / LORA_ADAMW_BLOCK]), sr = bf16_value(p.r_scale[pos / LORA_ADAMW_BLOCK]);
-        decode8(cm, m);
-        decode8(cr, r);
+        m = from_e4m3(make_uint2(__float_as_uint(x.m[0].x), __float_as_uint(x.m[0].y)));
+        r = from_e4m3(make_uint2(__float_as_uint(x.r[0].x), __float_as_uint(x.r[0].y)));
+        const float sm = bf16_value((uint16_t)x.scales), sr = bf16_value((uint16_t)(x.scales >> 16));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          m[k] *= sm;
-          r[k] *= sr;
-          r[k] *= r[k];
+        for (int k = 0; k < 4; ++k) {
+          m.p[k] = mul2(m.p[k], pair_of(sm, sm));
+          r.p[k] = mul2(r.p[k], pair_of(sr, sr));
+          r.p[k] = mul2(r.p[k], r.p[k]);
         }
       } else {
-        load8(static_cast<const float*>(p.m) + pos, m);
-        load8(static_cast<const float*>(p.r) + pos, r);
+        m = from_f32(x.m[0], x.m[kE4M3 ? 0 : 1]);
+        r = from_f32(x.r[0], x.r[kE4M3 ? 0 : 1]);
       }
-      if (p.master != nullptr) load8(p.master + pos, w);
-      else unpack8(*reinterpret_cast<const uint4*>(pool + pos), w);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        g[k] *= gs;
-        m[k] = b1 * m[k] + n1 * g[k];
-        r[k] = b2 * r[k] + n2 * (g[k] * g[k]);
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t gk = mul2(g.p[k], gs);
+        m.p[k] = fma2(b1, m.p[k], mul2(n1, gk));
+        r.p[k] = fma2(b2, r.p[k], mul2(n2, mul2(gk, gk)));
       }
       if (!kE4M3) {
         store8(static_cast<float*>(p.m) + pos, m);
         store8(static_cast<float*>(p.r) + pos, r);
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        r[k] = sqrt_fast(r[k]);
-        w[k] = fmaf(w[k], decay, -size * (m[k] * rcp_fast(fmaf(r[k], iroot, eps))));
+      for (int k = 0; k < 4; ++k) {
+        float u, v;
+        split(r.p[k], u, v);
+        r.p[k] = pair_of(sqrt_fast<kE4M3>(u), sqrt_fast<kE4M3>(v));
+        split(fma2(r.p[k], iroot, eps), u, v);
+        w.p[k] = fma2(w.p[k], decay, mul2(down, mul2(m.p[k], pair_of(rcp_fast(u), rcp_fast(v)))));
       }
       if (p.master != nullptr) store8(p.master + pos, w);
-      uint4 b;
-      b.x = pack_bf16x2(w[0], w[1]);
-      b.y = pack_bf16x2(w[2], w[3]);
-      b.z = pack_bf16x2(w[4], w[5]);
-      b.w = pack_bf16x2(w[6], w[7]);
-      *reinterpret_cast<uint4*>(pool + pos) = b;
-      if (a.zero_grad) {
-        const float zero[8] = {};
-        store8(p.grad + pos, zero);
-      }
+      *reinterpret_cast<uint4*>(pool + pos) = to_bf16(w);
+      if (a.zero_grad) store8(p.grad + pos, Eight{});
     }
     if (kE4M3) {  // lanes without elements hold zeros, which no scale sees
       const uint16_t bm = block_scale(m), br = block_scale(r);
-      if (!on) continue;
-      const float sm = bf16_value(bm), sr = bf16_value(br);
-      const float im = sm > 0.f ? rcp_fast(sm) : 0.f, ir = sr > 0.f ? rcp_fast(sr) : 0.f;
+      if (pos >= 0) {
+        const float sm = bf16_value(bm), sr = bf16_value(br);
+        const float im = sm > 0.f ? rcp_fast(sm) : 0.f, ir = sr > 0.f ? rcp_fast(sr) : 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        m[k] *= im;
-        r[k] *= ir;
-        if (r[k] > 0.f) r[k] = fmaxf(r[k], 0.001953125f);  // 2^-9, the smallest code
-      }
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m) + pos) = encode8(m);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.r) + pos) = encode8(r);
-      if (threadIdx.x % kBlockLanes == 0) {
-        p.m_scale[pos / LORA_ADAMW_BLOCK] = bm;
-        p.r_scale[pos / LORA_ADAMW_BLOCK] = br;
+        for (int k = 0; k < 4; ++k) {
+          float u, v;
+          m.p[k] = mul2(m.p[k], pair_of(im, im));
+          split(mul2(r.p[k], pair_of(ir, ir)), u, v);
+          if (u > 0.f) u = fmaxf(u, 0.001953125f);  // 2^-9, the smallest code
+          if (v > 0.f) v = fmaxf(v, 0.001953125f);
+          r.p[k] = pair_of(u, v);
+        }
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m) + pos) = to_e4m3(m);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.r) + pos) = to_e4m3(r);
+        if (threadIdx.x % kBlockLanes == 0) {
+          p.m_scale[pos / LORA_ADAMW_BLOCK] = bm;
+          p.r_scale[pos / LORA_ADAMW_BLOCK] = br;
+        }
       }
     }
   }
@@ -288,8 +352,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads) adamw_init_kernel(const __grid_constant__ TrainArgs a) {
   pdl_wait_then_release();
-  const Place q = find_place(a);
-  if (!q.live) return;
+  Place q = find_place(a);
+  if (!agree(a, q)) return;
   const DevProj& p = a.p[q.g];
   for (int j = 0; j < a.spans; ++j) {
     const long long e = q.e0 + (long long)(j * kThreads + threadIdx.x) * kGroup;
@@ -299,7 +363,7 @@ __global__ void __launch_bounds__(kThreads) adamw_init_kernel(const __grid_const
       report(a.err, LORA_DERR_BAD_PAGE);
       continue;
     }
-    const float zero[8] = {};
+    const Eight zero{};
     store8(p.grad + pos, zero);
     if (kE4M3) {
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.m) + pos) = make_uint2(0, 0);
@@ -313,20 +377,17 @@ __global__ void __launch_bounds__(kThreads) adamw_init_kernel(const __grid_const
       store8(static_cast<float*>(p.r) + pos, zero);
     }
     if (p.master != nullptr) {
-      float w[8];
-      unpack8(*reinterpret_cast<const uint4*>(p.v.pool + pos), w);
-      store8(p.master + pos, w);
+      store8(p.master + pos, from_bf16(*reinterpret_cast<const uint4*>(p.v.pool + pos)));
     }
   }
 }
 
-template <typename T>
-__device__ __forceinline__ T block_sum(T x, T* sh) {
+__device__ __forceinline__ float block_sum(float x, float* sh) {
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
   __syncthreads();
-  T t = 0;
+  float t = 0.f;
 #pragma unroll
   for (int k = 0; k < kThreads / 32; ++k) t += sh[k];
   return t;
@@ -337,9 +398,9 @@ __device__ __forceinline__ T block_sum(T x, T* sh) {
 __global__ void __launch_bounds__(kThreads) sumsq_kernel(const __grid_constant__ TrainArgs a) {
   __shared__ float sh[kThreads / 32];
   pdl_wait_then_release();
-  const Place q = find_place(a);
+  Place q = find_place(a);
   float s = 0.f;
-  if (q.live) {
+  if (agree(a, q)) {
     const DevProj& p = a.p[q.g];
     long long pos[kSumGroups];  // all first, then all loads: a thread has its 128 bytes in flight
 #pragma unroll
@@ -347,16 +408,23 @@ __global__ void __launch_bounds__(kThreads) sumsq_kernel(const __grid_constant__
       const long long e = q.e0 + (long long)(j * kThreads + threadIdx.x) * kGroup;
       pos[j] = e < q.size ? pool_pos(p.v, q, e) : -2;
     }
-    float g[kSumGroups][8] = {};
+    Eight g[kSumGroups] = {};
 #pragma unroll
     for (int j = 0; j < kSumGroups; ++j)
-      if (pos[j] >= 0) load8(p.grad + pos[j], g[j]);
+      if (pos[j] >= 0) {
+        const float4* at = reinterpret_cast<const float4*>(p.grad + pos[j]);
+        g[j] = from_f32(at[0], at[1]);
+      }
+    uint64_t two = pair_of(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < kSumGroups; ++j) {
       if (pos[j] == -1) report(a.err, LORA_DERR_BAD_PAGE);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s += g[j][k] * g[j][k];
+      for (int k = 0; k < 4; ++k) two = fma2(g[j].p[k], g[j].p[k], two);
     }
+    float u, v;
+    split(two, u, v);
+    s = u + v;
   }
   const float t = block_sum(s, sh);
   if (threadIdx.x == 0) a.partial[(long long)blockIdx.y * a.partial_stride + a.partial0 + blockIdx.x] = t;
@@ -371,19 +439,26 @@ struct FinishArgs {
   float* sumsq;
 };
 
-// One CTA an adapter: its chunks' sums, in double, in chunk order by thread.
+// One CTA an adapter: its chunks' sums, kept with what their rounding leaves out,
+// in a fixed order.
 __global__ void __launch_bounds__(kThreads) sumsq_finish_kernel(const __grid_constant__ FinishArgs a) {
-  __shared__ double sh[kThreads / 32];
+  __shared__ Pair32 sh[kThreads / 32];
   pdl_wait_then_release();
   const int e = blockIdx.x;
   const int ad = a.ids[e];
+  Pair32 s{0.f, 0.f};
+  for (int k = threadIdx.x; k < a.stride; k += kThreads) s = add_pair(s, Pair32{a.partial[(long long)e * a.stride + k], 0.f});
   int twice = 0;
   for (int k = threadIdx.x; k < e; k += kThreads) twice |= a.ids[k] == ad;
-  if (__syncthreads_or(twice) || ad < 0 || ad >= a.n_adapters) return;
-  double s = 0;
-  for (int k = threadIdx.x; k < a.stride; k += kThreads) s += a.partial[(long long)e * a.stride + k];
-  s = block_sum(s, sh);
-  if (threadIdx.x == 0) a.sumsq[ad] = (float)(a.accumulate ? s + a.sumsq[ad] : s);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+    s = add_pair(s, Pair32{__shfl_xor_sync(0xffffffffu, s.hi, d), __shfl_xor_sync(0xffffffffu, s.lo, d)});
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+  if (__syncthreads_or(twice) || ad < 0 || ad >= a.n_adapters || threadIdx.x != 0) return;
+  s = sh[0];
+  for (int k = 1; k < kThreads / 32; ++k) s = add_pair(s, sh[k]);
+  if (a.accumulate) s = add_pair(s, Pair32{a.sumsq[ad], 0.f});
+  a.sumsq[ad] = s.hi;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -7,6 +7,7 @@
 // rank end at once.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -20,8 +21,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kGroup = 8;                     // consecutive elements a thread takes: one page each (d % 8 == 0, pages >= 64)
 constexpr int kSpan = kThreads * kGroup;      // elements the CTA takes at once
-constexpr int kSumGroups = 4;                 // spans of a chunk of the sum
-constexpr int kSumChunk = kSpan * kSumGroups;
+constexpr int kSumGroups = 4;                 // spans of the sum that are read together
 constexpr int kMaxProj = 16;                  // projections of one launch (kernel parameters below 4 KB)
 constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
 constexpr int kBlockLanes = LORA_ADAMW_BLOCK / kGroup;  // lanes that share a block's scale
@@ -195,39 +195,69 @@ struct StepShared {
   int skip;
 };
 
-// What a thread reads of its eight elements.
-template <bool kE4M3>
-struct Raw {
-  float4 g[2], m[kE4M3 ? 1 : 2], r[kE4M3 ? 1 : 2];  // e4m3: the codes in m[0].x, .y (r alike)
-  uint4 w[2];                                        // bf16 in w[0], or fp32
-  uint32_t scales;
+// Asynchronous copies into a thread's own places in shared memory.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(kBytes) : "memory");
+}
+
+// What a thread works on: eight elements of a span.
+struct Work {
+  Eight g, w, m, r;  // r: the second moments
 };
-template <bool kE4M3>
-__device__ __forceinline__ Raw<kE4M3> read_raw(const DevProj& p, long long pos) {
-  Raw<kE4M3> x;
-  x.g[0] = reinterpret_cast<const float4*>(p.grad + pos)[0];
-  x.g[1] = reinterpret_cast<const float4*>(p.grad + pos)[1];
-  if (kE4M3) {
-    const float2 m = *reinterpret_cast<const float2*>(static_cast<const uint8_t*>(p.m) + pos);
-    const float2 r = *reinterpret_cast<const float2*>(static_cast<const uint8_t*>(p.r) + pos);
-    x.m[0] = make_float4(m.x, m.y, 0.f, 0.f);
-    x.r[0] = make_float4(r.x, r.y, 0.f, 0.f);
-    x.scales = p.m_scale[pos / LORA_ADAMW_BLOCK] | (uint32_t)p.r_scale[pos / LORA_ADAMW_BLOCK] << 16;
-  } else {
+
+// fp32 moments, read when they are worked on.
+__device__ __forceinline__ Eight read_f32(const float* at) {
+  return from_f32(reinterpret_cast<const float4*>(at)[0], reinterpret_cast<const float4*>(at)[1]);
+}
+__device__ __forceinline__ Work read_work(const DevProj& p, long long pos) {
+  Work x;
+  x.g = read_f32(p.grad + pos);
+  x.m = read_f32(static_cast<const float*>(p.m) + pos);
+  x.r = read_f32(static_cast<const float*>(p.r) + pos);
+  x.w = p.master != nullptr ? read_f32(p.master + pos) : from_bf16(*reinterpret_cast<const uint4*>(p.v.pool + pos));
+  return x;
+}
+
+// 8-bit moments: a CTA's threads read a span ahead into shared memory, each into
+// its own places.
+struct Stage {
+  float4 g[2][kThreads], w[2][kThreads];  // w: bf16 in w[0], or fp32
+  float4 codes[kThreads];                 // of m, then of the roots
+};
+__device__ __forceinline__ void read_ahead(Stage& st, const DevProj& p, long long pos) {
+  const int t = threadIdx.x;
 #pragma unroll
-    for (int k = 0; k < (kE4M3 ? 1 : 2); ++k) {
-      x.m[k] = reinterpret_cast<const float4*>(static_cast<const float*>(p.m) + pos)[k];
-      x.r[k] = reinterpret_cast<const float4*>(static_cast<const float*>(p.r) + pos)[k];
-    }
-  }
+  for (int k = 0; k < 2; ++k) copy_async<16>(&st.g[k][t], p.grad + pos + 4 * k);
+  copy_async<8>(&st.codes[t].x, static_cast<const uint8_t*>(p.m) + pos);
+  copy_async<8>(&st.codes[t].z, static_cast<const uint8_t*>(p.r) + pos);
   if (p.master != nullptr) {
-    x.w[0] = reinterpret_cast<const uint4*>(p.master + pos)[0];
-    x.w[1] = reinterpret_cast<const uint4*>(p.master + pos)[1];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) copy_async<16>(&st.w[k][t], p.master + pos + 4 * k);
   } else {
-    x.w[0] = *reinterpret_cast<const uint4*>(p.v.pool + pos);
+    copy_async<16>(&st.w[0][t], p.v.pool + pos);
+  }
+}
+__device__ __forceinline__ Work take_work(const Stage& st, bool master, uint32_t scales) {
+  const int t = threadIdx.x;
+  Work x;
+  x.g = from_f32(st.g[0][t], st.g[1][t]);
+  x.w = master ? from_f32(st.w[0][t], st.w[1][t]) : from_bf16(*reinterpret_cast<const uint4*>(&st.w[0][t]));
+  const uint4 c = *reinterpret_cast<const uint4*>(&st.codes[t]);
+  x.m = from_e4m3(make_uint2(c.x, c.y));
+  x.r = from_e4m3(make_uint2(c.z, c.w));
+  const float sm = bf16_value((uint16_t)scales), sr = bf16_value((uint16_t)(scales >> 16));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x.m.p[k] = mul2(x.m.p[k], pair_of(sm, sm));
+    x.r.p[k] = mul2(x.r.p[k], pair_of(sr, sr));
+    x.r.p[k] = mul2(x.r.p[k], x.r.p[k]);
   }
   return x;
 }
+struct NoStage {};
+template <bool kE4M3>
+using StageOf = std::conditional_t<kE4M3, Stage, NoStage>;
 
 // AdamW.  Bound by memory: per element 24 bytes (fp32 moments), 30 (and fp32
 // weights), 12 (8-bit moments), 4 more to clear the gradient; one pass, each
@@ -235,10 +265,16 @@ __device__ __forceinline__ Raw<kE4M3> read_raw(const DevProj& p, long long pos) 
 // eight neighbouring lanes, so a block's scale takes three shuffles.  Roots and
 // quotients are the hardware's approximations (2^-22 of an update, which is
 // itself a small part of a weight) and products work on pairs: with 8-bit moments
-// the IEEE forms' extra instructions, not memory, set the time.
+// the IEEE forms' extra instructions, not memory, set the time.  There a thread
+// also has its next eight on their way into its own places in shared memory (no
+// thread waits for another, no register is held): few bytes an element leave
+// latency to set the time (48 M elements with their norms: 190 us without, 169
+// with, 201 with two spans ahead; 188 M elements with fp32 moments, whose loads
+// are many, 1095 without and 1289 with).
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ TrainArgs a) {
   __shared__ StepShared sh;
+  __shared__ __align__(16) StageOf<kE4M3> stages[2];
   pdl_wait_then_release();
   Place q = find_place(a);
   const DevProj& p = a.p[q.g];
@@ -278,30 +314,34 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   const uint64_t b2 = pair_of(sh.b2, sh.b2), n2 = pair_of(sh.n2, sh.n2), down = pair_of(-sh.size, -sh.size);
   const uint64_t iroot = pair_of(sh.iroot, sh.iroot), eps = pair_of(sh.eps, sh.eps), decay = pair_of(sh.decay, sh.decay);
   uint16_t* const pool = const_cast<uint16_t*>(p.v.pool);
+  long long pos = place(0), npos = -2;
+  uint32_t scales = 0, nscales = 0;
+  auto ahead = [&](int j, long long at) -> uint32_t {
+    uint32_t two = 0;
+    if constexpr (kE4M3) {
+      if (at >= 0) {
+        read_ahead(stages[j & 1], p, at);
+        two = p.m_scale[at / LORA_ADAMW_BLOCK] | (uint32_t)p.r_scale[at / LORA_ADAMW_BLOCK] << 16;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    return two;
+  };
+  scales = ahead(0, pos);
   for (int j = 0; j < a.spans && q.e0 + (long long)j * kSpan < q.size; ++j) {
-    const long long pos = place(j);
-    Raw<kE4M3> x{};
-    if (pos >= 0) x = read_raw<kE4M3>(p, pos);
+    npos = place(j + 1);
+    nscales = ahead(j + 1, npos);
     if (pos == -1) report(a.err, LORA_DERR_BAD_PAGE);
     Eight m{}, r{};
+    if constexpr (kE4M3) asm volatile("cp.async.wait_group 1;" ::: "memory");
     if (pos >= 0) {
-      const Eight g = from_f32(x.g[0], x.g[1]);
-      Eight w = p.master != nullptr ? from_f32(*reinterpret_cast<const float4*>(&x.w[0]), *reinterpret_cast<const float4*>(&x.w[1]))
-                                    : from_bf16(x.w[0]);
-      if (kE4M3) {
-        m = from_e4m3(make_uint2(__float_as_uint(x.m[0].x), __float_as_uint(x.m[0].y)));
-        r = from_e4m3(make_uint2(__float_as_uint(x.r[0].x), __float_as_uint(x.r[0].y)));
-        const float sm = bf16_value((uint16_t)x.scales), sr = bf16_value((uint16_t)(x.scales >> 16));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          m.p[k] = mul2(m.p[k], pair_of(sm, sm));
-          r.p[k] = mul2(r.p[k], pair_of(sr, sr));
-          r.p[k] = mul2(r.p[k], r.p[k]);
-        }
-      } else {
-        m = from_f32(x.m[0], x.m[kE4M3 ? 0 : 1]);
-        r = from_f32(x.r[0], x.r[kE4M3 ? 0 : 1]);
-      }
+      Work x;
+      if constexpr (kE4M3) x = take_work(stages[j & 1], p.master != nullptr, scales);
+      else x = read_work(p, pos);
+      const Eight& g = x.g;
+      Eight& w = x.w;
+      m = x.m;
+      r = x.r;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint64_t gk = mul2(g.p[k], gs);
@@ -346,6 +386,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         }
       }
     }
+    pos = npos;
+    scales = nscales;
   }
 }
 
@@ -402,29 +444,28 @@ __global__ void __launch_bounds__(kThreads) sumsq_kernel(const __grid_constant__
   float s = 0.f;
   if (agree(a, q)) {
     const DevProj& p = a.p[q.g];
-    long long pos[kSumGroups];  // all first, then all loads: a thread has its 128 bytes in flight
+    for (int j0 = 0; j0 < a.spans; j0 += kSumGroups) {
+      long long pos[kSumGroups];  // all first, then all loads: a thread has its 128 bytes in flight
 #pragma unroll
-    for (int j = 0; j < kSumGroups; ++j) {
-      const long long e = q.e0 + (long long)(j * kThreads + threadIdx.x) * kGroup;
-      pos[j] = e < q.size ? pool_pos(p.v, q, e) : -2;
-    }
-    Eight g[kSumGroups] = {};
-#pragma unroll
-    for (int j = 0; j < kSumGroups; ++j)
-      if (pos[j] >= 0) {
-        const float4* at = reinterpret_cast<const float4*>(p.grad + pos[j]);
-        g[j] = from_f32(at[0], at[1]);
+      for (int j = 0; j < kSumGroups; ++j) {
+        const long long e = q.e0 + (long long)((j0 + j) * kThreads + threadIdx.x) * kGroup;
+        pos[j] = e < q.size ? pool_pos(p.v, q, e) : -2;
       }
-    uint64_t two = pair_of(0.f, 0.f);
+      Eight g[kSumGroups] = {};
 #pragma unroll
-    for (int j = 0; j < kSumGroups; ++j) {
-      if (pos[j] == -1) report(a.err, LORA_DERR_BAD_PAGE);
+      for (int j = 0; j < kSumGroups; ++j)
+        if (pos[j] >= 0) g[j] = read_f32(p.grad + pos[j]);
+      uint64_t two = pair_of(0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) two = fma2(g[j].p[k], g[j].p[k], two);
+      for (int j = 0; j < kSumGroups; ++j) {
+        if (pos[j] == -1) report(a.err, LORA_DERR_BAD_PAGE);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) two = fma2(g[j].p[k], g[j].p[k], two);
+      }
+      float u, v;
+      split(two, u, v);
+      s += u + v;
     }
-    float u, v;
-    split(two, u, v);
-    s = u + v;
   }
   const float t = block_sum(s, sh);
   if (threadIdx.x == 0) a.partial[(long long)blockIdx.y * a.partial_stride + a.partial0 + blockIdx.x] = t;
@@ -542,7 +583,16 @@ lora_status_t launch_over(const void* func, TrainArgs* a, const lora_train_proj_
   return LORA_OK;
 }
 
-// Spans of a chunk: four, which spreads a CTA's start over 8192 elements, once
+// Spans of a chunk of the sum: sixteen once the launch still has several CTAs for
+// every place on the GPU, else four.
+int sum_spans(const lora_train_proj_t* projs, int n_proj, int n_ids) {
+  long long chunks = 0;
+  for (int g = 0; g < n_proj; ++g)
+    chunks += chunks_of(projs[g].view.max_rank, (long long)projs[g].view.d_in + projs[g].view.d_out, 4 * kSumGroups * kSpan);
+  return chunks * n_ids >= 32LL * sm_count() ? 4 * kSumGroups : kSumGroups;
+}
+
+// Spans of a chunk of the step: four, which spreads a CTA's start over 8192 elements, once
 // the launch still has several CTAs for every place on the GPU.
 int step_spans(const lora_train_proj_t* projs, int n_proj, int n_ids) {
   long long chunks = 0;
@@ -552,11 +602,11 @@ int step_spans(const lora_train_proj_t* projs, int n_proj, int n_ids) {
 }
 
 // Chunks of all projections in the sum; -1 above what a launch can count.
-long long sum_chunks(const lora_train_proj_t* projs, int n_proj) {
+long long sum_chunks(const lora_train_proj_t* projs, int n_proj, int spans) {
   long long at = 0;
   for (int g = 0; g < n_proj; ++g)
-    at += chunks_of(projs[g].view.max_rank, projs[g].view.d_in, kSumChunk) +
-          chunks_of(projs[g].view.max_rank, projs[g].view.d_out, kSumChunk);
+    at += chunks_of(projs[g].view.max_rank, projs[g].view.d_in, spans * kSpan) +
+          chunks_of(projs[g].view.max_rank, projs[g].view.d_out, spans * kSpan);
   return at > 0x7fffffffLL ? -1 : at;
 }
 
@@ -584,7 +634,8 @@ size_t lora_grad_sumsq_workspace_bytes(const lora_train_proj_t* projs, int32_t n
   if (projs == nullptr || n_proj < 1 || n_ids < 0 || n_ids > LORA_MAX_ADAPTERS) return 0;
   for (int g = 0; g < n_proj; ++g)
     if (validate_view(&projs[g].view) != LORA_OK) return 0;
-  const long long n = sum_chunks(projs, n_proj);
+  const int spans = sum_spans(projs, n_proj, n_ids);
+  const long long n = sum_chunks(projs, n_proj, spans);
   return n < 0 ? 0 : (size_t)(((long long)n_ids * n * 4 + 16) / 16 * 16);
 }
 
@@ -596,7 +647,8 @@ lora_status_t lora_grad_sumsq(const lora_train_proj_t* projs, int32_t n_proj, co
   if (sumsq == nullptr || (reinterpret_cast<uintptr_t>(sumsq) & 3u) != 0) return LORA_ERR_INVALID_ARG;
   if (n_ids == 0) return LORA_OK;
   if (workspace == nullptr || !aligned16(workspace)) return LORA_ERR_INVALID_ARG;
-  const long long n = sum_chunks(projs, n_proj);
+  const int spans = sum_spans(projs, n_proj, n_ids);
+  const long long n = sum_chunks(projs, n_proj, spans);
   if (n < 0) return LORA_ERR_UNSUPPORTED;
   if (workspace_bytes < lora_grad_sumsq_workspace_bytes(projs, n_proj, n_ids)) return LORA_ERR_WORKSPACE;
   TrainArgs a;
@@ -605,7 +657,7 @@ lora_status_t lora_grad_sumsq(const lora_train_proj_t* projs, int32_t n_proj, co
   a.err = dev_err;
   a.partial = static_cast<float*>(workspace);
   a.partial_stride = (int)n;
-  st = launch_over((const void*)sumsq_kernel, &a, projs, n_proj, n_ids, kSumGroups, (cudaStream_t)stream);
+  st = launch_over((const void*)sumsq_kernel, &a, projs, n_proj, n_ids, spans, (cudaStream_t)stream);
   if (st != LORA_OK) return st;
   FinishArgs f;
   memset(&f, 0, sizeof(f));

@@ -460,6 +460,150 @@ __device__ __forceinline__ Grad pair_grad(const RowArgs& a, int t, int label) {
   return Grad{label, a.top[t], a.log2s[t], coef, false};
 }
 
+// -------------------------------------------------------------------- pairs --
+
+struct PairArgs {
+  const int32_t* labels;
+  const float* logp;
+  const float* ref;
+  const int32_t* indptr;
+  int n_pairs, T, V;
+  lora_pref_opts_t opt;
+  float* loss;
+  float* seq_logp;
+  float* coef;
+  int32_t* err;
+  int probed;  // the timeout probe is armed: the rows have no sums
+};
+
+// What a pair takes from one sequence's rows.
+struct PairSums {
+  Pair32 lp, d;
+  int count;
+};
+__device__ __forceinline__ PairSums add_sums(const PairSums& x, const PairSums& y) {
+  return PairSums{add_pair(x.lp, y.lp), add_pair(x.d, y.d), x.count + y.count};
+}
+
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+
+// What a pair gives its rows' gradients: their coefficient, by sequence.
+struct PairOut {
+  float coef[2];
+};
+
+// Whether the offsets are not ascending within [0, T], for a CTA of kT threads.
+template <int kT>
+__device__ __forceinline__ bool bad_offsets(const PairArgs& a) {
+  int bad = 0;
+  for (int k = threadIdx.x; k <= 2 * a.n_pairs; k += kT) {
+    const int hi = a.indptr[k], lo = k > 0 ? a.indptr[k - 1] : 0;
+    bad |= hi < lo || hi > a.T;
+  }
+  return __syncthreads_or(bad) != 0;
+}
+
+// No pair of a call with bad offsets has a loss.
+__device__ __forceinline__ void no_pair(const PairArgs& a, int p) {
+  a.loss[p] = 0.f;
+  if (a.seq_logp != nullptr) a.seq_logp[2 * p] = a.seq_logp[2 * p + 1] = 0.f;
+}
+
+// Pair p by a CTA of kT threads, half of it a sequence: the two sums (in a fixed
+// order), the loss (written where `write`) and its coefficients.  A latency: each
+// thread reads four rows at a time.
+template <int kT>
+__device__ __forceinline__ PairOut eval_pair(const PairArgs& a, int p, PairSums (&sh)[2][kT / 64], bool write) {
+  constexpr int kHalf = kT / 2;
+  const int tid = threadIdx.x, half = tid / kHalf, id = tid % kHalf;
+  const int t0 = a.indptr[2 * p + half], t1 = a.indptr[2 * p + half + 1];
+  PairSums x{{0.f, 0.f}, {0.f, 0.f}, 0};
+  for (long long t = t0 + id; t < t1; t += 4 * kHalf) {
+    int label[4];
+    float lp[4], ref[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const long long q = t + k * kHalf;
+      label[k] = q < t1 ? a.labels[q] : -1;
+      lp[k] = q < t1 ? a.logp[q] : 0.f;
+      ref[k] = q < t1 && a.ref != nullptr ? a.ref[q] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (label[k] >= 0 && label[k] < a.V) x = add_sums(x, PairSums{{lp[k], 0.f}, two_sum(lp[k], -ref[k]), 1});
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    PairSums o;
+    o.lp = Pair32{__shfl_xor_sync(0xffffffffu, x.lp.hi, s), __shfl_xor_sync(0xffffffffu, x.lp.lo, s)};
+    o.d = Pair32{__shfl_xor_sync(0xffffffffu, x.d.hi, s), __shfl_xor_sync(0xffffffffu, x.d.lo, s)};
+    o.count = __shfl_xor_sync(0xffffffffu, x.count, s);
+    x = add_sums(x, o);
+  }
+  if ((tid & 31) == 0) sh[half][id >> 5] = x;
+  __syncthreads();
+  Pair32 ratio[2];
+  float share[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    x = sh[s][0];
+    for (int k = 1; k < kHalf / 32; ++k) x = add_sums(x, sh[s][k]);
+    const bool mean = (a.opt.flags & LORA_PREF_AVERAGE) && x.count > 0;
+    share[s] = mean ? 1.f / (float)x.count : 1.f;
+    ratio[s] = mean ? Pair32{x.d.hi / (float)x.count, x.d.lo / (float)x.count} : x.d;
+    if (write && tid == 0 && a.seq_logp != nullptr) a.seq_logp[2 * p + s] = x.lp.hi;
+  }
+  const Pair32 dif = add_pair(ratio[0], Pair32{-ratio[1].hi, -ratio[1].lo});
+  const float D = dif.hi;
+  const float z = fmaf(a.opt.beta, D, -a.opt.margin);
+  float loss, slope;  // slope: dloss / dD
+  if (a.opt.kind == LORA_PREF_SIGMOID) {
+    const float e = a.opt.label_smoothing;
+    loss = slope = 0.f;  // a term of weight 0 is left out: its logarithm may be infinite
+    if (e < 1.f) {
+      loss = (1.f - e) * softplus(-z);
+      slope = (e - 1.f) * sigmoid(-z);
+    }
+    if (e > 0.f) {
+      loss += e * softplus(z);
+      slope += e * sigmoid(z);
+    }
+    slope *= a.opt.beta;
+  } else if (a.opt.kind == LORA_PREF_HINGE) {
+    loss = z < 1.f || z != z ? 1.f - z : 0.f;
+    slope = z < 1.f ? -a.opt.beta : z != z ? z : 0.f;
+  } else {
+    const float off = D - 0.5f / a.opt.beta;
+    loss = off * off;
+    slope = 2.f * off;
+  }
+  if (write && tid == 0) a.loss[p] = loss;
+  return PairOut{{slope * share[0] * a.opt.grad_scale, -slope * share[1] * a.opt.grad_scale}};
+}
+
+// One CTA a pair: its loss, and the coefficient of each of its rows.
+constexpr int kPairThreads = 512;
+__global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PairArgs a) {
+  __shared__ PairSums sh[2][kPairThreads / 64];
+  pdl_wait_then_release();
+  if (a.probed) return;
+  const int p = blockIdx.x;
+  if (bad_offsets<kPairThreads>(a)) {
+    if (threadIdx.x == 0) {
+      if (p == 0) report(a.err, LORA_DERR_BAD_SEQ);
+      no_pair(a, p);
+    }
+    return;
+  }
+  const PairOut o = eval_pair<kPairThreads>(a, p, sh, true);
+  if (a.coef == nullptr) return;
+  constexpr int kHalf = kPairThreads / 2;
+  const int half = threadIdx.x / kHalf;
+  for (long long t = a.indptr[2 * p + half] + threadIdx.x % kHalf; t < a.indptr[2 * p + half + 1]; t += kHalf)
+    a.coef[t] = o.coef[half];
+}
+
 // ------------------------------------------------------------- streamed form --
 
 // logp and lse of each row: one read of the logits.
@@ -494,6 +638,53 @@ __global__ void __launch_bounds__(kThreads) row_grad_kernel(const __grid_constan
   const int t = a.T - 1 - (int)cluster_id_x();
   const Cut<E> c = cut_row(static_cast<const E*>(a.logits) + (long long)t * a.ld, a.V, rank, n);
   const Grad g = pair_grad(a, t, row_label(a, t, false));
+  write_grad<E, kThreads>(c, static_cast<E*>(a.dlogits) + (long long)t * a.ldd, a.V, g);
+}
+
+// The same for calls of few rows, without the pairs' kernel before it: a row's CTAs
+// work its pair out themselves, from L2; the first row's leave the pair's loss.
+struct PairRowArgs {
+  RowArgs r;
+  PairArgs p;
+};
+template <typename E>
+__global__ void __launch_bounds__(kThreads) pair_row_kernel(const __grid_constant__ PairRowArgs f) {
+  __shared__ PairSums sh[2][kThreads / 64];
+  __shared__ int mine;  // the row's pair
+  const RowArgs& a = f.r;
+  const PairArgs& b = f.p;
+  const int n = (int)cluster_nctarank(), rank = (int)cluster_ctarank(), tid = threadIdx.x;
+  pdl_wait_then_release();
+  if (a.probe > 0) return;  // the sums of this call reported it
+  const int t = (int)cluster_id_x(), label = row_label(a, t, false);
+  const bool first_row = rank == 0 && t == 0;  // sees to pairs without rows, and to a bad call's
+  if (tid == 0) mine = -1;
+  const bool bad = bad_offsets<kThreads>(b);
+  if (bad && first_row) {
+    if (tid == 0) report(a.err, LORA_DERR_BAD_SEQ);
+    for (int k = tid; k < b.n_pairs; k += kThreads) no_pair(b, k);
+  }
+  if (!bad) {
+    for (int k = tid; k < b.n_pairs; k += kThreads)
+      if (b.indptr[2 * k] <= t && t < b.indptr[2 * k + 2]) mine = k;
+    if (first_row)
+      for (int k = 0; k < b.n_pairs; ++k)
+        if (b.indptr[2 * k] == b.indptr[2 * k + 2]) {
+          eval_pair<kThreads>(b, k, sh, true);
+          __syncthreads();
+        }
+  }
+  __syncthreads();
+  const int p = mine;
+  Grad g{label, 0.f, 0.f, 0.f, true};
+  if (p >= 0) {
+    const bool write = rank == 0 && t == b.indptr[2 * p];
+    if (label >= 0 || write) {
+      const float coef = eval_pair<kThreads>(b, p, sh, write).coef[t < b.indptr[2 * p + 1] ? 0 : 1];
+      if (label >= 0 && coef != 0.f && a.top[t] != -INF_F) g = Grad{label, a.top[t], a.log2s[t], coef, false};
+    }
+  }
+  const Cut<E> c = cut_row(static_cast<const E*>(a.logits) + (long long)t * a.ld, a.V, rank, n);
   write_grad<E, kThreads>(c, static_cast<E*>(a.dlogits) + (long long)t * a.ldd, a.V, g);
 }
 
@@ -738,121 +929,6 @@ __global__ void __launch_bounds__(held_threads(kG), (kVec > 8 ? 512 : 768) / hel
   if (n > 1) cluster_sync();
 }
 
-struct PairArgs {
-  const int32_t* labels;
-  const float* logp;
-  const float* ref;
-  const int32_t* indptr;
-  int n_pairs, T, V;
-  lora_pref_opts_t opt;
-  float* loss;
-  float* seq_logp;
-  float* coef;
-  int32_t* err;
-  int probed;  // the timeout probe is armed: the rows have no sums
-};
-
-// What a pair takes from one sequence's rows.
-struct PairSums {
-  Pair32 lp, d;
-  int count;
-};
-__device__ __forceinline__ PairSums add_sums(const PairSums& x, const PairSums& y) {
-  return PairSums{add_pair(x.lp, y.lp), add_pair(x.d, y.d), x.count + y.count};
-}
-
-__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
-
-// One CTA a pair, half of it a sequence: the two sums (in a fixed order), the
-// loss, and its coefficient for every row.  A latency: rows are read four at a
-// time by each thread.
-constexpr int kPairThreads = 512, kPairHalf = kPairThreads / 2;
-__global__ void __launch_bounds__(kPairThreads) pair_kernel(const __grid_constant__ PairArgs a) {
-  __shared__ PairSums sh[2][kPairHalf / 32];
-  pdl_wait_then_release();
-  if (a.probed) return;
-  const int p = blockIdx.x, tid = threadIdx.x, half = tid / kPairHalf, id = tid % kPairHalf;
-  int bad = 0;
-  for (int k = tid; k <= 2 * a.n_pairs; k += kPairThreads) {
-    const int hi = a.indptr[k], lo = k > 0 ? a.indptr[k - 1] : 0;
-    bad |= hi < lo || hi > a.T;
-  }
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) {
-      if (p == 0) report(a.err, LORA_DERR_BAD_SEQ);
-      a.loss[p] = 0.f;
-      if (a.seq_logp != nullptr) a.seq_logp[2 * p] = a.seq_logp[2 * p + 1] = 0.f;
-    }
-    return;
-  }
-  const int t0 = a.indptr[2 * p + half], t1 = a.indptr[2 * p + half + 1];
-  PairSums x{{0.f, 0.f}, {0.f, 0.f}, 0};
-  for (long long t = t0 + id; t < t1; t += 4 * kPairHalf) {
-    int label[4];
-    float lp[4], ref[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const long long q = t + k * kPairHalf;
-      label[k] = q < t1 ? a.labels[q] : -1;
-      lp[k] = q < t1 ? a.logp[q] : 0.f;
-      ref[k] = q < t1 && a.ref != nullptr ? a.ref[q] : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (label[k] >= 0 && label[k] < a.V) x = add_sums(x, PairSums{{lp[k], 0.f}, two_sum(lp[k], -ref[k]), 1});
-  }
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
-    PairSums o;
-    o.lp = Pair32{__shfl_xor_sync(0xffffffffu, x.lp.hi, s), __shfl_xor_sync(0xffffffffu, x.lp.lo, s)};
-    o.d = Pair32{__shfl_xor_sync(0xffffffffu, x.d.hi, s), __shfl_xor_sync(0xffffffffu, x.d.lo, s)};
-    o.count = __shfl_xor_sync(0xffffffffu, x.count, s);
-    x = add_sums(x, o);
-  }
-  if ((tid & 31) == 0) sh[half][id >> 5] = x;
-  __syncthreads();
-  Pair32 ratio[2];
-  float share[2];
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    x = sh[s][0];
-    for (int k = 1; k < kPairHalf / 32; ++k) x = add_sums(x, sh[s][k]);
-    const bool mean = (a.opt.flags & LORA_PREF_AVERAGE) && x.count > 0;
-    share[s] = mean ? 1.f / (float)x.count : 1.f;
-    ratio[s] = mean ? Pair32{x.d.hi / (float)x.count, x.d.lo / (float)x.count} : x.d;
-    if (tid == 0 && a.seq_logp != nullptr) a.seq_logp[2 * p + s] = x.lp.hi;
-  }
-  const Pair32 dif = add_pair(ratio[0], Pair32{-ratio[1].hi, -ratio[1].lo});
-  const float D = dif.hi;
-  const float z = fmaf(a.opt.beta, D, -a.opt.margin);
-  float loss, slope;  // slope: dloss / dD
-  if (a.opt.kind == LORA_PREF_SIGMOID) {
-    const float e = a.opt.label_smoothing;
-    loss = slope = 0.f;  // a term of weight 0 is left out: its logarithm may be infinite
-    if (e < 1.f) {
-      loss = (1.f - e) * softplus(-z);
-      slope = (e - 1.f) * sigmoid(-z);
-    }
-    if (e > 0.f) {
-      loss += e * softplus(z);
-      slope += e * sigmoid(z);
-    }
-    slope *= a.opt.beta;
-  } else if (a.opt.kind == LORA_PREF_HINGE) {
-    loss = z < 1.f || z != z ? 1.f - z : 0.f;
-    slope = z < 1.f ? -a.opt.beta : z != z ? z : 0.f;
-  } else {
-    const float off = D - 0.5f / a.opt.beta;
-    loss = off * off;
-    slope = 2.f * off;
-  }
-  if (tid == 0) a.loss[p] = loss;
-  if (a.coef == nullptr) return;
-  const float coef = (half == 0 ? slope * share[0] : -slope * share[1]) * a.opt.grad_scale;
-  for (long long t = t0 + id; t < t1; t += kPairHalf) a.coef[t] = coef;
-}
-
 // ------------------------------------------------------------------- host --
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -966,6 +1042,25 @@ lora_status_t launch_rows(int kind, int dtype, RowArgs* a, int T, cudaStream_t s
   return launch_pdl(f, dim3((unsigned)ctas), dim3((unsigned)threads), smem, s, p.n, a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
 
+// Whether the gradient's rows work their pairs out themselves.  It saves a launch
+// (host time, 2.3 us) and costs each row its pair's sums again: on the device 16
+// rows of 32000 take 7.9 us against 9.1, 90 rows 10.5 / 10.3, 256 rows 14.7 / 13.2.
+bool pairs_by_rows(int T, int V, int n_pairs, int dtype) {
+  return n_pairs > 0 && n_pairs <= 64 && T <= 128 && row_plan(kRowGrad, T, V, dtype).group == 0;
+}
+
+lora_status_t launch_pair_rows(int dtype, const RowArgs& a, const PairArgs& p, int T, cudaStream_t s) {
+  const int n = row_plan(kRowGrad, T, a.V, dtype).n;
+  PairRowArgs f;
+  memset(&f, 0, sizeof(f));
+  f.r = a;
+  f.r.T = T;
+  f.r.probe = wait_probe_cycles();
+  f.p = p;
+  const void* k = dtype == LORA_LOGITS_BF16 ? (const void*)pair_row_kernel<uint16_t> : (const void*)pair_row_kernel<float>;
+  return launch_pdl(k, dim3((unsigned)(T * n)), dim3(kThreads), 0, s, n, &f) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+}
+
 size_t pref_floats(int T) { return ((size_t)T + 3) / 4 * 4; }
 
 }  // namespace
@@ -1032,27 +1127,27 @@ lora_status_t lora_preference_loss(const void* logits, int64_t ld, int32_t dtype
   a.ldd = ldd;
   a.err = dev_err;
   if (T > 0 && (st = launch_rows(kRowSum, dtype, &a, T, s)) != LORA_OK) return st;
-  if (n_pairs > 0) {
-    PairArgs p;
-    memset(&p, 0, sizeof(p));
-    p.labels = labels;
-    p.logp = a.logp;
-    p.ref = ref_logp;
-    p.indptr = seq_indptr;
-    p.n_pairs = n_pairs;
-    p.T = T;
-    p.V = V;
-    p.opt = *opts;
-    p.loss = loss;
-    p.seq_logp = seq_logp;
-    p.coef = dlogits == nullptr ? nullptr : a.coef;
-    p.err = dev_err;
-    p.probed = a.probe > 0;
-    if (launch_pdl((const void*)pair_kernel, dim3((unsigned)n_pairs), dim3(kPairThreads), 0, s, 0, &p) != cudaSuccess)
-      return LORA_ERR_CUDA;
-  }
-  if (T == 0 || dlogits == nullptr) return LORA_OK;
-  return launch_rows(kRowGrad, dtype, &a, T, s);
+  PairArgs p;
+  memset(&p, 0, sizeof(p));
+  p.labels = labels;
+  p.logp = a.logp;
+  p.ref = ref_logp;
+  p.indptr = seq_indptr;
+  p.n_pairs = n_pairs;
+  p.T = T;
+  p.V = V;
+  p.opt = *opts;
+  p.loss = loss;
+  p.seq_logp = seq_logp;
+  p.coef = dlogits == nullptr ? nullptr : a.coef;
+  p.err = dev_err;
+  p.probed = wait_probe_cycles() > 0;
+  const bool grad = T > 0 && dlogits != nullptr;
+  if (grad && pairs_by_rows(T, V, n_pairs, dtype)) return launch_pair_rows(dtype, a, p, T, s);
+  if (n_pairs > 0 &&
+      launch_pdl((const void*)pair_kernel, dim3((unsigned)n_pairs), dim3(kPairThreads), 0, s, 0, &p) != cudaSuccess)
+    return LORA_ERR_CUDA;
+  return grad ? launch_rows(kRowGrad, dtype, &a, T, s) : LORA_OK;
 }
 
 lora_status_t lora_policy_loss(const void* logits, int64_t ld, int32_t dtype, const int32_t* labels,

@@ -421,3 +421,135 @@ def test_timeout_leaves_the_outputs():
     assert int(err) == 0
     want = torch.log_softmax(x.double(), 1)[:, 0]
     assert float((logp.double() - want).abs().max()) <= ATOL
+
+
+def policy64(x, lab, old, adv, ref, w, lo, hi, kl_coef, scale):
+    """(logp, loss, kl, gradient, coefficient) of the policy loss in 64 bits on the GPU (rows with visible labels)."""
+    x, on = x.double(), lab >= 0
+    at = lab.long().clamp(min=0)[:, None]
+    lse = torch.logsumexp(x, 1)
+    lp = torch.where(on, x.gather(1, at)[:, 0] - lse, torch.zeros_like(lse))
+    q, d, a = torch.exp(lp - old.double()), ref.double() - lp, adv.double()
+    first, held = q * a, q.clamp(1 - lo, 1 + hi) * a
+    kl = torch.expm1(d) - d
+    loss = w.double() * (kl_coef * kl - torch.minimum(first, held))
+    coef = -scale * w.double() * (kl_coef * torch.expm1(d) + torch.where(first <= held, first, torch.zeros_like(first)))
+    coef = torch.where(on, coef, torch.zeros_like(coef))
+    g = -coef[:, None] * torch.exp(x - lse[:, None])
+    g.scatter_add_(1, at, coef[:, None])
+    g = torch.where(on[:, None], g, torch.zeros_like(g))
+    zero = torch.zeros_like(lp)
+    return lp, torch.where(on, loss, zero), torch.where(on, kl, zero), g, coef, lse, q, torch.exp(d)
+
+
+# row lengths and counts on both sides of every change of the kernels' form
+FORMS = [(400, 1020), (400, 1030), (290, 3001), (400, 3001), (400, 4100), (400, 8001), (400, 8203), (400, 12003), (400, 16400),
+         (60, 20000), (150, 20000), (330, 20000), (20, 50257), (400, 50257), (310, 128256), (320, 65600)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", FORMS)
+@pytest.mark.parametrize("shift", [0, 3])
+def test_policy_forms(T, V, shift, dtype):
+    """Every form of the row kernels over many rows, aligned and not, apart and in place, with the same bits
+    twice."""
+    g = torch.Generator(device="cuda").manual_seed(T + V)
+    ld = V + (-V % 8 if shift == 0 else 5)
+    flat = torch.full((T * ld + 32,), GUARD, dtype=DTYPES[dtype], device="cuda")
+    x = flat[shift: shift + T * ld].view(T, ld)[:, :V]
+    x.copy_((torch.randn(T, V, generator=g, device="cuda") * 3).clamp(-30, 30))
+    lab = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    lab[torch.rand(T, generator=g, device="cuda") < 0.2] = -1
+    lp = torch.log_softmax(x.float(), 1).gather(1, lab.long().clamp(min=0)[:, None])[:, 0]
+    pick = torch.tensor([-0.6, -0.1, 0.0, 0.1, 0.6], device="cuda")[torch.randint(0, 5, (T,), generator=g, device="cuda")]
+    old, ref = lp + pick, lp + 0.3 * torch.randn(T, generator=g, device="cuda")
+    adv, w = torch.randn(T, generator=g, device="cuda"), 0.1 + torch.rand(T, generator=g, device="cuda")
+    e_lp, e_loss, e_kl, e_g, coef, lse, q, ed = policy64(x, lab, old, adv, ref, w, 0.2, 0.3, 0.07, 1.3)
+    logp, loss, kl = (torch.full((T,), GUARD, device="cuda") for _ in range(3))
+    d, err = torch.full((T, V), GUARD, dtype=DTYPES[dtype], device="cuda"), new_err()
+    kw = dict(ref_logp=ref, weight=w, clip_low=0.2, clip_high=0.3, kl_coef=0.07, grad_scale=1.3, err=err)
+    B.lora_policy_loss(x, lab, old, adv, logp, loss, kl, d, **kw)
+    assert float((logp - e_lp).abs().max()) <= ATOL
+    dq = 2e-5 * q * adv.abs().double()
+    dk = 0.07 * (ed + 1) * 2e-5
+    on = lab >= 0
+    assert bool(((loss - e_loss).abs() <= w * (dk + dq) + 1e-6 * e_loss.abs() + 1e-7)[on].all())
+    assert bool(((kl - e_kl).abs() <= (ed + 1) * 2e-5 + 2.0 ** -22 * e_kl + 1e-7)[on].all())
+    assert not loss[~on].any() and not kl[~on].any() and not logp[~on].any() and not d[~on].any()
+    c = coef.abs()[:, None]
+    p = torch.exp(x.double() - lse[:, None])
+    dc = (1.3 * w.double() * (dk + dq) + 1e-6 * coef.abs())[:, None]
+    one = torch.zeros_like(p).scatter_(1, lab.long().clamp(min=0)[:, None], 1.0)
+    bound = dc * ((one - p).abs() + PTOL) + c * (p * PTOL + (one + p) * 2.0 ** -22) + 1e-37
+    if dtype == "bf16":
+        bound = bound + 2.0 ** -8 * (e_g.abs() + bound)
+    assert bool(((d.double() - e_g).abs() <= bound)[on].all())
+    again, logp2 = torch.empty_like(d), torch.empty_like(logp)
+    B.lora_policy_loss(x, lab, old, adv, logp2, loss, kl, again, **kw)
+    assert torch.equal(again, d) and torch.equal(logp2, logp)
+    B.lora_policy_loss(x, lab, old, adv, logp2, loss, kl, x, **kw)
+    if shift == 0:
+        assert torch.equal(x, d)
+    else:  # another store path, the same values
+        assert torch.equal(x, d) and torch.equal(logp2, logp)
+    x.fill_(GUARD)
+    assert bool((flat == GUARD).all())
+    assert int(err) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,n", [(128, 9001, 3), (129, 9001, 3), (100, 9000, 64), (100, 9000, 65), (8, 40000, 4), (400, 50257, 6)])
+def test_preference_forms(T, V, n, dtype):
+    """Few and many rows, sequences without rows: loss, sums and gradient against 64 bits on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(T + V + n)
+    rng = np.random.default_rng(n)
+    x = (torch.randn(T, V, generator=g, device="cuda") * 3).to(DTYPES[dtype])
+    lab = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    lab[torch.rand(T, generator=g, device="cuda") < 0.3] = -1
+    indptr = sequences(rng, T, n)
+    indptr[2] = indptr[0]  # the first pair has no rows
+    indptr[1] = indptr[0]
+    indptr[-1] = T
+    x64 = x.double()
+    lse = torch.logsumexp(x64, 1)
+    at = lab.long().clamp(min=0)[:, None]
+    on = lab >= 0
+    lp = torch.where(on, x64.gather(1, at)[:, 0] - lse, torch.zeros_like(lse))
+    ref = (lp + 0.2 * torch.randn(T, generator=g, device="cuda")).float()
+    gap = torch.where(on, lp - ref.double(), torch.zeros_like(lp))
+    loss, seq, err = torch.full((n,), GUARD, device="cuda"), torch.full((2 * n,), GUARD, device="cuda"), new_err()
+    d = torch.full_like(x, GUARD)
+    B.lora_preference_loss(x, lab, dev(indptr, np.int32), loss, seq, d, B.preference_workspace(T, n), ref_logp=ref, beta=0.1,
+                           grad_scale=2.0, err=err)
+    coef = torch.zeros_like(lp)
+    for p in range(n):
+        i0, i1, i2 = (int(v) for v in indptr[2 * p: 2 * p + 3])
+        z = 0.1 * float(gap[i0:i1].sum() - gap[i1:i2].sum())
+        counted = int(on[i0:i2].sum())
+        assert abs(float(loss[p]) - np.log1p(np.exp(-z))) <= 0.1 * ATOL * counted + 1e-6 * (1 + abs(z))
+        for s, (a, b) in enumerate(((i0, i1), (i1, i2))):
+            assert abs(float(seq[2 * p + s]) - float(lp[a:b].sum())) <= ATOL * max(1, int(on[a:b].sum())) + 2.0 ** -23 * abs(float(lp[a:b].sum()))
+        slope = -0.1 * 2.0 / (1 + np.exp(z))
+        coef[i0:i1], coef[i1:i2] = slope, -slope
+    coef = torch.where(on, coef, torch.zeros_like(coef))
+    p = torch.exp(x64 - lse[:, None])
+    e_g = -coef[:, None] * p
+    e_g.scatter_add_(1, at, coef[:, None])
+    one = torch.zeros_like(p).scatter_(1, at, 1.0)
+    c = coef.abs()[:, None]
+    bound = c * 1e-6 + 2.0 * 0.0025 * ATOL * T * (one + p) + c * (p * PTOL + (one + p) * 2.0 ** -22) + 1e-37
+    if dtype == "bf16":
+        bound = bound + 2.0 ** -8 * (e_g.abs() + bound)
+    err_g = (d.double() - torch.where(on[:, None], e_g, torch.zeros_like(e_g))).abs()
+    assert bool((err_g <= bound).all())
+    assert int(err) == 0
+
+
+def test_preference_bad_offsets_of_long_rows():
+    x = torch.randn(20, 9000, device="cuda")
+    lab = torch.zeros(20, dtype=torch.int32, device="cuda")
+    loss, seq = torch.full((2,), GUARD, device="cuda"), torch.full((4,), GUARD, device="cuda")
+    d, err = torch.full_like(x, GUARD), new_err()
+    B.lora_preference_loss(x, lab, dev([0, 5, 10, 8, 20], np.int32), loss, seq, d, B.preference_workspace(20, 2), err=err)
+    assert int(err) == B.LORA_DERR_BAD_SEQ
+    assert not loss.any() and not seq.any() and not d.any()

@@ -48,7 +48,8 @@ struct TrainArgs {
   int partial_stride;
   int partial0;
   int zero_grad;
-  int spans;  // spans of a chunk
+  int spans;    // spans of a chunk
+  int reverse;  // chunks in reverse order
   int32_t* err;
 };
 static_assert(sizeof(TrainArgs) <= 4096, "kernel parameters");
@@ -70,7 +71,7 @@ struct Place {
 __device__ __forceinline__ Place find_place(const TrainArgs& a) {
   Place q;
   const int chunk = a.spans * kSpan;
-  const int e = blockIdx.y, c = blockIdx.x;
+  const int e = a.reverse ? gridDim.y - 1 - blockIdx.y : blockIdx.y, c = a.reverse ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
   q.ad = a.ids[e];
   q.g = 0;
   while (q.g + 1 < a.n_proj && c >= a.p[q.g + 1].chunk0) ++q.g;
@@ -688,6 +689,7 @@ lora_status_t lora_adamw_step(const lora_train_proj_t* projs, int32_t n_proj, in
   a.hyper = hyper;
   a.sumsq = sumsq;
   a.zero_grad = (flags & LORA_ADAMW_ZERO_GRAD) ? 1 : 0;
+  a.reverse = sumsq != nullptr;  // the gradients that the norms read last are still in L2
   a.err = dev_err;
   return launch_over(state == LORA_STATE_E4M3 ? (const void*)adamw_kernel<true> : (const void*)adamw_kernel<false>, &a,
                      projs, n_proj, n_ids, step_spans(projs, n_proj, n_ids), (cudaStream_t)stream);

@@ -266,12 +266,15 @@ def _check(status: int, what: str):
         raise LoraError(status, what)
 
 
+def _handle(stream) -> int:
+    """A stream's handle as a plain integer."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:  # the current stream's handle, without building a torch.cuda.Stream around it
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+    return ctypes.c_void_p(_handle(stream))
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -684,7 +687,7 @@ def lora_token_logprobs(logits: torch.Tensor, labels: torch.Tensor, logp: torch.
     f32 = torch.float32
     _check(lib().lora_token_logprobs(p, ld, code, _rows(labels, T, torch.int32, "labels"), T, V,
                                      _rows(logp, T, f32, "logp"), _rows(lse, T, f32, "lse"), _addr(err),
-                                     _stream(stream)), "lora_token_logprobs")
+                                     _handle(stream)), "lora_token_logprobs")
 
 
 def preference_workspace(T: int, n_pairs: int, device="cuda") -> torch.Tensor:
@@ -710,7 +713,7 @@ def lora_preference_loss(logits: torch.Tensor, labels: torch.Tensor, seq_indptr:
                                       _rows(seq_indptr, 2 * n + 1, torch.int32, "seq_indptr"), n, T, V,
                                       opts, _rows(loss, n, f32, "loss"),
                                       _rows(seq_logp, 2 * n, f32, "seq_logp"), dp, ldd, _addr(workspace),
-                                      workspace.numel() * workspace.element_size(), _addr(err), _stream(stream)),
+                                      workspace.nbytes, _addr(err), _handle(stream)),
            "lora_preference_loss")
 
 
@@ -729,7 +732,7 @@ def lora_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch
                                   _rows(old_logp, T, f32, "old_logp"), _rows(ref_logp, T, f32, "ref_logp"),
                                   _rows(advantage, T, f32, "advantage"), _rows(weight, T, f32, "weight"), T, V,
                                   opts, _rows(logp, T, f32, "logp"), _rows(loss, T, f32, "loss"),
-                                  _rows(kl, T, f32, "kl"), dp, ldd, _addr(err), _stream(stream)), "lora_policy_loss")
+                                  _rows(kl, T, f32, "kl"), dp, ldd, _addr(err), _handle(stream)), "lora_policy_loss")
 
 
 # --------------------------------------------------- training: optimizer step --
@@ -800,14 +803,15 @@ def adamw_hyper(n_adapters: int, step=1, lr=1e-4, beta1=0.9, beta2=0.999, eps=1e
 
 
 def _ids(ids: torch.Tensor):
-    n = int(ids.numel())
-    return _rows(ids, n, torch.int32, "ids"), n
+    if ids.dtype is not torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids: expected contiguous elements of torch.int32")
+    return ids.data_ptr(), ids.numel()
 
 
 def lora_adamw_init(train: TrainSet, ids: torch.Tensor, err: Optional[torch.Tensor] = None, stream=None):
     """Zero the listed adapters' gradients and moments; master takes the pool's weights."""
     p, n = _ids(ids)
-    _check(lib().lora_adamw_init(train.c, train.n, train.state, p, n, _addr(err), _stream(stream)), "lora_adamw_init")
+    _check(lib().lora_adamw_init(train.c, train.n, train.state, p, n, _addr(err), _handle(stream)), "lora_adamw_init")
 
 
 def lora_grad_sumsq(train: TrainSet, ids: torch.Tensor, sumsq: torch.Tensor, workspace: torch.Tensor,
@@ -816,7 +820,7 @@ def lora_grad_sumsq(train: TrainSet, ids: torch.Tensor, sumsq: torch.Tensor, wor
     p, n = _ids(ids)
     _check(lib().lora_grad_sumsq(train.c, train.n, p, n, 1 if accumulate else 0,
                                  _rows(sumsq, train.n_adapters, torch.float32, "sumsq"), _addr(workspace),
-                                 workspace.numel() * workspace.element_size(), _addr(err), _stream(stream)),
+                                 workspace.nbytes, _addr(err), _handle(stream)),
            "lora_grad_sumsq")
 
 
@@ -824,9 +828,9 @@ def lora_adamw_step(train: TrainSet, ids: torch.Tensor, hyper: torch.Tensor, sum
                     zero_grad: bool = False, err: Optional[torch.Tensor] = None, stream=None):
     """One AdamW step of the listed adapters in place (see include/lora_train.h); hyper: see adamw_hyper."""
     p, n = _ids(ids)
-    if hyper.numel() * hyper.element_size() != 32 * train.n_adapters or not hyper.is_contiguous():
+    if hyper.nbytes != 32 * train.n_adapters or not hyper.is_contiguous():
         raise ValueError("hyper: expected %d settings of 32 bytes" % train.n_adapters)
     _check(lib().lora_adamw_step(train.c, train.n, train.state, p, n, _addr(hyper),
                                  _rows(sumsq, train.n_adapters, torch.float32, "sumsq"),
-                                 LORA_ADAMW_ZERO_GRAD if zero_grad else 0, _addr(err), _stream(stream)),
+                                 LORA_ADAMW_ZERO_GRAD if zero_grad else 0, _addr(err), _handle(stream)),
            "lora_adamw_step")

@@ -142,7 +142,7 @@ lora_status_t lora_policy_loss(const void* logits, int64_t ld, int32_t dtype, co
  * A scale is bf16(largest magnitude of the block / 448); codes are rounded to
  * nearest, ties to even; a root above zero never takes code 0, so that no
  * element divides by eps alone; a block whose largest value is below 2^-100
- * holds zeros.
+ * holds zeros, and second moments below 2^-126 count as zero.
  */
 #define LORA_STATE_F32 0
 #define LORA_STATE_E4M3 1

@@ -114,7 +114,7 @@ int max_active_clusters(const void* func, int block, size_t smem, int cluster_x)
     int n;
   };
   static std::mutex mu;
-  static Entry cache[32];
+  static Entry cache[256];
   static int n_cache = 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
@@ -139,7 +139,7 @@ int max_active_clusters(const void* func, int block, size_t smem, int cluster_x)
     cudaGetLastError();
     n = 1;
   }
-  if (n_cache < 32) cache[n_cache++] = Entry{dev, func, block, smem, cluster_x, n};
+  if (n_cache < 256) cache[n_cache++] = Entry{dev, func, block, smem, cluster_x, n};
   return n;
 }
 

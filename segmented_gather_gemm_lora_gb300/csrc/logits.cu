@@ -41,6 +41,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
 // One element and a 16-byte vector of a row's type.
 template <typename E>
 struct Elem;
@@ -436,8 +437,10 @@ __device__ __forceinline__ PolicyRow policy_row(const RowArgs& a, int t, float x
 __device__ __forceinline__ Grad policy_grad(const RowArgs& a, int t, int label, const PolicyRow& p, const Sum& r, bool lead) {
   const float l2 = log2f(r.s);
   const float lp = empty(r) ? -INF_F : fmaf(l2, -kLn2, p.x - base_of(r.m)), q = expf(lp - p.old);
-  const float free_ = q * p.adv, held = fminf(fmaxf(q, 1.f - a.opt.clip_low), 1.f + a.opt.clip_high) * p.adv;
-  const bool open = free_ <= held;
+  // comparisons that a NaN fails leave it in the ratio and the ratio open
+  const float low = 1.f - a.opt.clip_low, high = 1.f + a.opt.clip_high;
+  const float free_ = q * p.adv, held = (q < low ? low : q > high ? high : q) * p.adv;
+  const bool open = !(free_ > held);
   float kl = 0.f, slope = 0.f;
   if (a.opt.kl_coef > 0.f) {
     const float d = p.ref - lp, g = expm1f(d);
@@ -717,7 +720,7 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const __grid_constant_
 // ----------------------------------------------------------------- held form --
 //
 // A row is held by a group of kG threads: a warp (kG = 32, eight rows a CTA at a
-// time) or a CTA of each of the n of a cluster (kG = 256), kVec vectors a thread.
+// time) or a CTA of kG threads of each of the n of a cluster, kVec vectors a thread.
 // Groups take rows group, group + groups, ...
 //
 // With kG > 32 the coming row's share waits in shared memory: thread 0 starts its

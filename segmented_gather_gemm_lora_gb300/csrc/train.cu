@@ -66,8 +66,7 @@ struct Place {
 };
 
 // Resolve blockIdx into a Place.  The threads still have to agree on `twice` (an
-// id listed before is passed over: its elements have one writer), so that loads
-// can be under way by then.
+// id listed before is passed over: its elements have one writer).
 __device__ __forceinline__ Place find_place(const TrainArgs& a) {
   Place q;
   const int chunk = a.spans * kSpan;
@@ -279,7 +278,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   pdl_wait_then_release();
   Place q = find_place(a);
   const DevProj& p = a.p[q.g];
-  // the pool position of this thread's eight elements of span j, -1 for none
+  // the pool position of this thread's eight elements of span j: -2 for none, -1
+  // off the pool
   auto place = [&](int j) -> long long {
     const long long e = q.e0 + (long long)(j * kThreads + threadIdx.x) * kGroup;
     return j < a.spans && e < q.size ? pool_pos(p.v, q, e) : -2;

@@ -553,3 +553,31 @@ def test_preference_bad_offsets_of_long_rows():
     B.lora_preference_loss(x, lab, dev([0, 5, 10, 8, 20], np.int32), loss, seq, d, B.preference_workspace(20, 2), err=err)
     assert int(err) == B.LORA_DERR_BAD_SEQ
     assert not loss.any() and not seq.any() and not d.any()
+
+
+@pytest.mark.parametrize("T,V", [(6, 100), (6, 3000), (400, 3000), (6, 40000), (400, 40000), (2, 600000)])
+def test_nan_logits_show_in_their_row_alone(T, V):
+    """A NaN among the logits makes its row's loss and gradient NaN (so the gradient norm skips the adapter)
+    and leaves the other rows as they are; in a pair it reaches the pair's rows and no other's."""
+    x = torch.randn(T, V, device="cuda")
+    lab = torch.arange(T, dtype=torch.int32, device="cuda") % V
+    old, adv = torch.full((T,), -8.0, device="cuda"), torch.ones(T, device="cuda")
+    adv[T // 2:] = -1.0
+    outs = []
+    for bad in (False, True):
+        if bad:
+            x[1, V // 3] = float("nan")
+        logp, loss, d = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty_like(x)
+        B.lora_policy_loss(x, lab, old, adv, logp, loss, None, d)
+        outs.append((logp, loss, d))
+    keep = torch.arange(T, device="cuda") != 1
+    for good, bad in zip(*outs):
+        assert torch.equal(good[keep], bad[keep])
+        assert bool(torch.isnan(bad[1]).all())
+    if T >= 4:
+        n = 2
+        indptr = dev([0, 1, T // 2, T // 2 + 1, T], np.int32)
+        loss, d = torch.empty(n, device="cuda"), torch.empty_like(x)
+        B.lora_preference_loss(x, lab, indptr, loss, None, d, B.preference_workspace(T, n), beta=0.01)
+        assert np.isnan(float(loss[0])) and np.isfinite(float(loss[1]))
+        assert bool(torch.isnan(d[: T // 2]).all()) and bool(torch.isfinite(d[T // 2:]).all())

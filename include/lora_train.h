@@ -17,7 +17,9 @@
  * argument errors found on the host are returned before anything is launched,
  * and what only the device can see is OR-ed into *dev_err (may be NULL).
  * Calls can be captured in CUDA graphs.  Results do not depend on timing: every
- * sum has a fixed order.
+ * sum has a fixed order (which depends on where a row's 16-byte boundaries lie).
+ * A bounded wait inside a kernel that ran out sets LORA_DERR_TIMEOUT; the rows it
+ * concerned are left as they were.
  */
 #ifndef LORA_TRAIN_H
 #define LORA_TRAIN_H

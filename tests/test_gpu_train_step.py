@@ -398,3 +398,52 @@ def test_other_stream_and_graph():
     for x in s[1:]:
         got = x.host()
         assert all(np.array_equal(want[k], got[k]) for k in want)
+
+
+@pytest.mark.parametrize("state", ["f32", "e4m3"])
+def test_hundreds_of_adapters(state):
+    """More listed adapters than a CTA has threads, one listed twice far apart, each with its own settings; the
+    chunks of long matrices (several spans) beside those of short ones."""
+    n = 300
+    ranks = [1 + (k * 7) % 3 for k in range(n)]
+    s = Setup(11, 64, 72, ranks, 64, state, True)
+    ts, err = B.TrainSet([s.t]), new_err()
+    order = np.random.default_rng(0).permutation(n)
+    listed = list(order) + [int(order[3])]
+    h = settings(n, 5, max_norm=[0.002 if k % 2 else 0.0 for k in range(n)])
+    sumsq = torch.zeros(n, device="cuda")
+    before = s.host()
+    B.lora_grad_sumsq(ts, ids_of(listed), sumsq, ts.sumsq_workspace(n + 1), err=err)
+    assert int(err) == B.LORA_DERR_BAD_ADAPTER  # the repeated id
+    err.zero_()
+    B.lora_adamw_step(ts, ids_of(listed), B.adamw_hyper(n, **h), sumsq=sumsq, zero_grad=True, err=err)
+    assert int(err) == B.LORA_DERR_BAD_ADAPTER
+    after, got = s.host(), sumsq.cpu().numpy()
+    where = []
+    for i in range(n):
+        total = sum(float((s.g[q].astype(np.float64) ** 2).sum()) for q in R.positions(s.pool, i))
+        assert abs(got[i] - total) <= 3e-6 * total
+        where.append(check_adapter(s, before, after, i, one(h, i), total, True))
+    untouched(s, before, after, where)
+
+
+@pytest.mark.parametrize("state", ["f32", "e4m3"])
+@pytest.mark.parametrize("master", [False, True])
+def test_chunks_of_several_spans(state, master):
+    """A launch of so many places (by max_rank) that a chunk is several spans, of the step and of the norms:
+    matrices that end inside a span, a block and a page."""
+    ranks = [1 + (k * 3) % 5 for k in range(72)]
+    s = Setup(12, 8200, 12008, ranks, 1024, state, master, max_rank=64)
+    listed = [k for k in reversed(range(72)) if k != 4]
+    ts, ids, err = B.TrainSet([s.t]), ids_of(listed), new_err()
+    h = settings(72, 6, max_norm=0.01)
+    sumsq, before = torch.zeros(72, device="cuda"), s.host()
+    B.lora_grad_sumsq(ts, ids, sumsq, ts.sumsq_workspace(len(listed)), err=err)
+    B.lora_adamw_step(ts, ids, B.adamw_hyper(72, **h), sumsq=sumsq, err=err)
+    after, got, where = s.host(), sumsq.cpu().numpy(), []
+    for i in listed:
+        total = sum(float((s.g[q].astype(np.float64) ** 2).sum()) for q in R.positions(s.pool, i))
+        assert abs(got[i] - total) <= 3e-6 * total
+        where.append(check_adapter(s, before, after, i, one(h, i), total, False))
+    untouched(s, before, after, where)
+    assert int(err) == 0

@@ -160,6 +160,19 @@ __device__ __forceinline__ uint2 to_e4m3(const Eight& x) {
   return make_uint2(w[0], w[1]);
 }
 
+// a / b where ib is near 1 / b and b has few bits (a scale, or 448): the approximate
+// quotient is a few units off, so its residual is exact, and one Newton step leaves a
+// quotient that rounds to the code or scale of the true one.  (a ib alone falls on
+// the other side of a boundary that a / b sits on or beside.)
+__device__ __forceinline__ float quotient(float a, float b, float ib) {
+  const float q = a * ib;
+  return fmaf(fmaf(-q, b, a), ib, q);
+}
+__device__ __forceinline__ uint64_t quotient2(uint64_t a, uint64_t minus_b, uint64_t ib) {
+  const uint64_t q = mul2(a, ib);
+  return fma2(fma2(q, minus_b, a), ib, q);
+}
+
 // The scale of a block of 64 whose elements the eight lanes around this one hold.
 __device__ __forceinline__ uint16_t block_scale(const Eight& x) {
   float top = 0.f;
@@ -171,17 +184,32 @@ __device__ __forceinline__ uint16_t block_scale(const Eight& x) {
   }
 #pragma unroll
   for (int s = 1; s < kBlockLanes; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  return __bfloat16_as_ushort(__float2bfloat16_rn(top < kTiny ? 0.f : top * (1.f / 448.f)));
+  return __bfloat16_as_ushort(__float2bfloat16_rn(top < kTiny ? 0.f : quotient(top, 448.f, 1.f / 448.f)));
 }
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 
-template <bool kFlush>  // 2^-23 relative; kFlush: denormal arguments count as zero (fewer instructions)
-__device__ __forceinline__ float sqrt_fast(float x) {
+__device__ __forceinline__ float sqrt_fast(float x) {  // 2^-23 relative
   float y;
-  if (kFlush) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  else asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two roots, within a hair of half a unit: from g near 1 / sqrt(x), x g and one step
+// of Newton's iteration.  Arguments below 2^-126 count as zero; infinity and NaN are
+// their own roots.
+__device__ __forceinline__ float rsqrt_fast(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(x, 1.17549435e-38f)));
+  return y;
+}
+__device__ __forceinline__ uint64_t roots(uint64_t x) {
+  asm("mul.rn.ftz.f32x2 %0, %0, %1;" : "+l"(x) : "l"(pair_of(1.f, 1.f)));
+  float u, v, a, b;
+  split(x, u, v);
+  const uint64_t g = pair_of(rsqrt_fast(u), rsqrt_fast(v)), y = mul2(x, g);
+  split(fma2(fma2(y, y, pair_of(-u, -v)), mul2(g, pair_of(-0.5f, -0.5f)), y), a, b);
+  const float inf = __int_as_float(0x7f800000);
+  return pair_of(u < inf ? a : u, v < inf ? b : v);
 }
 __device__ __forceinline__ float rcp_fast(float x) {  // one unit
   float y;
@@ -271,6 +299,10 @@ using StageOf = std::conditional_t<kE4M3, Stage, NoStage>;
 // latency to set the time (48 M elements with their norms: 190 us without, 169
 // with, 201 with two spans ahead; 188 M elements with fp32 moments, whose loads
 // are many, 1095 without and 1289 with).
+// What an 8-bit state keeps is rounded as its definition says: scales, codes and
+// roots carry the correction steps above (48 M elements with their norms: 167.5 us;
+// 166.5 with approximate roots, 164.5 with approximate quotients too, 177 with the
+// IEEE forms of everything.  1.4 M elements in pages of 64: 12.0, 12.0, 11.9, 13.3).
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ TrainArgs a) {
   __shared__ StepShared sh;
@@ -356,8 +388,12 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         float u, v;
-        split(r.p[k], u, v);
-        r.p[k] = pair_of(sqrt_fast<kE4M3>(u), sqrt_fast<kE4M3>(v));
+        if (kE4M3) {
+          r.p[k] = roots(r.p[k]);
+        } else {
+          split(r.p[k], u, v);
+          r.p[k] = pair_of(sqrt_fast(u), sqrt_fast(v));
+        }
         split(fma2(r.p[k], iroot, eps), u, v);
         w.p[k] = fma2(w.p[k], decay, mul2(down, mul2(m.p[k], pair_of(rcp_fast(u), rcp_fast(v)))));
       }
@@ -373,8 +409,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float u, v;
-          m.p[k] = mul2(m.p[k], pair_of(im, im));
-          split(mul2(r.p[k], pair_of(ir, ir)), u, v);
+          m.p[k] = quotient2(m.p[k], pair_of(-sm, -sm), pair_of(im, im));
+          split(quotient2(r.p[k], pair_of(-sr, -sr), pair_of(ir, ir)), u, v);
           if (u > 0.f) u = fmaxf(u, 0.001953125f);  // 2^-9, the smallest code
           if (v > 0.f) v = fmaxf(v, 0.001953125f);
           r.p[k] = pair_of(u, v);

@@ -189,11 +189,6 @@ __device__ __forceinline__ uint16_t block_scale(const Eight& x) {
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 
-__device__ __forceinline__ float sqrt_fast(float x) {  // 2^-23 relative
-  float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Two roots, within a hair of half a unit: from g near 1 / sqrt(x), x g and one step
 // of Newton's iteration.  Arguments below 2^-126 count as zero; infinity and NaN are
 // their own roots.
@@ -290,10 +285,12 @@ using StageOf = std::conditional_t<kE4M3, Stage, NoStage>;
 // AdamW.  Bound by memory: per element 24 bytes (fp32 moments), 30 (and fp32
 // weights), 12 (8-bit moments), 4 more to clear the gradient; one pass, each
 // byte moved once.  A thread's eight elements lie on one page, a block's 64 in
-// eight neighbouring lanes, so a block's scale takes three shuffles.  Roots and
-// quotients are the hardware's approximations (2^-22 of an update, which is
-// itself a small part of a weight) and products work on pairs: with 8-bit moments
-// the IEEE forms' extra instructions, not memory, set the time.  There a thread
+// eight neighbouring lanes, so a block's scale takes three shuffles.  Products
+// work on pairs.  With fp32 moments roots and quotients are IEEE's, which memory
+// hides (188 M elements with their norms 1075 us, 1077 with the hardware's
+// approximations; 9.4 M elements 57.3 and 56.3).  With 8-bit moments instructions
+// set the time, and the quotient of an update is approximate (2^-22 of it, a small
+// part of a weight).  There a thread
 // also has its next eight on their way into its own places in shared memory (no
 // thread waits for another, no register is held): few bytes an element leave
 // latency to set the time (48 M elements with their norms: 190 us without, 169
@@ -392,10 +389,18 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
           r.p[k] = roots(r.p[k]);
         } else {
           split(r.p[k], u, v);
-          r.p[k] = pair_of(sqrt_fast(u), sqrt_fast(v));
+          r.p[k] = pair_of(__fsqrt_rn(u), __fsqrt_rn(v));
         }
         split(fma2(r.p[k], iroot, eps), u, v);
-        w.p[k] = fma2(w.p[k], decay, mul2(down, mul2(m.p[k], pair_of(rcp_fast(u), rcp_fast(v)))));
+        uint64_t up;
+        if (kE4M3) {
+          up = mul2(m.p[k], pair_of(rcp_fast(u), rcp_fast(v)));
+        } else {
+          float a, b;
+          split(m.p[k], a, b);
+          up = pair_of(__fdiv_rn(a, u), __fdiv_rn(b, v));
+        }
+        w.p[k] = fma2(w.p[k], decay, mul2(down, up));
       }
       if (p.master != nullptr) store8(p.master + pos, w);
       *reinterpret_cast<uint4*>(pool + pos) = to_bf16(w);

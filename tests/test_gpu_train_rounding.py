@@ -97,3 +97,21 @@ def test_a_square_past_fp32_leaves_its_weight_and_a_tiny_one_counts_as_zero():
     assert abs(float(w1[q[128]]) - (float(w0[q[128]]) - 0.5)) <= 2.0 ** -20
     rest = np.setdiff1d(q[64:], [q[71], q[128]])
     assert np.array_equal(w1[rest], w0[rest])
+
+
+def test_fp32_update_of_a_first_gradient_is_its_sign():
+    """fp32 moments: m / (sqrt(v) + 0) is +-1 to the last bit, so weights of 0 move by the rate itself."""
+    s = Setup(22, 4096, 4096, [16], 4096, "f32", True)
+    ts, ids, err = B.TrainSet([s.t]), ids_of([0]), new_err()
+    B.lora_adamw_init(ts, ids, err=err)
+    q = np.concatenate(R.positions(s.pool, 0))
+    rng = np.random.default_rng(1)
+    g = np.zeros(s.own.size, dtype=np.float32)
+    g[q] = (np.exp(rng.uniform(np.log(1e-15), np.log(1e15), len(q))) * rng.choice([-1, 1], len(q))).astype(np.float32)
+    s.t.grad.copy_(torch.from_numpy(g))
+    s.t.master.zero_()
+    B.lora_adamw_step(ts, ids, B.adamw_hyper(1, lr=0.37, beta1=0.0, beta2=0.0, eps=0.0), err=err)
+    assert int(err) == 0
+    w = s.t.master.cpu().numpy()[q]
+    want = -np.sign(g[q]) * np.float32(0.37)
+    assert np.array_equal(w, want), "%d of %d" % ((w != want).sum(), len(q))

@@ -664,7 +664,8 @@ def _rows(t: Optional[torch.Tensor], n: int, dtype, what: str) -> int:
 
 @functools.lru_cache(maxsize=64)
 def _opts(kind, *values):
-    """A structure of options by reference: a training run passes the same few again and again."""
+    """A structure of options by reference: a training run passes the same few again and again.
+    Plain numbers only, which are their own key: a tensor's is its identity, not its value."""
     return ctypes.byref(kind(*values))
 
 
@@ -706,7 +707,8 @@ def lora_preference_loss(logits: torch.Tensor, labels: torch.Tensor, seq_indptr:
     p, ld, code, T, V = _logits(logits)
     n = int(loss.numel())
     f32 = torch.float32
-    opts = _opts(lora_pref_opts_t, kind, LORA_PREF_AVERAGE if average else 0, beta, label_smoothing, margin, grad_scale)
+    opts = _opts(lora_pref_opts_t, int(kind), LORA_PREF_AVERAGE if average else 0, float(beta), float(label_smoothing),
+                 float(margin), float(grad_scale))
     dp, ldd = _grad_of(logits, dlogits)
     _check(lib().lora_preference_loss(p, ld, code, _rows(labels, T, torch.int32, "labels"),
                                       _rows(ref_logp, T, f32, "ref_logp"),
@@ -726,7 +728,7 @@ def lora_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch
     dlogits may be the logits (the gradient takes their place) or None."""
     p, ld, code, T, V = _logits(logits)
     f32 = torch.float32
-    opts = _opts(lora_policy_opts_t, clip_low, clip_high, kl_coef, grad_scale)
+    opts = _opts(lora_policy_opts_t, float(clip_low), float(clip_high), float(kl_coef), float(grad_scale))
     dp, ldd = _grad_of(logits, dlogits)
     _check(lib().lora_policy_loss(p, ld, code, _rows(labels, T, torch.int32, "labels"),
                                   _rows(old_logp, T, f32, "old_logp"), _rows(ref_logp, T, f32, "ref_logp"),

@@ -1,0 +1,77 @@
+"""What the training calls of the binding pass to the library, without a GPU: the library is replaced by a
+recorder of its arguments, so nothing is launched whatever a test passes."""
+
+import ctypes
+
+import pytest
+import torch
+
+from segmented_gather_gemm_lora_gb300 import binding as B
+
+
+class Recorder:
+    """Stands for the library: every call succeeds and leaves its arguments."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return B.LORA_OK
+
+        return call
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    r = Recorder()
+    monkeypatch.setattr(B, "lib", lambda: r)
+    return r.calls
+
+
+def rows(T):
+    return torch.zeros(T, dtype=torch.int32), torch.zeros(T), torch.zeros(T)
+
+
+def options(args, kind):
+    """The structure of options among a call's arguments, as it is now."""
+    for a in args:
+        if hasattr(a, "_obj") and isinstance(a._obj, kind):
+            return a._obj
+    raise AssertionError("no options")
+
+
+def policy(**kw):
+    lab, f, g = rows(4)
+    x = torch.zeros(4, 8)
+    B.lora_policy_loss(x, lab, f, g, f.clone(), g.clone(), None, None, ref_logp=f, stream=0, **kw)
+
+
+def preference(**kw):
+    lab, f, g = rows(4)
+    B.lora_preference_loss(torch.zeros(4, 8), lab, torch.tensor([0, 2, 4], dtype=torch.int32), f[:1], None, None,
+                           torch.zeros(64, dtype=torch.uint8), stream=0, **kw)
+
+
+@pytest.mark.parametrize("name", ["clip_low", "clip_high", "kl_coef", "grad_scale"])
+def test_a_policy_option_held_in_a_tensor_is_read_at_each_call(calls, name):
+    value = torch.tensor(0.25, dtype=torch.float64)
+    for v in (0.25, 0.5, 0.125):
+        value.fill_(v)
+        policy(**{name: value})
+        assert getattr(options(calls[-1][1], B.lora_policy_opts_t), name) == v
+
+
+@pytest.mark.parametrize("name", ["beta", "label_smoothing", "margin", "grad_scale"])
+def test_a_preference_option_held_in_a_tensor_is_read_at_each_call(calls, name):
+    value = torch.tensor(0.25)
+    for v in (0.25, 0.5, 0.125):
+        value.fill_(v)
+        preference(**{name: value})
+        assert getattr(options(calls[-1][1], B.lora_pref_opts_t), name) == v
+    kind = torch.tensor(B.LORA_PREF_HINGE)
+    preference(kind=kind)
+    kind.fill_(B.LORA_PREF_IPO)
+    preference(kind=kind)
+    assert options(calls[-1][1], B.lora_pref_opts_t).kind == B.LORA_PREF_IPO

@@ -646,7 +646,11 @@ def _logits(t: torch.Tensor):
     ld, one = t.stride()
     if one != 1 and V > 1:
         raise ValueError("expected a 2-D row-major tensor with unit column stride")
-    return t.data_ptr(), max(ld, V), code, T, V  # a matrix of one row may have any stride there
+    if T <= 1:
+        ld = max(ld, V)  # the stride of a matrix of one row says nothing
+    elif ld < V:
+        raise ValueError("expected rows that do not overlap (a row stride of at least %d, got %d)" % (V, ld))
+    return t.data_ptr(), ld, code, T, V
 
 
 _LOGITS_CODE = {torch.bfloat16: LORA_LOGITS_BF16, torch.float32: LORA_LOGITS_F32}

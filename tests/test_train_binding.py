@@ -75,3 +75,31 @@ def test_a_preference_option_held_in_a_tensor_is_read_at_each_call(calls, name):
     kind.fill_(B.LORA_PREF_IPO)
     preference(kind=kind)
     assert options(calls[-1][1], B.lora_pref_opts_t).kind == B.LORA_PREF_IPO
+
+
+def strided(T, V, stride, dtype=torch.float32):
+    return torch.zeros(max(1, (T - 1) * stride + V), dtype=dtype).as_strided((T, V), (stride, 1))
+
+
+def loss_calls(x, d):
+    T = x.shape[0]
+    lab, f, g = rows(T)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    out = [lambda: B.lora_policy_loss(x, lab, f, g, f.clone(), g.clone(), None, d, stream=0),
+           lambda: B.lora_preference_loss(x, lab, torch.tensor([0, 1, T], dtype=torch.int32), f[:1], None, d, ws, stream=0)]
+    return out + ([lambda: B.lora_token_logprobs(x, lab, f, stream=0)] if d is None else [])
+
+
+@pytest.mark.parametrize("stride", [0, 1, 8, 15])
+def test_rows_closer_than_their_length_are_refused(calls, stride):
+    """Broadcast and overlapping rows: their buffer is shorter than T rows of V."""
+    for call in loss_calls(strided(4, 16, stride), None) + loss_calls(torch.zeros(4, 16), strided(4, 16, stride)):
+        with pytest.raises(ValueError):
+            call()
+    assert not calls
+
+
+def test_the_stride_of_rows_reaches_the_library(calls):
+    for T, V, stride, ld in [(4, 16, 16, 16), (4, 16, 19, 19), (1, 16, 0, 16), (1, 16, 5, 16), (1, 16, 40, 40), (0, 16, 0, 16), (3, 1, 1, 1)]:
+        B.lora_token_logprobs(strided(T, V, stride), *rows(T)[:2], stream=0)
+        assert calls[-1][1][1] == ld

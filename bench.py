@@ -11,6 +11,8 @@ A step is one pass of the whole path over one batch of one configuration:
   stages its adapters while the call ahead of it finishes);
 * backward (with --workload backward, and under per_config): lora_segments_build +
   lora_sgmv_backward on the prefill batch;
+* base_fused (with --workload base_fused, and under per_config; one GPU only):
+  lora_segments_build + lora_base_apply on the prefill batch;
 * mixed13b (the headline, the largest configuration that fits one GPU): one forward of
   the 13B-shaped mixed batch, one segment build and 40 layers x 7 projections, in four
   grouped calls per layer (lora_apply_multi for q, k, v on their shared input and for
@@ -945,7 +947,10 @@ def run_base_line(steps, warmup, soak_seconds, world, rank, local):
     """The base projection with the adapter term in its epilogue on the prefill batch: a
     step is lora_segments_build + lora_base_apply (y = x W0^T + s_i (x A_i^T) B_i, y written
     once) with a random 4096 x 4096 W0; timed beside cuBLAS's x W0^T followed by
-    lora_apply, the unfused way to the same y.  Two input sets rotate (each larger than L2)."""
+    lora_apply, the unfused way to the same y.  Two input sets rotate (each larger than L2).
+    One GPU only: the kernel loads with cluster multicast."""
+    if world > 1:
+        raise SystemExit("the base_fused workload runs on one GPU (its kernel loads with cluster multicast)")
     import torch
 
     from segmented_gather_gemm_lora_gb300 import binding as B
@@ -1311,7 +1316,8 @@ def main(argv=None):
             per_config[name] = config_line(name, args, world, rank, local, OTHER_STEPS[name])
         per_config["backward"] = run_backward_line(BACKWARD_STEPS, args.warmup, args.soak_seconds, world, rank,
                                                    local)
-        per_config["base_fused"] = run_base_line(BASE_STEPS, args.warmup, args.soak_seconds, world, rank, local)
+        if world == 1:
+            per_config["base_fused"] = run_base_line(BASE_STEPS, args.warmup, args.soak_seconds, world, rank, local)
         if rank == 0 and world == 1 and args.cpu_seconds > 0:
             for k in ("backward", "base_fused"):
                 per_config[k]["cpu_baseline"] = cpu_baseline_line(k, args.cpu_seconds)

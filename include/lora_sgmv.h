@@ -305,7 +305,8 @@ lora_status_t lora_sgmv_backward(const void* x, int64_t ldx, const void* dy, int
  * ordered on one stream.
  * y must not overlap x, w0 or the segment buffer.  The base product runs on
  * the tensor cores through TMA tensor maps: LORA_ERR_UNSUPPORTED when the
- * driver offers no tensor-map encoder.
+ * driver offers no tensor-map encoder.  Its loads of w0 are cluster multicasts:
+ * for processes that run on one GPU.
  */
 lora_status_t lora_base_apply(const void* x, int64_t ldx, const void* w0, int64_t ldw, void* y, int64_t ldy,
                               const int32_t* token_adapter, const lora_segments_t* seg,

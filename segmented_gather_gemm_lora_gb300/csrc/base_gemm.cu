@@ -19,7 +19,8 @@
 // TMA box of x (128 x 64) and one half (128 x 64) of the W0 box the two tiles
 // share, multicast into both CTAs, all with the 128-byte swizzle, into a
 // 4-stage ring: each CTA then reads two thirds of the bytes a CTA loading its
-// own W0 box would.  A stage is free again once both CTAs' MMAs have read it
+// own W0 box would.  (The multicast stays within this GPU's own memory, and the
+// call is for processes that run on one GPU.)  A stage is free again once both CTAs' MMAs have read it
 // (each MMA warp's commit arrives in both CTAs).  Warp 1 issues tcgen05.mma
 // (M = 128, N = 256, bf16, fp32 accumulator in tensor memory), alternating two
 // accumulators so that a tile's epilogue overlaps the next tile's MMAs.

@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "smem_limit.h"
 
 namespace lora {
 
@@ -70,33 +71,16 @@ size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 }  // namespace
 
 cudaError_t ensure_smem_attr(const void* func, size_t bytes) {
-  // A few kernels, each raised once per device to its largest request.
-  constexpr int kSlots = 24;
-  static std::atomic<size_t> cache[kSlots][kMaxDevices];
-  static std::atomic<const void*> funcs[kSlots];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  int slot = -1;
-  for (int i = 0; i < kSlots; ++i) {
-    const void* f = funcs[i].load();
-    if (f == func) { slot = i; break; }
-    if (f == nullptr) {
-      const void* expected = nullptr;
-      if (funcs[i].compare_exchange_strong(expected, func) || expected == func) { slot = i; break; }
-    }
-  }
-  if (slot >= 0 && cache[slot][dev].load() >= bytes) return cudaSuccess;
   // Raised even below 48 KB: the default limit covers dynamic and static shared
   // memory together, so a kernel with static shared memory of its own needs the
   // attribute for a dynamic size just under 48 KB too.
-  e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess && slot >= 0) {
-    size_t cur = cache[slot][dev].load();
-    while (cur < bytes && !cache[slot][dev].compare_exchange_weak(cur, bytes)) {}
-  }
-  return e;
+  static SmemLimits<64, kMaxDevices> limits;
+  auto set = [&] { return (int)cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); };
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return (cudaError_t)set();
+  return (cudaError_t)limits.raise(func, dev, bytes, set);
 }
 
 std::atomic<uint64_t> g_launches{0};

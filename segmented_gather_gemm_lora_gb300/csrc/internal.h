@@ -10,8 +10,8 @@ namespace lora {
 
 struct DevView;
 
-// Raise a kernel's dynamic shared-memory limit on the current device (once per
-// device and size).
+// Raise a kernel's dynamic shared-memory limit on the current device to at least
+// `bytes` (once per device and size), from any thread.
 cudaError_t ensure_smem_attr(const void* func, size_t bytes);
 
 // Launch `func` (whose only parameter is the struct at `args`) with a cluster

@@ -188,14 +188,18 @@ typedef struct {
 lora_status_t lora_adamw_init(const lora_train_proj_t* projs, int32_t n_proj, int32_t state,
                               const int32_t* ids, int32_t n_ids, int32_t* dev_err, lora_stream_t stream);
 
-/** Bytes of lora_grad_sumsq's workspace (16-byte aligned; contents do not matter); 0 on bad arguments. */
+/**
+ * Bytes of lora_grad_sumsq's workspace (16-byte aligned; contents do not matter); 0 on bad arguments.
+ * One made for n_ids adapters serves any shorter list over the same projections.
+ */
 size_t lora_grad_sumsq_workspace_bytes(const lora_train_proj_t* projs, int32_t n_proj, int32_t n_ids);
 
 /**
  * sumsq[i] = sum of grad^2 over adapter i's elements in all the projections,
  * for the listed ids (device fp32 [n_adapters]; others are not written); with
  * accumulate != 0 it is added to what sumsq[i] holds, so that a norm can span
- * several calls.  Squares are fp32, summed in a fixed order.
+ * several calls.  Squares are fp32, summed in an order that the projections fix:
+ * an adapter's sum does not depend on what is listed beside it.
  */
 lora_status_t lora_grad_sumsq(const lora_train_proj_t* projs, int32_t n_proj, const int32_t* ids,
                               int32_t n_ids, int32_t accumulate, float* sumsq, void* workspace,

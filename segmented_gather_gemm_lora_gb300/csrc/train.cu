@@ -21,7 +21,8 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kGroup = 8;                     // consecutive elements a thread takes: one page each (d % 8 == 0, pages >= 64)
 constexpr int kSpan = kThreads * kGroup;      // elements the CTA takes at once
-constexpr int kSumGroups = 4;                 // spans of the sum that are read together
+constexpr int kSumGroups = 4;                 // spans of the sum that are read together and share a slot of its workspace
+constexpr int kSumMost = 4;                   // slots of a chunk of the sum at most
 constexpr int kMaxProj = 16;                  // projections of one launch (kernel parameters below 4 KB)
 constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
 constexpr int kBlockLanes = LORA_ADAMW_BLOCK / kGroup;  // lanes that share a block's scale
@@ -36,6 +37,9 @@ struct DevProj {
   uint16_t* r_scale;
   int chunk0;   // first chunk of the projection in the launch
   int chunks_a;  // chunks of A at max_rank
+  int slot0;    // the same of the sum's slots
+  int slots_a;
+  int slots_b;
 };
 
 struct TrainArgs {
@@ -44,7 +48,7 @@ struct TrainArgs {
   const int32_t* ids;
   const lora_adamw_hyper_t* hyper;
   const float* sumsq;
-  float* partial;       // [n_ids][partial_stride]
+  float* partial;       // the sum's slots [n_ids][partial_stride]; the launch's begin at partial0
   int partial_stride;
   int partial0;
   int zero_grad;
@@ -56,8 +60,10 @@ static_assert(sizeof(TrainArgs) <= 4096, "kernel parameters");
 
 // A chunk's place: which adapter, projection and matrix, and its elements.
 struct Place {
+  int entry;  // of the list
   int ad;
   int g;
+  bool is_b;
   long long e0, size;  // first element; elements of the matrix (0: of no good adapter)
   long long slot0;     // page-list slot of the matrix
   bool lead;           // the CTA that reports the adapter's errors
@@ -71,20 +77,21 @@ __device__ __forceinline__ Place find_place(const TrainArgs& a) {
   Place q;
   const int chunk = a.spans * kSpan;
   const int e = a.reverse ? gridDim.y - 1 - blockIdx.y : blockIdx.y, c = a.reverse ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  q.entry = e;
   q.ad = a.ids[e];
   q.g = 0;
   while (q.g + 1 < a.n_proj && c >= a.p[q.g + 1].chunk0) ++q.g;
   const DevProj& p = a.p[q.g];
   const int cg = c - p.chunk0;
   q.lead = cg == 0;
-  const bool is_b = cg >= p.chunks_a;
-  q.e0 = (long long)(is_b ? cg - p.chunks_a : cg) * chunk;
+  q.is_b = cg >= p.chunks_a;
+  q.e0 = (long long)(q.is_b ? cg - p.chunks_a : cg) * chunk;
   const lora_adapter_desc_t d = adapter_desc(p.v, q.ad);
   q.twice = 0;
   for (int k = threadIdx.x; k < e; k += blockDim.x) q.twice |= a.ids[k] == q.ad;
-  q.slot0 = is_b ? d.b_page0 : d.a_page0;
+  q.slot0 = q.is_b ? d.b_page0 : d.a_page0;
   q.bad = q.ad < 0 || q.ad >= p.v.n_adapters ? LORA_DERR_BAD_ADAPTER : d.rank < 1 || d.rank > p.v.max_rank ? LORA_DERR_BAD_RANK : 0;
-  q.size = q.bad ? 0 : (long long)d.rank * (is_b ? p.v.d_out : p.v.d_in);
+  q.size = q.bad ? 0 : (long long)d.rank * (q.is_b ? p.v.d_out : p.v.d_in);
   return q;
 }
 
@@ -466,52 +473,55 @@ __global__ void __launch_bounds__(kThreads) adamw_init_kernel(const __grid_const
   }
 }
 
-__device__ __forceinline__ float block_sum(float x, float* sh) {
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
-  __syncthreads();
-  float t = 0.f;
-#pragma unroll
-  for (int k = 0; k < kThreads / 32; ++k) t += sh[k];
-  return t;
-}
-
-// Sum of squares of one chunk of gradients (4 bytes an element, read once) into
-// its own slot of the workspace: the order of the sum is the same in every run.
+// Sum of squares of one chunk of gradients (4 bytes an element, read once) into its
+// slots of the workspace, one for each kSumGroups spans however long the chunk is: an
+// adapter's sum has one order, whatever is listed beside it.
 __global__ void __launch_bounds__(kThreads) sumsq_kernel(const __grid_constant__ TrainArgs a) {
-  __shared__ float sh[kThreads / 32];
+  __shared__ float sh[kSumMost][kThreads];
   pdl_wait_then_release();
   Place q = find_place(a);
-  float s = 0.f;
-  if (agree(a, q)) {
-    const DevProj& p = a.p[q.g];
-    for (int j0 = 0; j0 < a.spans; j0 += kSumGroups) {
-      long long pos[kSumGroups];  // all first, then all loads: a thread has its 128 bytes in flight
-#pragma unroll
-      for (int j = 0; j < kSumGroups; ++j) {
-        const long long e = q.e0 + (long long)((j0 + j) * kThreads + threadIdx.x) * kGroup;
-        pos[j] = e < q.size ? pool_pos(p.v, q, e) : -2;
-      }
-      Eight g[kSumGroups] = {};
-#pragma unroll
-      for (int j = 0; j < kSumGroups; ++j)
-        if (pos[j] >= 0) g[j] = read_f32(p.grad + pos[j]);
-      uint64_t two = pair_of(0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < kSumGroups; ++j) {
-        if (pos[j] == -1) report(a.err, LORA_DERR_BAD_PAGE);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) two = fma2(g[j].p[k], g[j].p[k], two);
-      }
-      float u, v;
-      split(two, u, v);
-      s += u + v;
-    }
+  const DevProj& p = a.p[q.g];
+  const int groups = a.spans / kSumGroups, slot = (int)(q.e0 / (kSumGroups * kSpan));
+  float* const out = a.partial + (long long)q.entry * a.partial_stride + a.partial0 + p.slot0 + (q.is_b ? p.slots_a : 0) + slot;
+  const int slots = min(groups, (q.is_b ? p.slots_b : p.slots_a) - slot);
+  if (!agree(a, q)) {
+    if ((int)threadIdx.x < slots) out[threadIdx.x] = 0.f;
+    return;
   }
-  const float t = block_sum(s, sh);
-  if (threadIdx.x == 0) a.partial[(long long)blockIdx.y * a.partial_stride + a.partial0 + blockIdx.x] = t;
+  for (int k = 0; k < groups; ++k) {
+    long long pos[kSumGroups];  // all first, then all loads: a thread has its 128 bytes in flight
+#pragma unroll
+    for (int j = 0; j < kSumGroups; ++j) {
+      const long long e = q.e0 + (long long)((k * kSumGroups + j) * kThreads + threadIdx.x) * kGroup;
+      pos[j] = e < q.size ? pool_pos(p.v, q, e) : -2;
+    }
+    Eight g[kSumGroups] = {};
+#pragma unroll
+    for (int j = 0; j < kSumGroups; ++j)
+      if (pos[j] >= 0) g[j] = read_f32(p.grad + pos[j]);
+    uint64_t two = pair_of(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kSumGroups; ++j) {
+      if (pos[j] == -1) report(a.err, LORA_DERR_BAD_PAGE);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) two = fma2(g[j].p[i], g[j].p[i], two);
+    }
+    float u, v;
+    split(two, u, v);
+    sh[k][threadIdx.x] = u + v;
+  }
+  __syncthreads();
+  // a warp a slot
+  const int k = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (k >= slots) return;
+  float t = 0.f;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) t += sh[k][32 * w + lane];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+  if (lane == 0) out[k] = t;
 }
+static_assert(kSumMost <= kThreads / 32, "a warp a slot");
 
 struct FinishArgs {
   const int32_t* ids;
@@ -522,7 +532,7 @@ struct FinishArgs {
   float* sumsq;
 };
 
-// One CTA an adapter: its chunks' sums, kept with what their rounding leaves out,
+// One CTA an adapter: its slots, kept with what their rounding leaves out,
 // in a fixed order.
 __global__ void __launch_bounds__(kThreads) sumsq_finish_kernel(const __grid_constant__ FinishArgs a) {
   __shared__ Pair32 sh[kThreads / 32];
@@ -590,9 +600,10 @@ lora_status_t check_state(const lora_train_proj_t* projs, int n_proj, int state)
   return LORA_OK;
 }
 
-// Fill the projections [g0, g0 + n) of a launch; the number of its chunks.
-long long fill(TrainArgs* a, const lora_train_proj_t* projs, int g0, int n, int chunk) {
-  long long at = 0;
+// Fill the projections [g0, g0 + n) of a launch; the number of its chunks, and in
+// *slots that of the sum's slots.
+long long fill(TrainArgs* a, const lora_train_proj_t* projs, int g0, int n, int chunk, int* slots) {
+  long long at = 0, slot = 0;
   a->n_proj = n;
   for (int k = 0; k < n; ++k) {
     const lora_train_proj_t& s = projs[g0 + k];
@@ -607,8 +618,13 @@ long long fill(TrainArgs* a, const lora_train_proj_t* projs, int g0, int n, int 
     d.chunk0 = (int)at;
     d.chunks_a = (int)chunks_of(s.view.max_rank, s.view.d_in, chunk);
     at += d.chunks_a + chunks_of(s.view.max_rank, s.view.d_out, chunk);
-    if (at > 0x7fffffffLL) return -1;
+    d.slot0 = (int)slot;
+    d.slots_a = (int)chunks_of(s.view.max_rank, s.view.d_in, kSumGroups * kSpan);
+    d.slots_b = (int)chunks_of(s.view.max_rank, s.view.d_out, kSumGroups * kSpan);
+    slot += d.slots_a + d.slots_b;
+    if (at > 0x7fffffffLL || slot > 0x7fffffffLL) return -1;
   }
+  *slots = (int)slot;
   return at;
 }
 
@@ -616,11 +632,12 @@ lora_status_t launch_over(const void* func, TrainArgs* a, const lora_train_proj_
                           cudaStream_t s) {
   a->spans = spans;
   for (int g0 = 0; g0 < n_proj; g0 += kMaxProj) {
-    const long long chunks = fill(a, projs, g0, std::min(kMaxProj, n_proj - g0), spans * kSpan);
+    int slots = 0;
+    const long long chunks = fill(a, projs, g0, std::min(kMaxProj, n_proj - g0), spans * kSpan, &slots);
     if (chunks < 0) return LORA_ERR_UNSUPPORTED;
     if (launch_pdl(func, dim3((unsigned)chunks, (unsigned)n_ids), dim3(kThreads), 0, s, 0, a) != cudaSuccess)
       return LORA_ERR_CUDA;
-    a->partial0 += (int)chunks;
+    a->partial0 += slots;
   }
   return LORA_OK;
 }
@@ -630,8 +647,8 @@ lora_status_t launch_over(const void* func, TrainArgs* a, const lora_train_proj_
 int sum_spans(const lora_train_proj_t* projs, int n_proj, int n_ids) {
   long long chunks = 0;
   for (int g = 0; g < n_proj; ++g)
-    chunks += chunks_of(projs[g].view.max_rank, (long long)projs[g].view.d_in + projs[g].view.d_out, 4 * kSumGroups * kSpan);
-  return chunks * n_ids >= 32LL * sm_count() ? 4 * kSumGroups : kSumGroups;
+    chunks += chunks_of(projs[g].view.max_rank, (long long)projs[g].view.d_in + projs[g].view.d_out, kSumMost * kSumGroups * kSpan);
+  return chunks * n_ids >= 32LL * sm_count() ? kSumMost * kSumGroups : kSumGroups;
 }
 
 // Spans of a chunk of the step: four, which spreads a CTA's start over 8192 elements, once
@@ -643,12 +660,14 @@ int step_spans(const lora_train_proj_t* projs, int n_proj, int n_ids) {
   return chunks * n_ids >= 16LL * sm_count() ? 4 : 1;
 }
 
-// Chunks of all projections in the sum; -1 above what a launch can count.
-long long sum_chunks(const lora_train_proj_t* projs, int n_proj, int spans) {
+// Slots of an adapter in the sum's workspace, a function of the projections alone (so
+// that a workspace made for many adapters serves fewer); -1 above what a launch can
+// count.
+long long sum_slots(const lora_train_proj_t* projs, int n_proj) {
   long long at = 0;
   for (int g = 0; g < n_proj; ++g)
-    at += chunks_of(projs[g].view.max_rank, projs[g].view.d_in, spans * kSpan) +
-          chunks_of(projs[g].view.max_rank, projs[g].view.d_out, spans * kSpan);
+    at += chunks_of(projs[g].view.max_rank, projs[g].view.d_in, kSumGroups * kSpan) +
+          chunks_of(projs[g].view.max_rank, projs[g].view.d_out, kSumGroups * kSpan);
   return at > 0x7fffffffLL ? -1 : at;
 }
 
@@ -676,8 +695,7 @@ size_t lora_grad_sumsq_workspace_bytes(const lora_train_proj_t* projs, int32_t n
   if (projs == nullptr || n_proj < 1 || n_ids < 0 || n_ids > LORA_MAX_ADAPTERS) return 0;
   for (int g = 0; g < n_proj; ++g)
     if (validate_view(&projs[g].view) != LORA_OK) return 0;
-  const int spans = sum_spans(projs, n_proj, n_ids);
-  const long long n = sum_chunks(projs, n_proj, spans);
+  const long long n = sum_slots(projs, n_proj);
   return n < 0 ? 0 : (size_t)(((long long)n_ids * n * 4 + 16) / 16 * 16);
 }
 
@@ -689,8 +707,7 @@ lora_status_t lora_grad_sumsq(const lora_train_proj_t* projs, int32_t n_proj, co
   if (sumsq == nullptr || (reinterpret_cast<uintptr_t>(sumsq) & 3u) != 0) return LORA_ERR_INVALID_ARG;
   if (n_ids == 0) return LORA_OK;
   if (workspace == nullptr || !aligned16(workspace)) return LORA_ERR_INVALID_ARG;
-  const int spans = sum_spans(projs, n_proj, n_ids);
-  const long long n = sum_chunks(projs, n_proj, spans);
+  const long long n = sum_slots(projs, n_proj);
   if (n < 0) return LORA_ERR_UNSUPPORTED;
   if (workspace_bytes < lora_grad_sumsq_workspace_bytes(projs, n_proj, n_ids)) return LORA_ERR_WORKSPACE;
   TrainArgs a;
@@ -699,7 +716,8 @@ lora_status_t lora_grad_sumsq(const lora_train_proj_t* projs, int32_t n_proj, co
   a.err = dev_err;
   a.partial = static_cast<float*>(workspace);
   a.partial_stride = (int)n;
-  st = launch_over((const void*)sumsq_kernel, &a, projs, n_proj, n_ids, spans, (cudaStream_t)stream);
+  st = launch_over((const void*)sumsq_kernel, &a, projs, n_proj, n_ids, sum_spans(projs, n_proj, n_ids),
+                   (cudaStream_t)stream);
   if (st != LORA_OK) return st;
   FinishArgs f;
   memset(&f, 0, sizeof(f));

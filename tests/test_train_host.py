@@ -237,3 +237,20 @@ def test_hyper_holds_each_adapters_settings():
     assert h.view(torch.int32)[:, 0].tolist() == [1, 5, 9]
     one = B.lora_adamw_hyper_t.from_buffer_copy(h.numpy().tobytes()[32:64])
     assert one.step == 5 and abs(one.lr - 2e-3) < 1e-9 and one.max_norm == 1.5 and one.grad_scale == 1.0
+
+
+def sized_proj(d_in=4096, d_out=4096, max_rank=64, **kw):
+    return fake_proj(view=fake_view(d_in=d_in, d_out=d_out, max_rank=max_rank), **kw)
+
+
+@pytest.mark.parametrize("shapes,max_rank", [([(4096, 4096)] * 4 + [(4096, 11008)] * 2 + [(11008, 4096)], 64),
+                                             ([(2048, 2048)], 8), ([(8, 8)], 1), ([(5120, 13824)] * 20, 16)])
+def test_a_norm_workspace_for_many_adapters_serves_fewer(shapes, max_rank):
+    """The size grows with the list, and a byte less than a list's own size is refused."""
+    L = B.lib()
+    arr = (B.lora_train_proj_t * len(shapes))(*(sized_proj(a, b, max_rank) for a, b in shapes))
+    need = [L.lora_grad_sumsq_workspace_bytes(arr, len(shapes), n) for n in range(B.LORA_MAX_ADAPTERS + 1)]
+    assert all(0 < a <= b for a, b in zip(need, need[1:]))
+    for n in (1, 2, 5, 15, 16, 17, 31, 32, 200, 1000):
+        status = L.lora_grad_sumsq(arr, len(shapes), vp(0x1000), n, 0, vp(0x2000), vp(0x3000), need[n] - 1, None, None)
+        assert status == B.LORA_ERR_WORKSPACE

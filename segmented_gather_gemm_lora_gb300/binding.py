@@ -752,15 +752,18 @@ class TrainProj:
                  master: Optional[torch.Tensor] = None, m_scale: Optional[torch.Tensor] = None,
                  v_scale: Optional[torch.Tensor] = None):
         n = view.c.n_pages * view.c.page_elems
+        if (m_scale is None) != (v_scale is None):
+            raise ValueError("m_scale, v_scale: expected both (8-bit moments) or none")
         self.state = LORA_STATE_F32 if m_scale is None else LORA_STATE_E4M3
-        size = 4 if self.state == LORA_STATE_F32 else 1
-        for name, t, count, width in (("grad", grad, n, 4), ("m", m, n, size), ("v", v, n, size),
-                                      ("master", master, n, 4), ("m_scale", m_scale, n // LORA_ADAMW_BLOCK, 2),
-                                      ("v_scale", v_scale, n // LORA_ADAMW_BLOCK, 2)):
+        f32, bf16 = (torch.float32,), (torch.bfloat16,)
+        moment = f32 if self.state == LORA_STATE_F32 else (torch.float8_e4m3fn, torch.uint8)
+        for name, t, count, types in (("grad", grad, n, f32), ("m", m, n, moment), ("v", v, n, moment),
+                                      ("master", master, n, f32), ("m_scale", m_scale, n // LORA_ADAMW_BLOCK, bf16),
+                                      ("v_scale", v_scale, n // LORA_ADAMW_BLOCK, bf16)):
             if t is None:
                 continue
-            if t.numel() < count or t.element_size() != width or not t.is_contiguous():
-                raise ValueError("%s: expected %d contiguous elements of %d bytes" % (name, count, width))
+            if t.numel() < count or t.dtype not in types or not t.is_contiguous():
+                raise ValueError("%s: expected %d contiguous elements of %s" % (name, count, " or ".join(map(str, types))))
         self.view, self.grad, self.m, self.v = view, grad, m, v
         self.master, self.m_scale, self.v_scale = master, m_scale, v_scale
         self.c = lora_train_proj_t(view.c, *(_addr(t) or None for t in (grad, master, m, v, m_scale, v_scale)))

@@ -103,3 +103,43 @@ def test_the_stride_of_rows_reaches_the_library(calls):
     for T, V, stride, ld in [(4, 16, 16, 16), (4, 16, 19, 19), (1, 16, 0, 16), (1, 16, 5, 16), (1, 16, 40, 40), (0, 16, 0, 16), (3, 1, 1, 1)]:
         B.lora_token_logprobs(strided(T, V, stride), *rows(T)[:2], stream=0)
         assert calls[-1][1][1] == ld
+
+
+def proj_arrays(e4m3=False, n=512):
+    """A view's worth of state arrays for TrainProj, by name."""
+    a = dict(grad=torch.zeros(n), m=torch.zeros(n), v=torch.zeros(n), master=torch.zeros(n))
+    if e4m3:
+        a.update(m=torch.zeros(n, dtype=torch.uint8), v=torch.zeros(n, dtype=torch.uint8).view(torch.float8_e4m3fn),
+                 m_scale=torch.zeros(n // 64, dtype=torch.bfloat16), v_scale=torch.zeros(n // 64, dtype=torch.bfloat16))
+    return a
+
+
+def view(n=512):
+    return B.PoolView(torch.zeros(n // 64, 64, dtype=torch.bfloat16), torch.zeros(8, dtype=torch.int32),
+                      torch.zeros(2, 4, dtype=torch.int32), 64, 4, 64, 64)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_state_arrays_of_another_type_are_refused(e4m3):
+    good = proj_arrays(e4m3)
+    assert B.TrainProj(view(), **good).state == (B.LORA_STATE_E4M3 if e4m3 else B.LORA_STATE_F32)
+    assert B.TrainProj(view(), **dict(good, master=None)).c.master is None
+    wrong = {"grad": (torch.int32,), "master": (torch.int32,), "m": (torch.int8, torch.float8_e5m2) if e4m3 else (torch.int32,),
+             "m_scale": (torch.float16, torch.int16) if e4m3 else ()}
+    wrong["v"], wrong["v_scale"] = wrong["m"], wrong["m_scale"]
+    for name, types in wrong.items():
+        for t in types:
+            with pytest.raises(ValueError, match=name):
+                B.TrainProj(view(), **dict(good, **{name: good[name].view(t)}))
+    for name in good:
+        with pytest.raises(ValueError, match=name):  # short, and not contiguous
+            B.TrainProj(view(), **dict(good, **{name: good[name][:-1]}))
+        with pytest.raises(ValueError, match=name):
+            B.TrainProj(view(), **dict(good, **{name: torch.empty(2 * good[name].numel(), dtype=good[name].dtype)[::2]}))
+
+
+def test_both_scales_or_none():
+    a = proj_arrays(True)
+    for name in ("m_scale", "v_scale"):
+        with pytest.raises(ValueError, match="scale"):
+            B.TrainProj(view(), **dict(a, **{name: None}))

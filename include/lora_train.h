@@ -17,7 +17,8 @@
  * argument errors found on the host are returned before anything is launched,
  * and what only the device can see is OR-ed into *dev_err (may be NULL).
  * Calls can be captured in CUDA graphs.  Results do not depend on timing: every
- * sum has a fixed order (which depends on where a row's 16-byte boundaries lie).
+ * sum has a fixed order (a row's depends on the call, on T and V and on where its
+ * 16-byte boundaries lie).
  * A bounded wait inside a kernel that ran out sets LORA_DERR_TIMEOUT; the rows it
  * concerned are left as they were.
  */
@@ -122,6 +123,9 @@ typedef struct {
  * old_logp, advantage: device fp32 [T]; ref_logp (NULL only if kl_coef = 0) and
  * weight (NULL: 1) likewise.  A row of weight 0 has loss 0 and a zero gradient
  * row, whatever its ratio.  logp, loss: device fp32 [T]; kl: fp32 [T] or NULL.
+ * logp is lora_token_logprobs's but for the order of the row's sum (the same bits
+ * up to V = 128 vectors of 16 bytes), so the first step on a policy's own samples
+ * has ratios of 1 within its rounding.
  */
 lora_status_t lora_policy_loss(const void* logits, int64_t ld, int32_t dtype, const int32_t* labels,
                                const float* old_logp, const float* ref_logp, const float* advantage,

@@ -33,7 +33,6 @@ constexpr int kUnroll = 4;    // vectors a thread takes at once
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;    // log2 e to fp32 and what that leaves (the rounding
 constexpr float kLog2eLo = 1.9259629911267e-8f;  // has one sign in every row: sums of logp gather it)
-constexpr float kLn2 = 0.6931471805599453f;
 #define INF_F __int_as_float(0x7f800000)
 
 __device__ __forceinline__ float ex2(float x) {
@@ -399,14 +398,16 @@ __device__ __forceinline__ int row_label(const RowArgs& a, int t, bool lead) {
 // Nothing of the row is visible (a NaN among the masked entries is).
 __device__ __forceinline__ bool empty(const Sum& t) { return t.m == -INF_F && t.s == 0.f; }
 
-__device__ __forceinline__ float label_logp(float x, const Sum& t) {
-  return empty(t) ? -INF_F : (x - base_of(t.m)) - logf(t.s);
+// The same in every call: a policy that has not moved has ratio 1.
+__device__ __forceinline__ float label_logp(float x, const Sum& t, float logs) {
+  return empty(t) ? -INF_F : (x - base_of(t.m)) - logs;
 }
 
 // What a counted row leaves besides its gradient.
 __device__ __forceinline__ void put_sum(const RowArgs& a, int t, float x, const Sum& r) {
-  a.logp[t] = label_logp(x, r);
-  if (a.lse != nullptr) a.lse[t] = base_of(r.m) + logf(r.s);
+  const float logs = logf(r.s);
+  a.logp[t] = label_logp(x, r, logs);
+  if (a.lse != nullptr) a.lse[t] = base_of(r.m) + logs;
   if (a.top != nullptr) {
     a.top[t] = empty(r) ? r.m : base_of(r.m);
     a.log2s[t] = log2f(r.s);
@@ -435,8 +436,8 @@ __device__ __forceinline__ PolicyRow policy_row(const RowArgs& a, int t, float x
 // The policy loss of a row whose sum is r, written where `lead`; its gradient's
 // coefficient.  (Every thread works it out: cheaper than another barrier.)
 __device__ __forceinline__ Grad policy_grad(const RowArgs& a, int t, int label, const PolicyRow& p, const Sum& r, bool lead) {
-  const float l2 = log2f(r.s);
-  const float lp = empty(r) ? -INF_F : fmaf(l2, -kLn2, p.x - base_of(r.m)), q = expf(lp - p.old);
+  const float logs = logf(r.s), l2 = fmaf(logs, kLog2e, logs * kLog2eLo);
+  const float lp = label_logp(p.x, r, logs), q = expf(lp - p.old);
   // comparisons that a NaN fails leave it in the ratio and the ratio open
   const float low = 1.f - a.opt.clip_low, high = 1.f + a.opt.clip_high;
   const float free_ = q * p.adv, held = (q < low ? low : q > high ? high : q) * p.adv;

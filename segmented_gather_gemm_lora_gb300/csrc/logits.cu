@@ -960,6 +960,11 @@ lora_status_t check_grad(const void* logits, long long ld, int dtype, const void
   const long long b = dtype == LORA_LOGITS_BF16 ? 2 : 4;
   if (ldd < V || ldd > (1LL << 40) / T || !aligned_to(d, b)) return LORA_ERR_INVALID_ARG;
   if (d == logits && ldd == ld) return LORA_OK;
+  if (ldd == ld) {  // rows that take turns (halves of one buffer) do not overlap either
+    const long long step = ld * b, off = (long long)(reinterpret_cast<uintptr_t>(d) - reinterpret_cast<uintptr_t>(logits)) % step;
+    const long long at = off < 0 ? off + step : off;
+    if (at >= V * b && at <= step - V * b) return LORA_OK;
+  }
   const long long rows = T - 1;
   return overlap(logits, (rows * ld + V) * b, d, (rows * ldd + V) * b) ? LORA_ERR_INVALID_ARG : LORA_OK;
 }

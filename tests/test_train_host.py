@@ -254,3 +254,18 @@ def test_a_norm_workspace_for_many_adapters_serves_fewer(shapes, max_rank):
     for n in (1, 2, 5, 15, 16, 17, 31, 32, 200, 1000):
         status = L.lora_grad_sumsq(arr, len(shapes), vp(0x1000), n, 0, vp(0x2000), vp(0x3000), need[n] - 1, None, None)
         assert status == B.LORA_ERR_WORKSPACE
+
+
+def test_gradient_rows_between_the_logits_rows_are_accepted():
+    """Halves of one buffer whose rows take turns do not overlap; shifted into each other they do."""
+    big = dict(ld=256, ldd=256, ws=0x5000, wsb=16, T=10, V=100)  # stops at the workspace, after the checks of the rows
+    base = 0x10000000
+    for shift in (100, 128, 156):
+        assert call_preference(**big, d=base + 2 * shift) == B.LORA_ERR_WORKSPACE
+        assert call_preference(**big, d=base - 2 * shift) == B.LORA_ERR_WORKSPACE
+    for shift in (1, 99, 157, 255, 256, 256 + 99, 9 * 256 - 1):
+        assert call_preference(**big, d=base + 2 * shift) == B.LORA_ERR_INVALID_ARG
+        assert call_preference(**big, d=base - 2 * shift) == B.LORA_ERR_INVALID_ARG
+    # other strides: their ranges must not meet
+    assert call_preference(**dict(big, ldd=300), d=base + 2 * 128) == B.LORA_ERR_INVALID_ARG
+    assert call_preference(**dict(big, ldd=300), d=base + 2 * 2404) == B.LORA_ERR_WORKSPACE

@@ -269,6 +269,8 @@ __device__ __forceinline__ Sum row_sum(Sum t, RowShared* sh, int rank, int n) {
 
 // The gradient of a row: entry v is coef * ([v = label] - 2^((x - base) log2 e - l2)),
 // l2 the log2 of the row's sum; `zero`: every entry 0 (the logits are not looked at).
+// log2 e is one fp32 here: what that leaves out moves an entry by 1.3e-8 (x - base) of
+// itself (2e-7 where it is 4e-8 of the row's largest) and is not added up over rows.
 struct Grad {
   int label;
   float base, l2, coef;
@@ -984,7 +986,9 @@ struct RowPlan {
 //    to a CTA of four (then eight) vectors a thread leaves SMs idle, those: 64 x
 //    32000 6.9 / 5.0; else 16 vectors a thread, in groups of 128 threads while
 //    those hold the row (more rows under way on an SM: 8192 x 8192 57.1 / 45.4),
-//    else of 256: 1200 x 50256 53.0 / 45.4, 8192 x 128256 826 / 607.
+//    else of 256: 1200 x 50256 53.0 / 45.4, 8192 x 128256 826 / 607.  (The rule
+//    does not ask whether the gradient is wanted.  Without it a row is touched once,
+//    and 8192 x 32000 takes 82 / 100, 8192 x 50256 122 / 189.)
 //  - longer rows of the other two, which touch a row once: streamed.  8192 x 32000
 //    sums 80.6 / 94.2 held, 8192 x 50256 124 / 186.
 //  - rows beyond eight CTAs of 16 vectors a thread: streamed.
@@ -1052,8 +1056,10 @@ lora_status_t launch_rows(int kind, int dtype, RowArgs* a, int T, cudaStream_t s
 }
 
 // Whether the gradient's rows work their pairs out themselves.  It saves a launch
-// (host time, 2.3 us) and costs each row its pair's sums again: on the device 16
-// rows of 32000 take 7.9 us against 9.1, 90 rows 10.5 / 10.3, 256 rows 14.7 / 13.2.
+// (2.3 us of host time, which a captured step does not pay) and costs each row its
+// pair's sums again.  On the device, one pair of rows of 32000 (bf16), us against the
+// pairs apart: 16 rows 7.6 / 8.7, 48 9.9 / 9.5, 64 11.4 / 9.7, 96 9.8 / 10.2,
+// 128 12.3 / 10.4.
 bool pairs_by_rows(int T, int V, int n_pairs, int dtype) {
   return n_pairs > 0 && n_pairs <= 64 && T <= 128 && row_plan(kRowGrad, T, V, dtype).group == 0;
 }

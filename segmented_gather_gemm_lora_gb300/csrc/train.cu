@@ -304,9 +304,9 @@ using StageOf = std::conditional_t<kE4M3, Stage, NoStage>;
 // with, 201 with two spans ahead; 188 M elements with fp32 moments, whose loads
 // are many, 1095 without and 1289 with).
 // What an 8-bit state keeps is rounded as its definition says: scales, codes and
-// roots carry the correction steps above (48 M elements with their norms: 167.5 us;
-// 166.5 with approximate roots, 164.5 with approximate quotients too, 177 with the
-// IEEE forms of everything.  1.4 M elements in pages of 64: 12.0, 12.0, 11.9, 13.3).
+// roots carry the correction steps above (3 us of 166 for 48 M elements with their
+// norms, where the IEEE forms of everything cost 13; 1.4 M elements in pages of 64 take
+// 12 us with and without them, 13.3 with the IEEE forms).
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ TrainArgs a) {
   __shared__ StepShared sh;
@@ -651,8 +651,11 @@ int sum_spans(const lora_train_proj_t* projs, int n_proj, int n_ids) {
   return chunks * n_ids >= 32LL * sm_count() ? kSumMost * kSumGroups : kSumGroups;
 }
 
-// Spans of a chunk of the step: four, which spreads a CTA's start over 8192 elements, once
-// the launch still has several CTAs for every place on the GPU.
+// Spans of a chunk of the step: four, which spreads a CTA's start over 4096 elements, once
+// the launch still has several CTAs for every place on the GPU.  (Device times of one
+// span and of four, us: 8-bit moments, 3.3 M elements 11.5 / 13.4, 9.1 M 28.4 / 23.0,
+// 31.5 M with seven projections 98 / 69; fp32 moments and weights, 2.5 M 12.5 / 17.7,
+// 62 M 293 / 280.)
 int step_spans(const lora_train_proj_t* projs, int n_proj, int n_ids) {
   long long chunks = 0;
   for (int g = 0; g < n_proj; ++g)

@@ -5,8 +5,9 @@
  * lora_sgmv_backward (lora_sgmv.h) turns dL/dy into dA_i and dB_i, added into an
  * fp32 gradient array laid out like the pool's pages.  This part is what stands
  * on either side of it in a training step:
- *   - lora_token_logprobs, lora_preference_loss, lora_policy_loss: from the
- *     logits of a batch to its loss and dL/dlogits;
+ *   - lora_token_logprobs, lora_preference_loss, lora_policy_loss, lora_distill_loss:
+ *     from the logits of a batch to its loss and dL/dlogits;
+ *   - lora_topk_logits: what a teacher's logits leave for lora_distill_loss;
  *   - lora_grad_sumsq, lora_adamw_step: from the gradient array to new weights
  *     in the pool, for the adapters listed in a call, each with its own step
  *     count, learning rate and clipping norm (tenants train at their own pace);
@@ -32,9 +33,10 @@ extern "C" {
 #endif
 
 /* Further bits of the device error word. */
-#define LORA_DERR_BAD_LABEL 16 /* a label >= V: its row does not count */
+#define LORA_DERR_BAD_LABEL 16 /* a label or listed entry >= V, or listed twice: its row does not count */
 #define LORA_DERR_BAD_SEQ 32   /* sequence offsets not ascending within [0, T] */
-#define LORA_DERR_NONFINITE 64 /* an adapter's gradient norm is not finite: it was not stepped */
+#define LORA_DERR_NONFINITE 64 /* an adapter's gradient norm is not finite: it was not stepped; a group
+                                * quantised by lora_f8_quantize holds an infinity or a NaN */
 
 /* ------------------------------------------------------------ loss on logits --
  *
@@ -132,6 +134,66 @@ lora_status_t lora_policy_loss(const void* logits, int64_t ld, int32_t dtype, co
                                const float* weight, int32_t T, int32_t V, const lora_policy_opts_t* opts,
                                float* logp, float* loss, float* kl, void* dlogits, int64_t ldd,
                                int32_t* dev_err, lora_stream_t stream);
+
+/** Longest list of lora_topk_logits and lora_distill_loss. */
+#define LORA_TOPK_MAX 256
+
+/**
+ * The k largest entries of each row: ids[t, j] (device int32 [T, k]) and
+ * values[t, j] (device fp32 [T, k], the logits themselves), in falling order,
+ * equal values by rising index (-0 equals +0, a NaN comes before +inf); and
+ *     tail[t] = log sum over the entries not listed of exp(logits[t, v] / temperature)
+ * (device fp32 [T], may be NULL; -inf where nothing is left).  Entries of -inf are
+ * not listed: their places hold id -1 and value -inf.  labels (may be NULL: every
+ * row counts): a row with a negative label lists nothing, its tail is -inf.
+ * 1 <= k <= min(V, LORA_TOPK_MAX), temperature > 0.
+ */
+lora_status_t lora_topk_logits(const void* logits, int64_t ld, int32_t dtype, const int32_t* labels, int32_t T,
+                               int32_t V, int32_t k, float temperature, int32_t* ids, float* values, float* tail,
+                               int32_t* dev_err, lora_stream_t stream);
+
+/* Kinds of lora_distill_loss. */
+#define LORA_DISTILL_FORWARD 0
+#define LORA_DISTILL_REVERSE 1
+#define LORA_DISTILL_JSD 2
+
+typedef struct {
+  int32_t kind;      /* LORA_DISTILL_* */
+  float temperature; /* > 0, of teacher and student (not of the cross-entropy) */
+  float mix;         /* 0 < mix < 1: the teacher's share of LORA_DISTILL_JSD's mixture */
+  float kd_weight;   /* >= 0: weight of the divergence (temperature^2 keeps its gradient's size) */
+  float ce_weight;   /* >= 0: weight of the labels' cross-entropy; 0: labels only say which rows count */
+  float grad_scale;  /* multiplies the gradient */
+} lora_distill_opts_t;
+
+/**
+ * Divergence of a student from a teacher's list, per row, and its gradient.
+ * ids, values, tail: what lora_topk_logits leaves (device int32 and fp32 [T, k], fp32
+ * [T]), in any order; an entry with a negative id or a value of -inf is absent.
+ * Outcomes are the listed entries, and everything else together as one:
+ *     p = softmax over the list of values / temperature and, for the rest, tail
+ *         (NULL or -inf: the teacher gives the rest nothing),
+ *     q = softmax(logits[t] / temperature), the rest's entries added up,
+ *     kd = forward: KL(p | q) = sum p log(p / q),    reverse: KL(q | p),
+ *          jsd: mix KL(p | m) + (1 - mix) KL(q | m),  m = mix p + (1 - mix) q,
+ *     ce = -log softmax(logits[t])[labels[t]],
+ *     loss[t] = weight[t] (kd_weight kd + ce_weight ce),
+ *     dlogits[t, v] = grad_scale dloss[t] / dlogits[t, v].
+ * Terms are summed as p log(p / q) - p + q, none of which is negative, so a small
+ * divergence is not a difference of large sums; the rest's share is summed without
+ * the listed entries.  A kd that is infinite by the teacher giving nothing (reverse)
+ * leaves the row a zero gradient, as does a row with nothing but -inf.  A list with
+ * nothing in it (nor a tail) has kd 0.  labels (int32 [T]) may be NULL with ce_weight
+ * 0: every row counts; else a negative label marks a row that does not.  weight (fp32
+ * [T]) NULL stands for ones; weight 0: loss 0 and a zero gradient row.  An id >= V or
+ * listed twice in a row sets LORA_DERR_BAD_LABEL and the row does not count.
+ * Reverse needs tail.  loss: device fp32 [T]; kd, ce: fp32 [T] or NULL (ce is computed
+ * only with ce_weight > 0, else 0); 1 <= k <= LORA_TOPK_MAX.
+ */
+lora_status_t lora_distill_loss(const void* logits, int64_t ld, int32_t dtype, const int32_t* ids, const float* values,
+                                const float* tail, int32_t k, const int32_t* labels, const float* weight, int32_t T,
+                                int32_t V, const lora_distill_opts_t* opts, float* loss, float* kd, float* ce,
+                                void* dlogits, int64_t ldd, int32_t* dev_err, lora_stream_t stream);
 
 /* ------------------------------------------------------------ optimizer step --
  *

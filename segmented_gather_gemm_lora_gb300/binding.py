@@ -1,5 +1,5 @@
 """Thin Python binding of liblora_sgmv.so (the C ABI in include/lora_sgmv.h,
-include/lora_pool.h and include/lora_train.h).
+include/lora_pool.h, include/lora_train.h and include/lora_f8.h).
 
 Argument marshalling only: every step of the LoRA path runs in the library's
 CUDA kernels.  PyTorch supplies device memory and the current stream.  There is
@@ -50,6 +50,16 @@ LORA_STATE_F32 = 0
 LORA_STATE_E4M3 = 1
 LORA_ADAMW_BLOCK = 64
 LORA_ADAMW_ZERO_GRAD = 1
+LORA_TOPK_MAX = 256
+LORA_DISTILL_FORWARD = 0
+LORA_DISTILL_REVERSE = 1
+LORA_DISTILL_JSD = 2
+LORA_F8_E4M3 = 0
+LORA_F8_E5M2 = 1
+LORA_F8_FROM_BF16 = 0
+LORA_F8_FROM_F32 = 1
+LORA_F8_BLOCK = 128
+LORA_F8_POW2 = 1
 
 EXPORTED = (
     "lora_segments_buffer_bytes",
@@ -91,6 +101,11 @@ EXPORTED = (
     "lora_grad_sumsq_workspace_bytes",
     "lora_grad_sumsq",
     "lora_adamw_step",
+    "lora_topk_logits",
+    "lora_distill_loss",
+    "lora_f8_quantize",
+    "lora_base_f8",
+    "lora_base_f8_backward",
 )
 
 
@@ -147,6 +162,17 @@ class lora_adamw_hyper_t(ctypes.Structure):
     _fields_ = [("step", ctypes.c_int32), ("lr", ctypes.c_float), ("beta1", ctypes.c_float),
                 ("beta2", ctypes.c_float), ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float),
                 ("max_norm", ctypes.c_float), ("grad_scale", ctypes.c_float)]
+
+
+class lora_distill_opts_t(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("temperature", ctypes.c_float), ("mix", ctypes.c_float),
+                ("kd_weight", ctypes.c_float), ("ce_weight", ctypes.c_float), ("grad_scale", ctypes.c_float)]
+
+
+class lora_f8_matrix_t(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("scale_row", ctypes.c_int64), ("scale_col", ctypes.c_int64), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32), ("block_rows", ctypes.c_int32), ("type", ctypes.c_int32)]
 
 
 class LoraError(RuntimeError):
@@ -249,6 +275,17 @@ def lib():
         L.lora_grad_sumsq.argtypes = [proj_p, i32, vp, i32, i32, vp, vp, sz, vp, vp]
         L.lora_adamw_step.restype = i32
         L.lora_adamw_step.argtypes = [proj_p, i32, i32, vp, i32, vp, vp, u32, vp, vp]
+        L.lora_topk_logits.restype = i32
+        L.lora_topk_logits.argtypes = [vp, i64, i32, vp, i32, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp]
+        L.lora_distill_loss.restype = i32
+        L.lora_distill_loss.argtypes = [vp, i64, i32, vp, vp, vp, i32, vp, vp, i32, i32,
+                                        ctypes.POINTER(lora_distill_opts_t), vp, vp, vp, vp, i64, vp, vp]
+        f8_p = ctypes.POINTER(lora_f8_matrix_t)
+        L.lora_f8_quantize.restype = i32
+        L.lora_f8_quantize.argtypes = [vp, i64, i32, f8_p, u32, vp, vp]
+        for f in (L.lora_base_f8, L.lora_base_f8_backward):
+            f.restype = i32
+            f.argtypes = [f8_p, f8_p, vp, i64, i32, vp, vp]
         _lib = L
     return _lib
 
@@ -741,6 +778,69 @@ def lora_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch
                                   _rows(kl, T, f32, "kl"), dp, ldd, _addr(err), _handle(stream)), "lora_policy_loss")
 
 
+def _one_device(stream, first: torch.Tensor, *others: Optional[torch.Tensor]):
+    """Refuse tensors that do not share a CUDA device, or that of the current stream where none is given: the
+    library would read their addresses on the device the call runs on."""
+    d = first.get_device()
+    if d < 0:
+        raise ValueError("expected tensors on a CUDA device")
+    if stream is None and d != torch.cuda.current_device():
+        raise ValueError("expected tensors on the current CUDA device (%d), or a stream of theirs" % torch.cuda.current_device())
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError("expected tensors on one CUDA device")
+
+
+def _err_word(err: Optional[torch.Tensor]) -> int:
+    if err is None:
+        return 0
+    if err.dtype is not torch.int32 or err.numel() < 1:
+        raise ValueError("err: expected an element of torch.int32")
+    return err.data_ptr()
+
+
+def lora_topk_logits(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, tail: Optional[torch.Tensor] = None,
+                     temperature: float = 1.0, labels: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
+                     stream=None):
+    """The k largest logits of each row, largest first (ids int32 and values fp32 [T, k]; equal ones by rising
+    index), and tail[t] = log of the sum of exp(logit / temperature) over the others.  labels int32 [T]: rows with a
+    negative label list nothing.  See include/lora_train.h."""
+    _one_device(stream, logits, ids, values, tail, labels, err)
+    p, ld, code, T, V = _logits(logits)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError("ids: expected a row for each row of logits")
+    k = ids.shape[1]
+    i32, f32 = torch.int32, torch.float32
+    _check(lib().lora_topk_logits(p, ld, code, _rows(labels, T, i32, "labels"), T, V, k, float(temperature),
+                                  _rows(ids, T * k, i32, "ids"), _rows(values, T * k, f32, "values"),
+                                  _rows(tail, T, f32, "tail"), _err_word(err), _handle(stream)), "lora_topk_logits")
+
+
+def lora_distill_loss(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, loss: torch.Tensor,
+                      kd: Optional[torch.Tensor], dlogits: Optional[torch.Tensor], tail: Optional[torch.Tensor] = None,
+                      labels: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                      ce: Optional[torch.Tensor] = None, kind: int = LORA_DISTILL_FORWARD, mix: float = 0.5,
+                      temperature: float = 1.0, kd_weight: float = 1.0, ce_weight: float = 0.0, grad_scale: float = 1.0,
+                      err: Optional[torch.Tensor] = None, stream=None):
+    """Divergence of a student's logits from a teacher's list (ids, values [T, k] and tail, as lora_topk_logits
+    leaves them), with the labels' cross-entropy, per row, and its gradient (see include/lora_train.h).  dlogits may
+    be the logits (the gradient takes their place) or None."""
+    _one_device(stream, logits, ids, values, loss, kd, dlogits, tail, labels, weight, ce, err)
+    p, ld, code, T, V = _logits(logits)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError("ids: expected a row for each row of logits")
+    k = ids.shape[1]
+    i32, f32 = torch.int32, torch.float32
+    opts = _opts(lora_distill_opts_t, int(kind), float(temperature), float(mix), float(kd_weight), float(ce_weight),
+                 float(grad_scale))
+    dp, ldd = _grad_of(logits, dlogits)
+    _check(lib().lora_distill_loss(p, ld, code, _rows(ids, T * k, i32, "ids"), _rows(values, T * k, f32, "values"),
+                                   _rows(tail, T, f32, "tail"), k, _rows(labels, T, i32, "labels"),
+                                   _rows(weight, T, f32, "weight"), T, V, opts, _rows(loss, T, f32, "loss"),
+                                   _rows(kd, T, f32, "kd"), _rows(ce, T, f32, "ce"), dp, ldd, _err_word(err),
+                                   _handle(stream)), "lora_distill_loss")
+
+
 # --------------------------------------------------- training: optimizer step --
 
 class TrainProj:
@@ -843,3 +943,82 @@ def lora_adamw_step(train: TrainSet, ids: torch.Tensor, hyper: torch.Tensor, sum
                                  _rows(sumsq, train.n_adapters, torch.float32, "sumsq"),
                                  LORA_ADAMW_ZERO_GRAD if zero_grad else 0, _addr(err), _handle(stream)),
            "lora_adamw_step")
+
+
+# ------------------------------------------------------------- base in 8 bits --
+
+_F8_CODE = {torch.float8_e4m3fn: LORA_F8_E4M3, torch.float8_e5m2: LORA_F8_E5M2}
+_F8_TORCH = {code: t for t, code in _F8_CODE.items()}
+_F8_FROM = {torch.bfloat16: LORA_F8_FROM_BF16, torch.float32: LORA_F8_FROM_F32}
+
+
+class F8Matrix:
+    """An 8-bit matrix (lora_f8_matrix_t): codes [rows, cols] of float8_e4m3fn or float8_e5m2 whose rows start on
+    16-byte boundaries, and fp32 scales [rows / block_rows, cols / 128] (rounded up) of any strides.  block_rows: 1
+    (activations, gradients) or 128 (weights)."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 1):
+        code = _F8_CODE.get(codes.dtype)
+        if code is None or codes.dim() != 2:
+            raise ValueError("codes: expected a matrix of float8_e4m3fn or float8_e5m2")
+        if block_rows not in (1, LORA_F8_BLOCK):
+            raise ValueError("block_rows: expected 1 or %d" % LORA_F8_BLOCK)
+        rows, cols = codes.shape
+        ld = codes.stride(0)
+        if rows <= 1:
+            ld = max(ld, -(-cols // 16) * 16) // 16 * 16  # the stride of a matrix of one row says nothing
+        if cols < 1 or (cols > 1 and codes.stride(1) != 1) or ld % 16 or ld < cols or codes.data_ptr() % 16:
+            raise ValueError("codes: expected rows of consecutive elements on 16-byte boundaries")
+        if scales.dtype is not torch.float32 or tuple(scales.shape) != (-(-rows // block_rows), -(-cols // LORA_F8_BLOCK)):
+            raise ValueError("scales: expected torch.float32 of [%d, %d]"
+                             % (-(-rows // block_rows), -(-cols // LORA_F8_BLOCK)))
+        self.codes, self.scales, self.block_rows, self.type = codes, scales, block_rows, code
+        self.c = lora_f8_matrix_t(codes.data_ptr() or None, ld, scales.data_ptr() or None, scales.stride(0), scales.stride(1),
+                                  rows, cols, block_rows, code)
+        self.ref = ctypes.byref(self.c)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, block_rows: int = 1, type: int = LORA_F8_E4M3, device="cuda"):
+        """Room for a matrix: rows padded to 16 bytes, the scales of a group of 128 columns side by side for all the
+        rows (block_rows 1), the layout the product reads fastest."""
+        codes = torch.empty(rows, -(-cols // 16) * 16, dtype=torch.uint8, device=device).view(_F8_TORCH[type])[:, :cols]
+        groups, blocks = -(-cols // LORA_F8_BLOCK), -(-rows // block_rows)
+        scales = torch.empty(groups, blocks, device=device).t() if block_rows == 1 else torch.empty(blocks, groups, device=device)
+        return cls(codes, scales, block_rows)
+
+
+def _plain(t: torch.Tensor, rows: int, cols: int, what: str):
+    """(address, row stride, type code) of a plain [rows, cols] matrix beside 8-bit ones."""
+    code = _F8_FROM.get(t.dtype)
+    if code is None or t.shape != (rows, cols):
+        raise ValueError("%s: expected bfloat16 or float32 of [%d, %d]" % (what, rows, cols))
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError("%s: expected a row-major matrix with unit column stride" % what)
+    if rows <= 1:
+        ld = max(ld, cols)
+    elif ld < cols:
+        raise ValueError("%s: expected rows that do not overlap" % what)
+    return t.data_ptr(), ld, code
+
+
+def lora_f8_quantize(x: torch.Tensor, q: F8Matrix, pow2: bool = False, err: Optional[torch.Tensor] = None, stream=None):
+    """Quantise x (bf16 or fp32, q's shape) into q; pow2: scales are powers of two (see include/lora_f8.h)."""
+    _one_device(stream, x, q.codes, q.scales, err)
+    p, ld, code = _plain(x, q.c.rows, q.c.cols, "x")
+    _check(lib().lora_f8_quantize(p, ld, code, q.ref, LORA_F8_POW2 if pow2 else 0, _err_word(err), _handle(stream)),
+           "lora_f8_quantize")
+
+
+def lora_base_f8(x: F8Matrix, w: F8Matrix, y: torch.Tensor, err: Optional[torch.Tensor] = None, stream=None):
+    """y = x W0^T, written only (bf16 or fp32): x [T, d_in] in groups of a row, w [d_out, d_in] in blocks of 128 rows."""
+    _one_device(stream, y, x.codes, x.scales, w.codes, w.scales, err)
+    p, ld, code = _plain(y, x.c.rows, w.c.rows, "y")
+    _check(lib().lora_base_f8(x.ref, w.ref, p, ld, code, _err_word(err), _handle(stream)), "lora_base_f8")
+
+
+def lora_base_f8_backward(dy: F8Matrix, w: F8Matrix, dx: torch.Tensor, err: Optional[torch.Tensor] = None, stream=None):
+    """dx = dy W0, written only (bf16 or fp32): the gradient of lora_base_f8's input (the base is frozen)."""
+    _one_device(stream, dx, dy.codes, dy.scales, w.codes, w.scales, err)
+    p, ld, code = _plain(dx, dy.c.rows, w.c.cols, "dx")
+    _check(lib().lora_base_f8_backward(dy.ref, w.ref, p, ld, code, _err_word(err), _handle(stream)), "lora_base_f8_backward")

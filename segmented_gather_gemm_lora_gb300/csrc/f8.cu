@@ -1,5 +1,5 @@
-// The base in 8-bit floating point (lora_f8.h): quantising, the base's product
-// and its input's gradient.
+// The base in 8-bit floating point (lora_f8.h): quantising, and the entry points of
+// the product and its input's gradient (f8_gemm.cu).
 //
 // Quantising: a group's largest magnitude a is an integer maximum of the values'
 // bits without their signs (which orders a NaN above everything, so it is kept);
@@ -93,61 +93,6 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_consta
       static_cast<uint8_t*>(a.q.codes)[r * a.q.ld + c] = (uint8_t)pack_f8(quotient(value_at(a, r, c), v), 0.f, a.q.type);
 }
 
-// ------------------------------------------------------------------ product --
-
-struct ProductArgs {
-  lora_f8_matrix_t x, w;
-  void* y;
-  long long ldy;
-  int f32, back;
-  int T, inner, outer;  // y [T, outer] = x [T, inner] times w, or w transposed
-};
-
-__device__ __forceinline__ float widen(uint8_t c, int type) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, type == LORA_F8_E4M3 ? __NV_E4M3 : __NV_E5M2)));
-}
-
-constexpr int kPTile = 64, kPStep = 16;
-__global__ void __launch_bounds__(256) product_kernel(const __grid_constant__ ProductArgs a) {
-  __shared__ float xs[kPStep][kPTile + 1], ws[kPStep][kPTile + 1];
-  pdl_wait_then_release();
-  const int t0 = blockIdx.y * kPTile, n0 = blockIdx.x * kPTile, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  float acc[4][4] = {};
-  for (int g = 0; g * LORA_F8_BLOCK < a.inner; ++g) {
-    float part[4][4] = {};
-    for (int k0 = g * LORA_F8_BLOCK; k0 < min(a.inner, (g + 1) * LORA_F8_BLOCK); k0 += kPStep) {
-      for (int i = threadIdx.x; i < kPStep * kPTile; i += 256) {
-        const int k = k0 + i % kPStep, t = t0 + i / kPStep, n = n0 + i / kPStep;
-        xs[i % kPStep][i / kPStep] =
-            k < a.inner && t < a.T ? widen(static_cast<const uint8_t*>(a.x.codes)[t * a.x.ld + k], a.x.type) : 0.f;
-        const long long at = a.back ? k * a.w.ld + n : n * a.w.ld + k;
-        ws[i % kPStep][i / kPStep] =
-            k < a.inner && n < a.outer ? widen(static_cast<const uint8_t*>(a.w.codes)[at], a.w.type) : 0.f;
-      }
-      __syncthreads();
-      for (int k = 0; k < kPStep; ++k)
-        for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 4; ++j) part[i][j] = fmaf(xs[k][ty * 4 + i], ws[k][tx * 4 + j], part[i][j]);
-      __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int t = t0 + ty * 4 + i, n = n0 + tx * 4 + j, nb = n / LORA_F8_BLOCK;
-        if (t >= a.T || n >= a.outer) continue;
-        const float s = a.x.scales[t * a.x.scale_row + g * a.x.scale_col] *
-                        a.w.scales[(a.back ? g : nb) * a.w.scale_row + (a.back ? nb : g) * a.w.scale_col];
-        acc[i][j] = fmaf(part[i][j], s, acc[i][j]);
-      }
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int t = t0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (t >= a.T || n >= a.outer) continue;
-      if (a.f32) static_cast<float*>(a.y)[t * a.ldy + n] = acc[i][j];
-      else static_cast<uint16_t*>(a.y)[t * a.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[i][j]));
-    }
-}
-
 // -------------------------------------------------------------------- host --
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -200,21 +145,7 @@ lora_status_t product(const lora_f8_matrix_t* x, const lora_f8_matrix_t* w, void
   const long long bytes = plain_bytes(ldy, dtype, x->rows, outer);
   for (const lora_f8_matrix_t* m : {x, w})
     if (overlap(y, bytes, m->codes, code_bytes(*m)) || overlap(y, bytes, m->scales, scale_bytes(*m))) return LORA_ERR_INVALID_ARG;
-  ProductArgs a;
-  memset(&a, 0, sizeof(a));
-  a.x = *x;
-  a.w = *w;
-  a.y = y;
-  a.ldy = ldy;
-  a.f32 = dtype == LORA_F8_FROM_F32;
-  a.back = back;
-  a.T = x->rows;
-  a.inner = inner;
-  a.outer = outer;
-  (void)err;
-  const dim3 grid((unsigned)blocks_of(outer, kPTile), (unsigned)blocks_of(a.T, kPTile));
-  if (grid.y > 65535) return LORA_ERR_UNSUPPORTED;
-  return launch_pdl((const void*)product_kernel, grid, dim3(256), 0, s, 0, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  return launch_f8_product(x, w, y, ldy, dtype == LORA_F8_FROM_F32, back, err, s);
 }
 
 }  // namespace

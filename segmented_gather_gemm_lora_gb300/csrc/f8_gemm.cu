@@ -1,0 +1,589 @@
+// The products of an 8-bit base (lora_f8.h): y = x W0^T and dx = dy W0 with a scale
+// for each row's group of 128 of the one and for each 128 x 128 block of the other.
+//
+//     y[t, n] = sum_g xs[t, g] ws[n / 128, g] (sum over the 128 k of group g of xc[t, k] wc[n, k])
+//
+// The inner sums are tcgen05.mma.kind::f8f6f4 (four of K = 32) into tensor memory;
+// between groups the scales change, so each group's sums are read back and added, times
+// the product of the two scales, to fp32 sums in registers ("promotion").  Two
+// accumulators in tensor memory alternate, so the next group's MMAs run meanwhile.
+// dx = dy W0 sums over W0's rows: the same kernels with the operand from W0 MN-major,
+// taken as it lies.  Ends inside a tile are the tensor maps' zero fill.
+//
+// Two forms:
+//  - wide: 128 tokens x 256 outputs, tokens down the tile, so a thread's row has one
+//    factor a group and a block of weights (a promotion is one FMA an element).  A
+//    cluster of two CTAs takes two tiles of the same outputs and each loads half of
+//    their weights for both.
+//  - split: few tokens.  128 outputs down the tile (so that every thread of a warpgroup has
+//    work) and 16 to 128 tokens across; a cluster of up to eight CTAs shares the sum
+//    over k and adds its parts up in rank order through distributed shared memory.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "internal.h"
+#include "lora_f8.h"
+#include "pairs.cuh"
+#include "tc.cuh"
+
+namespace lora {
+
+namespace {
+
+constexpr int kG = LORA_F8_BLOCK;
+
+struct GemmArgs {
+  CUtensorMap xmap;  // [T, inner], boxes of 128 columns
+  CUtensorMap wmap;  // [N, K], boxes of 128 columns
+  const float* xs;
+  const float* ws;
+  long long xs_t, xs_g;  // of a token, of a group
+  long long ws_o, ws_g;  // of a block of outputs, of a group
+  void* y;
+  long long ldy;
+  uint32_t idesc;
+  int f32, wide_store;  // output type; rows of y on 16-byte boundaries
+  int T, outer, nk;     // nk: groups of 128 of the sum
+  int n_o, n_pairs;     // wide: tiles of outputs; pairs of tiles
+  int32_t* err;
+  long long probe;
+};
+
+// Every thread of a block learns whether the timeout probe's wait ran out.
+__device__ __forceinline__ bool probe_passes(const GemmArgs& a) {
+  if (a.probe <= 0) return true;
+  __shared__ uint64_t probe_bar;
+  __shared__ int probe_ok;
+  if (threadIdx.x == 0) probe_ok = wait_probe(&probe_bar, a.probe) ? 1 : 0;
+  __syncthreads();
+  return probe_ok != 0;
+}
+
+// Sixteen or so bytes of outputs from fp32 values, one rounding each.
+template <typename O>
+__device__ __forceinline__ uint4 pack_out(const float* f);
+template <>
+__device__ __forceinline__ uint4 pack_out<uint16_t>(const float* f) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+template <>
+__device__ __forceinline__ uint4 pack_out<float>(const float* f) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+
+// The four MMAs of one group: descriptors step 32 bytes along a K-major operand, 32
+// rows of 128 bytes along an MN-major one.
+template <bool kAMn, bool kBMn>
+__device__ __forceinline__ void group_mma(uint32_t d, uint32_t as, uint32_t bs, uint32_t b_lbo, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < kG / 32; ++kk) {
+    const uint64_t ad = kAMn ? sdesc_sw128(as + 4096 * kk, 0, 1024) : sdesc_sw128(as + 32 * kk, 16, 1024);
+    const uint64_t bd = kBMn ? sdesc_sw128(bs + 4096 * kk, b_lbo, 1024) : sdesc_sw128(bs + 32 * kk, 16, 1024);
+    mma_f8(d, ad, bd, idesc, kk != 0);
+  }
+}
+
+// Wait (bounded) for the copies of the last `issued` stages that may be under way.
+__device__ __forceinline__ void drain(uint64_t* full, uint32_t issued, int stages) {
+  for (uint32_t g = issued > (uint32_t)stages ? issued - stages : 0; g < issued; ++g)
+    mbar_wait(smem_u32(&full[g % stages]), (g / stages) & 1);
+}
+
+// --------------------------------------------------------------------- wide --
+
+constexpr int kWM = 128, kWN = 256, kWStages = 4;
+constexpr int kWEpiWarps = 8;
+constexpr int kWThreads = 128 + 32 * kWEpiWarps;  // warp 0 copies, warp 1 issues MMAs, warps 4-11 promote
+// Registers: 384 threads are launched with 168 each; the first warpgroup gives up 128 x 128
+// of them, which the promoting ones' 128 sums a thread take (64 x 256): 64512 in all, as launched.
+#define LORA_FEWER_REGISTERS() asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory")
+#define LORA_MORE_REGISTERS() asm volatile("setmaxnreg.inc.sync.aligned.u32 232;" ::: "memory")
+constexpr int kWABytes = kWM * kG, kWStageBytes = kWABytes + kWN * kG;
+constexpr size_t kWOffOut = (size_t)kWStages * kWStageBytes;  // a promoting warp's 32 rows of 128 bytes
+constexpr size_t kWOffBars = kWOffOut + (size_t)kWEpiWarps * 4096;
+constexpr size_t kWSmem = kWOffBars + (2 * kWStages + 5) * 8 + 16 + 1024;
+static_assert(kWSmem <= 232448, "shared memory of one CTA");
+
+// 32 rows x 128 bytes of a tile's outputs (this lane's row in v, 8 pieces of 16 bytes)
+// through shared memory, so that a store covers whole lines.
+template <typename O>
+__device__ __forceinline__ void store_rows(const GemmArgs& a, uint8_t* st, const uint4 (&v)[8], int t0, int n0, int lane) {
+  constexpr int kPer = 16 / sizeof(O);  // outputs of a piece
+#pragma unroll
+  for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(st + lane * 128 + ((q ^ (lane & 7)) << 4)) = v[q];
+  __syncwarp();
+  O* const y = static_cast<O*>(a.y);
+  const int piece = lane & 7, n = n0 + piece * kPer;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3), t = t0 + r;
+    if (t >= a.T || n >= a.outer) continue;
+    const uint4 u = *reinterpret_cast<const uint4*>(st + r * 128 + ((piece ^ (r & 7)) << 4));
+    O* const dst = y + (long long)t * a.ldy + n;
+    if (a.wide_store && n + kPer <= a.outer) {
+      *reinterpret_cast<uint4*>(dst) = u;
+    } else {
+      const O* e = reinterpret_cast<const O*>(&u);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (n + j < a.outer) dst[j] = e[j];
+    }
+  }
+  __syncwarp();
+}
+
+template <bool kBack>
+__global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_constant__ GemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kWOffBars);  // [stages] copied bytes
+  uint64_t* empty = full + kWStages;                             // [stages] both CTAs' MMA commits
+  uint64_t* acc_full = empty + kWStages;                         // [2] MMA commit: a group's sums are complete
+  uint64_t* acc_empty = acc_full + 2;                            // [2] the promoting warps have them
+  uint64_t* mma_done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t crank = cluster_ctarank(), cid = cluster_id_x(), ncl = ncluster_x();
+  if (tid == 0) {
+    for (int s = 0; s < kWStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 2);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&acc_full[b]), 1);
+      mbar_init(smem_u32(&acc_empty[b]), kWEpiWarps);
+    }
+    mbar_init(smem_u32(mma_done), 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 2 * kWN);
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers are there before the peer's copies and commits
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait_then_release();
+  bool ok = probe_passes(a);
+  // this CTA's tiles: tokens (2 (p / n_o) + crank), outputs p % n_o of the cluster's pairs p
+  if (warp < 4) {
+    LORA_FEWER_REGISTERS();
+    if (warp == 0 && lane == 0 && ok) {
+      prefetch_tensormap(&a.xmap);
+      prefetch_tensormap(&a.wmap);
+      uint32_t g = 0;
+      for (int p = (int)cid; p < a.n_pairs && ok; p += (int)ncl) {
+        const int t0 = (2 * (p / a.n_o) + (int)crank) * kWM, o0 = (p % a.n_o) * kWN + (int)crank * kG;
+        for (int kb = 0; kb < a.nk; ++kb, ++g) {
+          const uint32_t st = g % kWStages;
+          if (g >= kWStages && !mbar_wait(smem_u32(&empty[st]), ((g / kWStages) - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = smem_u32(sm + (size_t)st * kWStageBytes), bar = smem_u32(&full[st]);
+          // this CTA's tokens, and its half of the weights into both CTAs
+          mbar_arrive_expect_tx(bar, kWStageBytes);
+          tma_load_2d(dst, &a.xmap, kb * kG, t0, bar);
+          tma_load_2d_mc(dst + kWABytes + crank * (kG * kG), &a.wmap, kBack ? o0 : kb * kG, kBack ? kb * kG : o0, bar,
+                         (uint16_t)3u);
+        }
+      }
+      if (!ok) report(a.err, LORA_DERR_TIMEOUT);
+      drain(full, g, kWStages);
+    }
+    if (warp == 1 && lane == 0 && ok) {
+      uint32_t g = 0;
+      for (int p = (int)cid; p < a.n_pairs && ok; p += (int)ncl) {
+        for (int kb = 0; kb < a.nk; ++kb, ++g) {
+          const uint32_t st = g % kWStages, ab = g & 1;
+          if ((g >= 2 && !mbar_wait(smem_u32(&acc_empty[ab]), ((g >> 1) - 1) & 1)) ||
+              !mbar_wait(smem_u32(&full[st]), (g / kWStages) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t as = smem_u32(sm + (size_t)st * kWStageBytes);
+          group_mma<false, kBack>(tmem + ab * kWN, as, as + kWABytes, kG * kG, a.idesc);
+          mma_commit_mc(smem_u32(&empty[st]), (uint16_t)3u);  // free in both CTAs once both have read it
+          mma_commit(smem_u32(&acc_full[ab]));
+        }
+      }
+      if (g > 0) {  // every MMA has completed before tensor memory is freed
+        mma_commit(smem_u32(mma_done));
+        mbar_wait(smem_u32(mma_done), 0);
+      }
+      if (!ok) report(a.err, LORA_DERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    LORA_MORE_REGISTERS();
+    const int quarter = warp & 3, half = (warp - 4) >> 2;  // tensor-memory lanes; the block of outputs
+    uint8_t* const out = sm + kWOffOut + (size_t)(warp - 4) * 4096;
+    uint32_t g = 0;
+    for (int p = (int)cid; p < a.n_pairs && ok; p += (int)ncl) {
+      const int t0 = (2 * (p / a.n_o) + (int)crank) * kWM + quarter * 32, t = t0 + lane;
+      const int n0 = (p % a.n_o) * kWN + half * kG;
+      const bool row_on = t < a.T, col_on = n0 < a.outer;
+      const float* const xs = a.xs + (row_on ? t * a.xs_t : 0);
+      const float* const ws = a.ws + (col_on ? n0 / kG * a.ws_o : 0);
+      // the factors of the coming groups, two ahead
+      float x1 = xs[0], w1 = ws[0], x2 = 0.f, w2 = 0.f;
+      if (a.nk > 1) {
+        x2 = xs[a.xs_g];
+        w2 = ws[a.ws_g];
+      }
+      uint64_t acc[kG / 2];
+#pragma unroll
+      for (int i = 0; i < kG / 2; ++i) acc[i] = 0;
+      for (int kb = 0; kb < a.nk; ++kb, ++g) {
+        const float f = x1 * w1;
+        x1 = x2;
+        w1 = w2;
+        if (kb + 2 < a.nk) {
+          x2 = xs[(kb + 2) * a.xs_g];
+          w2 = ws[(kb + 2) * a.ws_g];
+        }
+        const uint32_t ab = g & 1;
+        if (__any_sync(0xffffffffu, !mbar_wait(smem_u32(&acc_full[ab]), (g >> 1) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t f2 = pair_of(f, f);
+#pragma unroll
+        for (int c = 0; c < kG / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32_nowait(tmem + ab * kWN + half * kG + c * 32 + ((uint32_t)(quarter * 32) << 16), r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            acc[c * 16 + i] = fma2(pair_of(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[c * 16 + i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&acc_empty[ab]));
+      }
+      if (!ok) break;
+      const int per = a.f32 ? 32 : 64;  // outputs of 128 bytes
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (a.f32) {
+          uint4 v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float e[4];
+            split(acc[c * 16 + 2 * q], e[0], e[1]);
+            split(acc[c * 16 + 2 * q + 1], e[2], e[3]);
+            v[q] = pack_out<float>(e);
+          }
+          if (n0 + c * per < a.outer) store_rows<float>(a, out, v, t0, n0 + c * per, lane);
+        } else if (c < 2) {
+          uint4 v[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float e[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split(acc[c * 32 + 4 * q + j], e[2 * j], e[2 * j + 1]);
+            v[q] = pack_out<uint16_t>(e);
+          }
+          if (n0 + c * per < a.outer) store_rows<uint16_t>(a, out, v, t0, n0 + c * per, lane);
+        }
+      }
+    }
+    if (!ok && lane == 0) report(a.err, LORA_DERR_TIMEOUT);
+  }
+  tc_fence_before();
+  cluster_sync();  // neither CTA leaves while the peer may still copy into it or arrive on its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 2 * kWN);
+  }
+}
+
+// -------------------------------------------------------------------- split --
+
+constexpr int kSMaxSplit = 8;
+constexpr int kSThreads = 64 + 128;  // warp 0 copies, warp 1 issues MMAs, warps 2-5 promote
+
+template <int kNT>
+struct Split {
+  static constexpr int kStages = kNT == 16 ? 6 : kNT == 32 ? 5 : kNT == 64 ? 4 : 3;
+  static constexpr int kStageBytes = kG * kG + kNT * kG;
+  static constexpr int kCols = kNT < 16 ? 32 : 2 * kNT;  // tensor-memory columns: two accumulators
+  static constexpr size_t kOffF = (size_t)kStages * kStageBytes;       // [4][kNT] factors of coming groups
+  static constexpr size_t kOffBars = kOffF + 4 * kNT * sizeof(float);
+  static constexpr size_t kSmem = kOffBars + (2 * kStages + 5) * 8 + 16 + 1024;
+  static_assert((size_t)kStages * kStageBytes >= (size_t)kNT * kG * 4, "the parts of the sum take the stages' place");
+};
+
+// Whether `p` holds in all the promoting threads (a barrier of theirs, too).
+__device__ __forceinline__ bool all_promoting(bool p) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred q, o;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.and.pred o, 1, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, o;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ float4 ld_dsmem_v4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+template <int kNT, bool kBack>
+__global__ void __launch_bounds__(kSThreads, 2) f8_split_kernel(const __grid_constant__ GemmArgs a) {
+  using S = Split<kNT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int failed;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  float* factors = reinterpret_cast<float*>(sm + S::kOffF);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::kOffBars);
+  uint64_t* empty = full + S::kStages;
+  uint64_t* acc_full = empty + S::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* mma_done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
+  const int tile = (int)cluster_id_x(), o0 = tile % a.n_o * kG, t0 = tile / a.n_o * kNT;
+  // this CTA's groups of the sum
+  const int k0 = (int)((long long)a.nk * rank / n), k1 = (int)((long long)a.nk * (rank + 1) / n);
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&acc_full[b]), 1);
+      mbar_init(smem_u32(&acc_empty[b]), 4);
+    }
+    mbar_init(smem_u32(mma_done), 1);
+    failed = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), S::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait_then_release();
+  bool ok = probe_passes(a);
+  if (warp == 0) {
+    if (lane == 0 && ok) {
+      prefetch_tensormap(&a.wmap);
+      prefetch_tensormap(&a.xmap);
+      uint32_t g = 0;
+      for (int kb = k0; kb < k1; ++kb, ++g) {
+        const uint32_t st = g % S::kStages;
+        if (g >= S::kStages && !mbar_wait(smem_u32(&empty[st]), ((g / S::kStages) - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = smem_u32(sm + (size_t)st * S::kStageBytes), bar = smem_u32(&full[st]);
+        mbar_arrive_expect_tx(bar, S::kStageBytes);
+        tma_load_2d(dst, &a.wmap, kBack ? o0 : kb * kG, kBack ? kb * kG : o0, bar);
+        tma_load_2d(dst + kG * kG, &a.xmap, kb * kG, t0, bar);
+      }
+      if (!ok) report(a.err, LORA_DERR_TIMEOUT);
+      drain(full, g, S::kStages);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && ok) {
+      uint32_t g = 0;
+      for (int kb = k0; kb < k1; ++kb, ++g) {
+        const uint32_t st = g % S::kStages, ab = g & 1;
+        if ((g >= 2 && !mbar_wait(smem_u32(&acc_empty[ab]), ((g >> 1) - 1) & 1)) ||
+            !mbar_wait(smem_u32(&full[st]), (g / S::kStages) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t ws = smem_u32(sm + (size_t)st * S::kStageBytes);
+        group_mma<kBack, false>(tmem + ab * kNT, ws, ws + kG * kG, 0, a.idesc);
+        mma_commit(smem_u32(&empty[st]));
+        mma_commit(smem_u32(&acc_full[ab]));
+      }
+      if (g > 0) {
+        mma_commit(smem_u32(mma_done));
+        mbar_wait(smem_u32(mma_done), 0);
+      }
+      if (!ok) report(a.err, LORA_DERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
+    const int id = tid - 64, quarter = warp & 3;
+    uint64_t acc[kNT / 2];
+#pragma unroll
+    for (int i = 0; i < kNT / 2; ++i) acc[i] = 0;
+    // factors: thread id of the first kNT works out its token's, a group ahead in shared
+    // memory and one more in registers
+    const bool mine = id < kNT && t0 + id < a.T;
+    const float* const xs = a.xs + (mine ? (t0 + id) * a.xs_t : 0);
+    const float* const ws = a.ws + o0 / kG * a.ws_o;
+    auto factor = [&](int kb) { return mine && kb < k1 ? xs[kb * a.xs_g] * ws[kb * a.ws_g] : 0.f; };
+    if (id < kNT) factors[id] = factor(k0);
+    float coming = factor(k0 + 1);
+    ok = all_promoting(ok);
+    uint32_t g = 0;
+    for (int kb = k0; kb < k1 && ok; ++kb, ++g) {
+      if (id < kNT) factors[((g + 1) & 3) * kNT + id] = coming;
+      coming = factor(kb + 2);
+      const uint32_t ab = g & 1;
+      ok = all_promoting(mbar_wait(smem_u32(&acc_full[ab]), (g >> 1) & 1));
+      if (!ok) break;
+      tc_fence_after();
+      const float* const f = factors + (g & 3) * kNT;
+#pragma unroll
+      for (int c = 0; c < kNT / 16; ++c) {
+        float r[16];
+        tmem_ld16(tmem + ab * kNT + c * 16 + ((uint32_t)(quarter * 32) << 16), r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 p = *reinterpret_cast<const float2*>(f + c * 16 + 2 * i);
+          acc[c * 8 + i] = fma2(pair_of(r[2 * i], r[2 * i + 1]), pair_of(p.x, p.y), acc[c * 8 + i]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&acc_empty[ab]));
+    }
+    if (!ok) {
+      if (id == 0) {
+        report(a.err, LORA_DERR_TIMEOUT);
+        failed = 1;
+      }
+    } else {
+      // this CTA's part of the sum, a token's outputs side by side, where the stages
+      // were (their copies and MMAs are over: the last group's sums have been read)
+      float* const part = reinterpret_cast<float*>(sm);
+      const int row = quarter * 32 + lane;
+#pragma unroll
+      for (int i = 0; i < kNT / 2; ++i) {
+        float u, v;
+        split(acc[i], u, v);
+        part[(2 * i) * kG + row] = u;
+        part[(2 * i + 1) * kG + row] = v;
+      }
+    }
+  }
+  tc_fence_before();
+  if (n > 1) cluster_sync();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kCols);
+  }
+  // the parts added up in rank order: a warp a token, four outputs a lane
+  bool whole = true;
+  for (int q = 0; q < n; ++q) {
+    uint32_t bad;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(bad) : "r"(mapa(smem_u32(&failed), q)) : "memory");
+    whole = whole && bad == 0;
+  }
+  if (whole && k1 >= k0) {
+    for (int j = rank + n * warp; j < kNT && t0 + j < a.T; j += n * (kSThreads / 32)) {
+      const uint32_t at = smem_u32(sm) + (uint32_t)((j * kG + 4 * lane) * 4);
+      float4 p[kSMaxSplit];
+#pragma unroll
+      for (int q = 0; q < kSMaxSplit; ++q)
+        if (q < n) p[q] = ld_dsmem_v4(mapa(at, q));
+      float e[4] = {p[0].x, p[0].y, p[0].z, p[0].w};
+#pragma unroll
+      for (int q = 1; q < kSMaxSplit; ++q)
+        if (q < n) {
+          e[0] += p[q].x;
+          e[1] += p[q].y;
+          e[2] += p[q].z;
+          e[3] += p[q].w;
+        }
+      const int o = o0 + 4 * lane;
+      if (o >= a.outer) continue;
+      const long long dst = (long long)(t0 + j) * a.ldy + o;
+      const bool whole4 = a.wide_store && o + 4 <= a.outer;
+      if (a.f32) {
+        float* const y = static_cast<float*>(a.y) + dst;
+        if (whole4) *reinterpret_cast<float4*>(y) = make_float4(e[0], e[1], e[2], e[3]);
+        else
+          for (int i = 0; i < 4 && o + i < a.outer; ++i) y[i] = e[i];
+      } else {
+        uint16_t* const y = static_cast<uint16_t*>(a.y) + dst;
+        if (whole4) *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]));
+        else
+          for (int i = 0; i < 4 && o + i < a.outer; ++i) y[i] = __bfloat16_as_ushort(__float2bfloat16_rn(e[i]));
+      }
+    }
+  }
+  if (n > 1) cluster_sync();  // no CTA leaves while its part may be read
+}
+
+template <int kNT>
+lora_status_t launch_split(GemmArgs* a, int back, int splits, long long tiles, cudaStream_t s) {
+  const void* f = back ? (const void*)f8_split_kernel<kNT, true> : (const void*)f8_split_kernel<kNT, false>;
+  if (ensure_smem_attr(f, Split<kNT>::kSmem) != cudaSuccess) return LORA_ERR_CUDA;
+  if (tiles * splits > 0x7fffffffLL) return LORA_ERR_UNSUPPORTED;
+  return launch_pdl(f, dim3((unsigned)(tiles * splits)), dim3(kSThreads), Split<kNT>::kSmem, s, splits, a) == cudaSuccess
+             ? LORA_OK
+             : LORA_ERR_CUDA;
+}
+
+}  // namespace
+
+lora_status_t launch_f8_product(const lora_f8_matrix_t* x, const lora_f8_matrix_t* w, void* y, long long ldy, int f32, int back,
+                                int32_t* err, cudaStream_t s) {
+  GemmArgs a;
+  memset(&a, 0, sizeof(a));
+  const int inner = back ? w->rows : w->cols;
+  a.T = x->rows;
+  a.outer = back ? w->cols : w->rows;
+  a.nk = (inner + kG - 1) / kG;
+  a.xs = x->scales;
+  a.xs_t = x->scale_row;
+  a.xs_g = x->scale_col;
+  a.ws = w->scales;
+  a.ws_o = back ? w->scale_col : w->scale_row;
+  a.ws_g = back ? w->scale_row : w->scale_col;
+  a.y = y;
+  a.ldy = ldy;
+  a.f32 = f32;
+  const int size = f32 ? 4 : 2;
+  a.wide_store = reinterpret_cast<uintptr_t>(y) % 16 == 0 && ldy * size % 16 == 0;
+  a.err = err;
+  a.probe = wait_probe_cycles();
+  const int n_o = (a.outer + kG - 1) / kG;
+  const long long m128 = (a.T + kWM - 1) / kWM;
+  const int sms = sm_count();
+  if (m128 * ((n_o + 1) / 2) >= sms / 2 && a.T > kWM) {
+    if (!make_byte_map(&a.xmap, x->codes, a.T, inner, x->ld, kWM)) return LORA_ERR_UNSUPPORTED;
+    if (!make_byte_map(&a.wmap, w->codes, w->rows, w->cols, w->ld, kG)) return LORA_ERR_UNSUPPORTED;
+    a.n_o = (n_o + 1) / 2;
+    if ((m128 + 1) / 2 * a.n_o > 0x7fffffffLL) return LORA_ERR_UNSUPPORTED;
+    a.n_pairs = (int)((m128 + 1) / 2 * a.n_o);
+    a.idesc = idesc_f8(kWM, kWN, x->type, w->type, 0, back);
+    const void* f = back ? (const void*)f8_wide_kernel<true> : (const void*)f8_wide_kernel<false>;
+    if (ensure_smem_attr(f, kWSmem) != cudaSuccess) return LORA_ERR_CUDA;
+    const int clusters = std::min(a.n_pairs, std::max(1, max_active_clusters(f, kWThreads, kWSmem, 2)));
+    return launch_pdl(f, dim3((unsigned)(2 * clusters)), dim3(kWThreads), kWSmem, s, 2, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  }
+  const int nt = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
+  if (!make_byte_map(&a.xmap, x->codes, a.T, inner, x->ld, nt)) return LORA_ERR_UNSUPPORTED;
+  if (!make_byte_map(&a.wmap, w->codes, w->rows, w->cols, w->ld, kG)) return LORA_ERR_UNSUPPORTED;
+  a.n_o = n_o;
+  a.idesc = idesc_f8(kG, nt, w->type, x->type, back, 0);
+  const long long tiles = (long long)n_o * ((a.T + nt - 1) / nt);
+  int splits = 1;
+  while (splits < kSMaxSplit && tiles * splits * 2 <= 2 * sms && a.nk >= 2 * splits) splits *= 2;
+  if (nt == 16) return launch_split<16>(&a, back, splits, tiles, s);
+  if (nt == 32) return launch_split<32>(&a, back, splits, tiles, s);
+  if (nt == 64) return launch_split<64>(&a, back, splits, tiles, s);
+  return launch_split<128>(&a, back, splits, tiles, s);
+}
+
+}  // namespace lora

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "lora_f8.h"
 #include "lora_sgmv.h"
 
 namespace lora {
@@ -152,5 +153,10 @@ lora_status_t launch_shrink_tc(const void* x, long long ldx, float* h, long long
 lora_status_t launch_expand_tc(const float* h, long long ldh, int h_by_token, int after_gather, void* y, long long ldy,
                                const lora_segments_t* seg, const lora_pool_view_t* view, int32_t* err,
                                cudaStream_t stream, float* yf = nullptr, long long ldyf = 0);
+
+// The products of an 8-bit base (f8_gemm.cu): y = x W^T, or x W with back; arguments
+// checked as lora_base_f8 does, at least one row.
+lora_status_t launch_f8_product(const lora_f8_matrix_t* x, const lora_f8_matrix_t* w, void* y, long long ldy, int f32, int back,
+                                int32_t* err, cudaStream_t s);
 
 }  // namespace lora

@@ -97,6 +97,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int b_mn_major) 
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Instruction descriptor of tcgen05.mma.kind::f8f6f4: fp32 accumulator, A and B of
+// e4m3 (0) or e5m2 (1), each K-major (0) or MN-major (1), shape M x N; the same fields.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_type, int b_type, int a_mn_major, int b_mn_major) {
+  return (1u << 4) | ((uint32_t)a_type << 7) | ((uint32_t)b_type << 10) | ((uint32_t)a_mn_major << 15) |
+         ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
 // -------------------------------------------------------------- tcgen05 --
 
 // Allocate `ncols` tensor-memory columns (a power of two >= 32); one whole warp.
@@ -119,6 +126,17 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same of one-byte operands (K = 32 a call).
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -197,6 +215,8 @@ __device__ __forceinline__ uint32_t sw128_offset(int row, int chunk) {
 // offers no encoder or rejects the map; the kernels then copy every tile row by
 // row.
 bool make_act_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows);
+// The same of one-byte elements: boxes of box_rows x 128.
+bool make_byte_map(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows);
 
 // ------------------------------------------------------- long tiles --
 

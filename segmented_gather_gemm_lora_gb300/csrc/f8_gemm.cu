@@ -11,10 +11,12 @@
 // taken as it lies.  Ends inside a tile are the tensor maps' zero fill.
 //
 // Two forms:
-//  - wide: 128 tokens x 256 outputs, tokens down the tile, so a thread's row has one
-//    factor a group and a block of weights (a promotion is one FMA an element).  A
-//    cluster of two CTAs takes two tiles of the same outputs and each loads half of
-//    their weights for both.
+//  - wide: 256 tokens x 256 outputs by a pair of CTAs that share their MMAs
+//    (cta_group::2), tokens down the tile, so a thread's row has one factor a group and a
+//    block of weights (a promotion is one FMA an element).  Each CTA holds half of the
+//    tokens and half of the weights, and all the outputs of its tokens.  (With an MMA a
+//    CTA, 128 x 256, each also reads the other half of the weights: 96 bytes a clock of
+//    operands and as many of copies pass the shared memory's 128.)
 //  - split: few tokens.  128 outputs down the tile (so that every thread of a warpgroup has
 //    work) and 16 to 128 tokens across; a cluster of up to eight CTAs shares the sum
 //    over k and adds its parts up in rank order through distributed shared memory.
@@ -74,15 +76,21 @@ __device__ __forceinline__ uint4 pack_out<float>(const float* f) {
 }
 
 // The four MMAs of one group: descriptors step 32 bytes along a K-major operand, 32
-// rows of 128 bytes along an MN-major one.
-template <bool kAMn, bool kBMn>
-__device__ __forceinline__ void group_mma(uint32_t d, uint32_t as, uint32_t bs, uint32_t b_lbo, uint32_t idesc) {
+// rows of 128 bytes along an MN-major one (which is one swizzle atom of 128 wide).
+template <bool kPair, bool kAMn, bool kBMn>
+__device__ __forceinline__ void group_mma(uint32_t d, uint32_t as, uint32_t bs, uint32_t idesc) {
 #pragma unroll
   for (int kk = 0; kk < kG / 32; ++kk) {
     const uint64_t ad = kAMn ? sdesc_sw128(as + 4096 * kk, 0, 1024) : sdesc_sw128(as + 32 * kk, 16, 1024);
-    const uint64_t bd = kBMn ? sdesc_sw128(bs + 4096 * kk, b_lbo, 1024) : sdesc_sw128(bs + 32 * kk, 16, 1024);
-    mma_f8(d, ad, bd, idesc, kk != 0);
+    const uint64_t bd = kBMn ? sdesc_sw128(bs + 4096 * kk, 0, 1024) : sdesc_sw128(bs + 32 * kk, 16, 1024);
+    if (kPair) mma_f8_pair(d, ad, bd, idesc, kk != 0);
+    else mma_f8(d, ad, bd, idesc, kk != 0);
   }
+}
+
+// Arrive on a barrier of a CTA of the cluster; nothing written is passed on with it.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // Wait (bounded) for the copies of the last `issued` stages that may be under way.
@@ -93,14 +101,14 @@ __device__ __forceinline__ void drain(uint64_t* full, uint32_t issued, int stage
 
 // --------------------------------------------------------------------- wide --
 
-constexpr int kWM = 128, kWN = 256, kWStages = 4;
+constexpr int kWM = 128, kWN = 256, kWStages = 6;
 constexpr int kWEpiWarps = 8;
 constexpr int kWThreads = 128 + 32 * kWEpiWarps;  // warp 0 copies, warp 1 issues MMAs, warps 4-11 promote
 // Registers: 384 threads are launched with 168 each; the first warpgroup gives up 128 x 128
 // of them, which the promoting ones' 128 sums a thread take (64 x 256): 64512 in all, as launched.
 #define LORA_FEWER_REGISTERS() asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory")
 #define LORA_MORE_REGISTERS() asm volatile("setmaxnreg.inc.sync.aligned.u32 232;" ::: "memory")
-constexpr int kWABytes = kWM * kG, kWStageBytes = kWABytes + kWN * kG;
+constexpr int kWABytes = kWM * kG, kWStageBytes = kWABytes + kWN / 2 * kG;
 constexpr size_t kWOffOut = (size_t)kWStages * kWStageBytes;  // a promoting warp's 32 rows of 128 bytes
 constexpr size_t kWOffBars = kWOffOut + (size_t)kWEpiWarps * 4096;
 constexpr size_t kWSmem = kWOffBars + (2 * kWStages + 5) * 8 + 16 + 1024;
@@ -134,14 +142,27 @@ __device__ __forceinline__ void store_rows(const GemmArgs& a, uint8_t* st, const
   __syncwarp();
 }
 
+// Pair p of tiles: bands of kBand x 256 tokens, in a band outputs outermost, so that what
+// runs at once is near square: 76 pairs of 256 x 256 read 8 x 256 rows of x and ten tiles of
+// weights instead of all the weights.
+constexpr int kBand = 8;
+struct Tile {
+  int m, o;  // in tiles of 2 kWM and kWN
+};
+__device__ __forceinline__ Tile tile_of(const GemmArgs& a, int p) {
+  const int band = p / (kBand * a.n_o), in = p - band * kBand * a.n_o;
+  const int rows = min(kBand, a.n_pairs / a.n_o - band * kBand);
+  return Tile{band * kBand + in % rows, in / rows};
+}
+
 template <bool kBack>
 __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_constant__ GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kWOffBars);  // [stages] copied bytes
-  uint64_t* empty = full + kWStages;                             // [stages] both CTAs' MMA commits
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kWOffBars);  // [stages] of the first CTA: both CTAs' copied bytes
+  uint64_t* empty = full + kWStages;                             // [stages] MMA commit
   uint64_t* acc_full = empty + kWStages;                         // [2] MMA commit: a group's sums are complete
-  uint64_t* acc_empty = acc_full + 2;                            // [2] the promoting warps have them
+  uint64_t* acc_empty = acc_full + 2;                            // [2] of the first CTA: both CTAs' promoting warps have them
   uint64_t* mma_done = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -149,23 +170,22 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
   if (tid == 0) {
     for (int s = 0; s < kWStages; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 2);
+      mbar_init(smem_u32(&empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&acc_full[b]), 1);
-      mbar_init(smem_u32(&acc_empty[b]), kWEpiWarps);
+      mbar_init(smem_u32(&acc_empty[b]), 2 * kWEpiWarps);
     }
     mbar_init(smem_u32(mma_done), 1);
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 2 * kWN);
+  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 2 * kWN);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers are there before the peer's copies and commits
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait_then_release();
   bool ok = probe_passes(a);
-  // this CTA's tiles: tokens (2 (p / n_o) + crank), outputs p % n_o of the cluster's pairs p
   if (warp < 4) {
     LORA_FEWER_REGISTERS();
     if (warp == 0 && lane == 0 && ok) {
@@ -173,25 +193,31 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
       prefetch_tensormap(&a.wmap);
       uint32_t g = 0;
       for (int p = (int)cid; p < a.n_pairs && ok; p += (int)ncl) {
-        const int t0 = (2 * (p / a.n_o) + (int)crank) * kWM, o0 = (p % a.n_o) * kWN + (int)crank * kG;
+        const Tile tile = tile_of(a, p);
+        const int t0 = (2 * tile.m + (int)crank) * kWM, o0 = tile.o * kWN + (int)crank * kG;
         for (int kb = 0; kb < a.nk; ++kb, ++g) {
           const uint32_t st = g % kWStages;
           if (g >= kWStages && !mbar_wait(smem_u32(&empty[st]), ((g / kWStages) - 1) & 1)) {
             ok = false;
             break;
           }
-          const uint32_t dst = smem_u32(sm + (size_t)st * kWStageBytes), bar = smem_u32(&full[st]);
-          // this CTA's tokens, and its half of the weights into both CTAs
-          mbar_arrive_expect_tx(bar, kWStageBytes);
-          tma_load_2d(dst, &a.xmap, kb * kG, t0, bar);
-          tma_load_2d_mc(dst + kWABytes + crank * (kG * kG), &a.wmap, kBack ? o0 : kb * kG, kBack ? kb * kG : o0, bar,
-                         (uint16_t)3u);
+          // this CTA's tokens and its half of the weights, counted by the first CTA, which
+          // issues the MMAs (the other's bytes may come before it expects them)
+          const uint32_t dst = smem_u32(sm + (size_t)st * kWStageBytes), bar = mapa(smem_u32(&full[st]), 0);
+          if (crank == 0) mbar_arrive_expect_tx(smem_u32(&full[st]), 2 * kWStageBytes);
+          tma_load_2d_pair(dst, &a.xmap, kb * kG, t0, bar);
+          tma_load_2d_pair(dst + kWABytes, &a.wmap, kBack ? o0 : kb * kG, kBack ? kb * kG : o0, bar);
         }
       }
-      if (!ok) report(a.err, LORA_DERR_TIMEOUT);
-      drain(full, g, kWStages);
+      // the last stages' commits have reached this CTA (so its copies have been read), or,
+      // where a wait ran out, the copies under way have landed
+      for (uint32_t i = g > kWStages ? g - kWStages : 0; i < g && ok; ++i) ok = mbar_wait(smem_u32(&empty[i % kWStages]), (i / kWStages) & 1);
+      if (!ok) {
+        report(a.err, LORA_DERR_TIMEOUT);
+        if (crank == 0) drain(full, g, kWStages);
+      }
     }
-    if (warp == 1 && lane == 0 && ok) {
+    if (warp == 1 && lane == 0 && ok && crank == 0) {
       uint32_t g = 0;
       for (int p = (int)cid; p < a.n_pairs && ok; p += (int)ncl) {
         for (int kb = 0; kb < a.nk; ++kb, ++g) {
@@ -203,13 +229,13 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
           }
           tc_fence_after();
           const uint32_t as = smem_u32(sm + (size_t)st * kWStageBytes);
-          group_mma<false, kBack>(tmem + ab * kWN, as, as + kWABytes, kG * kG, a.idesc);
-          mma_commit_mc(smem_u32(&empty[st]), (uint16_t)3u);  // free in both CTAs once both have read it
-          mma_commit(smem_u32(&acc_full[ab]));
+          group_mma<true, false, kBack>(tmem + ab * kWN, as, as + kWABytes, a.idesc);
+          mma_commit_pair(smem_u32(&empty[st]));
+          mma_commit_pair(smem_u32(&acc_full[ab]));
         }
       }
       if (g > 0) {  // every MMA has completed before tensor memory is freed
-        mma_commit(smem_u32(mma_done));
+        mma_commit_pair(smem_u32(mma_done), 1);
         mbar_wait(smem_u32(mma_done), 0);
       }
       if (!ok) report(a.err, LORA_DERR_TIMEOUT);
@@ -221,8 +247,9 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
     uint8_t* const out = sm + kWOffOut + (size_t)(warp - 4) * 4096;
     uint32_t g = 0;
     for (int p = (int)cid; p < a.n_pairs && ok; p += (int)ncl) {
-      const int t0 = (2 * (p / a.n_o) + (int)crank) * kWM + quarter * 32, t = t0 + lane;
-      const int n0 = (p % a.n_o) * kWN + half * kG;
+      const Tile tile = tile_of(a, p);
+      const int t0 = (2 * tile.m + (int)crank) * kWM + quarter * 32, t = t0 + lane;
+      const int n0 = tile.o * kWN + half * kG;
       const bool row_on = t < a.T, col_on = n0 < a.outer;
       const float* const xs = a.xs + (row_on ? t * a.xs_t : 0);
       const float* const ws = a.ws + (col_on ? n0 / kG * a.ws_o : 0);
@@ -254,14 +281,14 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
         for (int c = 0; c < kG / 32; ++c) {
           uint32_t r[32];
           tmem_ld32_nowait(tmem + ab * kWN + half * kG + c * 32 + ((uint32_t)(quarter * 32) << 16), r);
-          tmem_wait_ld();
+          tmem_wait_ld32(r);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             acc[c * 16 + i] = fma2(pair_of(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[c * 16 + i]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&acc_empty[ab]));
+        if (lane == 0) mbar_arrive_relaxed(mapa(smem_u32(&acc_empty[ab]), 0));
       }
       if (!ok) break;
       const int per = a.f32 ? 32 : 64;  // outputs of 128 bytes
@@ -296,7 +323,7 @@ __global__ void __launch_bounds__(kWThreads, 1) f8_wide_kernel(const __grid_cons
   cluster_sync();  // neither CTA leaves while the peer may still copy into it or arrive on its barriers
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * kWN);
+    tmem_dealloc_pair(tmem, 2 * kWN);
   }
 }
 
@@ -407,7 +434,7 @@ __global__ void __launch_bounds__(kSThreads, 2) f8_split_kernel(const __grid_con
         }
         tc_fence_after();
         const uint32_t ws = smem_u32(sm + (size_t)st * S::kStageBytes);
-        group_mma<kBack, false>(tmem + ab * kNT, ws, ws + kG * kG, 0, a.idesc);
+        group_mma<false, kBack, false>(tmem + ab * kNT, ws, ws + kG * kG, a.idesc);
         mma_commit(smem_u32(&empty[st]));
         mma_commit(smem_u32(&acc_full[ab]));
       }
@@ -566,7 +593,7 @@ lora_status_t launch_f8_product(const lora_f8_matrix_t* x, const lora_f8_matrix_
     a.n_o = (n_o + 1) / 2;
     if ((m128 + 1) / 2 * a.n_o > 0x7fffffffLL) return LORA_ERR_UNSUPPORTED;
     a.n_pairs = (int)((m128 + 1) / 2 * a.n_o);
-    a.idesc = idesc_f8(kWM, kWN, x->type, w->type, 0, back);
+    a.idesc = idesc_f8(2 * kWM, kWN, x->type, w->type, 0, back);
     const void* f = back ? (const void*)f8_wide_kernel<true> : (const void*)f8_wide_kernel<false>;
     if (ensure_smem_attr(f, kWSmem) != cudaSuccess) return LORA_ERR_CUDA;
     const int clusters = std::min(a.n_pairs, std::max(1, max_active_clusters(f, kWThreads, kWSmem, 2)));

@@ -57,40 +57,144 @@ struct QuantArgs {
   const void* x;
   long long ldx;
   lora_f8_matrix_t q;
-  int bf16, pow2;
+  int groups, spans;  // of a row: groups, spans of groups that a warp takes
+  int pow2;
+  int wide;  // rows of x on 16-byte boundaries
   int32_t* err;
 };
 
-__device__ __forceinline__ float value_at(const QuantArgs& a, long long r, int c) {
-  if (a.bf16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.x)[r * a.ldx + c] << 16);
-  return static_cast<const float*>(a.x)[r * a.ldx + c];
+// One 16-byte vector of x: its values, and the largest magnitude's bits.  Entries from
+// `left` on are not there.
+template <typename E>
+struct Vec;
+template <>
+struct Vec<uint16_t> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ uint4 load(const uint16_t* p, int left, bool wide) {
+    if (wide && left >= kN) return *reinterpret_cast<const uint4*>(p);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (i < left) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ uint32_t top(const uint4& v) {
+    // two magnitudes a word, as 16-bit integers
+    const uint32_t m = 0x7fff7fffu;
+    const uint32_t t = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+    return max(t & 0xffff0000u, t << 16);
+  }
+  static __device__ __forceinline__ float get(const uint4& v, int i) {
+    const uint32_t u = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    return i & 1 ? bf_hi(u) : bf_lo(u);
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ uint4 load(const float* p, int left, bool wide) {
+    if (wide && left >= kN) return *reinterpret_cast<const uint4*>(p);
+    return make_uint4(left > 0 ? __float_as_uint(p[0]) : 0, left > 1 ? __float_as_uint(p[1]) : 0,
+                      left > 2 ? __float_as_uint(p[2]) : 0, left > 3 ? __float_as_uint(p[3]) : 0);
+  }
+  static __device__ __forceinline__ uint32_t top(const uint4& v) {
+    const uint32_t m = 0x7fffffffu;
+    return max(max(v.x & m, v.y & m), max(v.z & m, v.w & m));
+  }
+  static __device__ __forceinline__ float get(const uint4& v, int i) {
+    return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+  }
+};
+
+// The codes of a vector (rows of codes start on 16-byte boundaries, groups on 128).
+template <typename E>
+__device__ __forceinline__ void put_codes(uint8_t* dst, const uint4& v, int left, const Inverse& s, int type) {
+  constexpr int kN = Vec<E>::kN;
+  uint32_t w[kN / 4];
+#pragma unroll
+  for (int i = 0; i < kN / 4; ++i)
+    w[i] = pack_f8(quotient(Vec<E>::get(v, 4 * i), s), quotient(Vec<E>::get(v, 4 * i + 1), s), type) |
+           pack_f8(quotient(Vec<E>::get(v, 4 * i + 2), s), quotient(Vec<E>::get(v, 4 * i + 3), s), type) << 16;
+  if (left >= kN) {
+    if constexpr (kN == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (i < left) dst[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+  }
 }
 
-// A CTA a group: rows of it (1 or 128) by 128 columns.
-constexpr int kQThreads = 128;
-__global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_constant__ QuantArgs a) {
+// Rows: a warp takes kSteps vectors a lane of one row: a group is 16 lanes (bf16) or 32.
+constexpr int kQThreads = 256, kSteps = 4;
+template <typename E>
+__global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const __grid_constant__ QuantArgs a) {
+  constexpr int kN = Vec<E>::kN, kLanes = LORA_F8_BLOCK / kN, kPer = 32 / kLanes;  // groups a step
+  pdl_wait_then_release();
+  const int lane = threadIdx.x & 31, in = lane % kLanes;
+  const long long unit = (long long)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5), r = unit / a.spans;
+  if (r >= a.q.rows) return;
+  const int g0 = (int)(unit - r * a.spans) * kSteps * kPer + lane / kLanes;
+  const E* const row = static_cast<const E*>(a.x) + r * a.ldx;
+  uint8_t* const codes = static_cast<uint8_t*>(a.q.codes) + r * a.q.ld;
+  uint4 v[kSteps];
+  uint32_t top[kSteps];
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) {
+    const int c = (g0 + u * kPer) * LORA_F8_BLOCK + in * kN;
+    v[u] = c < a.q.cols ? Vec<E>::load(row + c, a.q.cols - c, a.wide) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) top[u] = Vec<E>::top(v[u]);
+#pragma unroll
+  for (int d = kLanes / 2; d > 0; d >>= 1)
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], d));
+  bool bad = false;
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) {
+    const int g = g0 + u * kPer, c = g * LORA_F8_BLOCK + in * kN;
+    const float s = scale_of(top[u], a.q.type, a.pow2);
+    if (in == 0 && g < a.groups) a.q.scales[r * a.q.scale_row + g * a.q.scale_col] = s;
+    if (c < a.q.cols) put_codes<E>(codes + c, v[u], a.q.cols - c, inverse_of(s), a.q.type);
+    bad |= top[u] >= kInfBits;
+  }
+  if (bad && in == 0) report(a.err, LORA_DERR_NONFINITE);
+}
+
+// Blocks: a CTA a block of 128 x 128, kept in registers between its maximum and its codes.
+template <typename E>
+__global__ void __launch_bounds__(kQThreads) quantize_block_kernel(const __grid_constant__ QuantArgs a) {
+  constexpr int kN = Vec<E>::kN, kLanes = LORA_F8_BLOCK / kN, kRows = kQThreads / kLanes, kVec = LORA_F8_BLOCK / kRows;
   __shared__ uint32_t part[kQThreads / 32];
   pdl_wait_then_release();
-  const int groups = (a.q.cols + LORA_F8_BLOCK - 1) / LORA_F8_BLOCK;
-  const long long b = blockIdx.x / groups;
-  const int g = blockIdx.x % groups, c = g * LORA_F8_BLOCK + threadIdx.x;
-  const long long r0 = b * a.q.block_rows, r1 = min((long long)a.q.rows, r0 + a.q.block_rows);
+  const long long b = blockIdx.x / a.groups, r0 = b * LORA_F8_BLOCK + threadIdx.x / kLanes;
+  const int g = blockIdx.x % a.groups, c = g * LORA_F8_BLOCK + threadIdx.x % kLanes * kN, left = a.q.cols - c;
+  uint4 v[kVec];
   uint32_t top = 0;
-  if (c < a.q.cols)
-    for (long long r = r0; r < r1; ++r) top = max(top, __float_as_uint(value_at(a, r, c)) & 0x7fffffffu);
+#pragma unroll
+  for (int u = 0; u < kVec; ++u) {
+    const long long r = r0 + u * kRows;
+    v[u] = left > 0 && r < a.q.rows ? Vec<E>::load(static_cast<const E*>(a.x) + r * a.ldx + c, left, a.wide) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int u = 0; u < kVec; ++u) top = max(top, Vec<E>::top(v[u]));
   top = __reduce_max_sync(0xffffffffu, top);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
   __syncthreads();
-  top = max(max(part[0], part[1]), max(part[2], part[3]));
+#pragma unroll
+  for (int i = 0; i < kQThreads / 32; ++i) top = max(top, part[i]);
   const float s = scale_of(top, a.q.type, a.pow2);
-  const Inverse v = inverse_of(s);
+  const Inverse inv = inverse_of(s);
   if (threadIdx.x == 0) {
     a.q.scales[b * a.q.scale_row + g * a.q.scale_col] = s;
     if (top >= kInfBits) report(a.err, LORA_DERR_NONFINITE);
   }
-  if (c < a.q.cols)
-    for (long long r = r0; r < r1; ++r)
-      static_cast<uint8_t*>(a.q.codes)[r * a.q.ld + c] = (uint8_t)pack_f8(quotient(value_at(a, r, c), v), 0.f, a.q.type);
+#pragma unroll
+  for (int u = 0; u < kVec; ++u) {
+    const long long r = r0 + u * kRows;
+    if (left > 0 && r < a.q.rows) put_codes<E>(static_cast<uint8_t*>(a.q.codes) + r * a.q.ld + c, v[u], left, inv, a.q.type);
+  }
 }
 
 // -------------------------------------------------------------------- host --
@@ -171,19 +275,28 @@ lora_status_t lora_f8_quantize(const void* x, int64_t ldx, int32_t dtype, const 
   if (overlap(x, bytes, q->codes, code_bytes(*q)) || overlap(x, bytes, q->scales, scale_bytes(*q)) ||
       overlap(q->codes, code_bytes(*q), q->scales, scale_bytes(*q)))
     return LORA_ERR_INVALID_ARG;
-  if (rows * groups > 0x7fffffffLL) return LORA_ERR_UNSUPPORTED;
   QuantArgs a;
   memset(&a, 0, sizeof(a));
   a.x = x;
   a.ldx = ldx;
   a.q = *q;
-  a.bf16 = dtype == LORA_F8_FROM_BF16;
+  a.groups = (int)groups;
   a.pow2 = (flags & LORA_F8_POW2) != 0;
   a.err = dev_err;
-  return launch_pdl((const void*)quantize_kernel, dim3((unsigned)(rows * groups)), dim3(kQThreads), 0, (cudaStream_t)stream,
-                    0, &a) == cudaSuccess
-             ? LORA_OK
-             : LORA_ERR_CUDA;
+  const bool bf16 = dtype == LORA_F8_FROM_BF16;
+  a.wide = aligned_to(x, 16) && ldx * (bf16 ? 2 : 4) % 16 == 0;
+  const void* f;
+  long long ctas;
+  if (q->block_rows == 1) {
+    a.spans = (int)blocks_of(groups, kSteps * (bf16 ? 2 : 1));
+    ctas = blocks_of(rows * a.spans, kQThreads / 32);
+    f = bf16 ? (const void*)quantize_rows_kernel<uint16_t> : (const void*)quantize_rows_kernel<float>;
+  } else {
+    ctas = rows * groups;
+    f = bf16 ? (const void*)quantize_block_kernel<uint16_t> : (const void*)quantize_block_kernel<float>;
+  }
+  if (ctas > 0x7fffffffLL) return LORA_ERR_UNSUPPORTED;
+  return launch_pdl(f, dim3((unsigned)ctas), dim3(kQThreads), 0, (cudaStream_t)stream, 0, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
 
 lora_status_t lora_base_f8(const lora_f8_matrix_t* x, const lora_f8_matrix_t* w, void* y, int64_t ldy, int32_t out_dtype,

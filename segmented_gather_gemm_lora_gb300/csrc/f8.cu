@@ -6,16 +6,16 @@
 // its scale is s = fp32(a / M), or a power of two that a's bits give: M is 1.75 times
 // a power of two for both types, so M 2^e >= a exactly if a's significand is at
 // most 1.75 or e is one more.  A code is that of the correctly rounded quotient
-// x / s: with r the rounded reciprocal of s and q = x r, q + (x - q s) r rounds to it
-// (Markstein), and x - q s is exact where it matters since a >= 2^-64.
-#include <cuda_fp8.h>
-
+// x / s: with r the reciprocal of s and q = x r, q + (x - q s) r rounds to it (Markstein; it
+// could miss only within 2^-22 of a unit of the middle of two fp32), and x - q s is exact
+// where it matters since a >= 2^-64.
 #include <algorithm>
 #include <cstring>
 
 #include "common.cuh"
 #include "internal.h"
 #include "lora_f8.h"
+#include "pairs.cuh"
 
 namespace lora {
 
@@ -26,38 +26,85 @@ namespace {
 constexpr uint32_t kTinyBits = 0x1f800000u;  // 2^-64
 constexpr uint32_t kInfBits = 0x7f800000u;
 
+// fp32(a / M) of a finite a >= 2^-64: with r the rounded 1 / M and q = a r, q + (a - q M) r
+// rounds to it (all 2^23 significands agree with the division).
+template <int kType>
+__device__ __forceinline__ float over_largest(float a) {
+  constexpr float kM = kType == LORA_F8_E4M3 ? 448.f : 57344.f, kR = 1.f / kM;
+  const float q = a * kR;
+  return fmaf(fmaf(-q, kM, a), kR, q);
+}
+
 // The scale of a group whose largest magnitude has these bits.
-__device__ __forceinline__ float scale_of(uint32_t top, int type, bool pow2) {
+template <int kType>
+__device__ __forceinline__ float scale_of(uint32_t top, bool pow2) {
   if (top < kTinyBits) return 0.f;
-  if (top >= kInfBits || !pow2) return __fdiv_rn(__uint_as_float(top), type == LORA_F8_E4M3 ? 448.f : 57344.f);
-  const uint32_t e = (top >> 23) - (type == LORA_F8_E4M3 ? 8 : 15) + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+  if (top >= kInfBits) return __uint_as_float(top);
+  if (!pow2) return over_largest<kType>(__uint_as_float(top));
+  const uint32_t e = (top >> 23) - (kType == LORA_F8_E4M3 ? 8 : 15) + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
   return __uint_as_float(e << 23);
 }
 
+// Of a scale: its negative and its reciprocal, twice each.  The reciprocal of the hardware
+// (a unit off at most) after one Newton step is off by half a unit or a little more.  A
+// scale of 0 has reciprocal 0, so that its quotients are 0.
 struct Inverse {
-  float s, r;
-  bool odd;  // a zero or non-finite scale
+  uint64_t ns, r;
 };
 __device__ __forceinline__ Inverse inverse_of(float s) {
-  const bool odd = !(s > 0.f && s < __uint_as_float(kInfBits));
-  return Inverse{s, odd ? 0.f : __frcp_rn(s), odd};
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  r = s == 0.f ? 0.f : fmaf(fmaf(-s, r, 1.f), r, r);
+  return Inverse{pair_of(-s, -s), pair_of(r, r)};
 }
-__device__ __forceinline__ float quotient(float x, const Inverse& v) {
-  if (v.odd) return v.s == 0.f ? 0.f : __fdiv_rn(x, v.s);
-  const float q = x * v.r;
-  return fmaf(fmaf(-q, v.s, x), v.r, q);
+__device__ __forceinline__ uint64_t quotients(uint64_t x, const Inverse& v) {
+  const uint64_t q = mul2(x, v.r);
+  return fma2(fma2(q, v.ns, x), v.r, q);
 }
 
-// Two codes, `a` in the low byte.
-__device__ __forceinline__ uint32_t pack_f8(float a, float b, int type) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, type == LORA_F8_E4M3 ? __NV_E4M3 : __NV_E5M2);
+// Four codes, the first in the low byte.
+template <int kType>
+__device__ __forceinline__ uint32_t pack_f8(float a, float b, float c, float d) {
+  uint32_t r;
+  if constexpr (kType == LORA_F8_E4M3)
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
+
+// A unit's place, and its step to the next without a division.
+struct Place {
+  long long r;
+  int s;
+  __device__ __forceinline__ void next(int step_r, int step_s, int spans) {
+    r += step_r;
+    s += step_s;
+    if (s >= spans) {
+      s -= spans;
+      ++r;
+    }
+  }
+};
 
 struct QuantArgs {
   const void* x;
   long long ldx;
   lora_f8_matrix_t q;
-  int groups, spans;  // of a row: groups, spans of groups that a warp takes
+  int groups;       // of a row
+  long long units;  // rows of blocks x spans: what a warp (or, of blocks, a CTA) takes at once
+  int spans;        // of a row of units
+  int step_r, step_s;  // from a unit to its taker's next one
   int pow2;
   int wide;  // rows of x on 16-byte boundaries
   int32_t* err;
@@ -84,9 +131,10 @@ struct Vec<uint16_t> {
     const uint32_t t = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
     return max(t & 0xffff0000u, t << 16);
   }
-  static __device__ __forceinline__ float get(const uint4& v, int i) {
-    const uint32_t u = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
-    return i & 1 ? bf_hi(u) : bf_lo(u);
+  // elements 2 i and 2 i + 1
+  static __device__ __forceinline__ uint64_t pair(const uint4& v, int i) {
+    const uint32_t u = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return pair_of(bf_lo(u), bf_hi(u));
   }
 };
 template <>
@@ -101,20 +149,31 @@ struct Vec<float> {
     const uint32_t m = 0x7fffffffu;
     return max(max(v.x & m, v.y & m), max(v.z & m, v.w & m));
   }
-  static __device__ __forceinline__ float get(const uint4& v, int i) {
-    return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+  static __device__ __forceinline__ uint64_t pair(const uint4& v, int i) {
+    return i == 0 ? pair_of(__uint_as_float(v.x), __uint_as_float(v.y)) : pair_of(__uint_as_float(v.z), __uint_as_float(v.w));
   }
 };
 
-// The codes of a vector (rows of codes start on 16-byte boundaries, groups on 128).
-template <typename E>
-__device__ __forceinline__ void put_codes(uint8_t* dst, const uint4& v, int left, const Inverse& s, int type) {
+// The codes of a vector of a group with scale s (rows of codes start on 16-byte boundaries,
+// groups on 128).
+template <typename E, int kType>
+__device__ __forceinline__ void put_codes(uint8_t* dst, const uint4& v, int left, float s, const Inverse& inv) {
   constexpr int kN = Vec<E>::kN;
+  const bool finite = s < __uint_as_float(kInfBits);
   uint32_t w[kN / 4];
 #pragma unroll
-  for (int i = 0; i < kN / 4; ++i)
-    w[i] = pack_f8(quotient(Vec<E>::get(v, 4 * i), s), quotient(Vec<E>::get(v, 4 * i + 1), s), type) |
-           pack_f8(quotient(Vec<E>::get(v, 4 * i + 2), s), quotient(Vec<E>::get(v, 4 * i + 3), s), type) << 16;
+  for (int i = 0; i < kN / 4; ++i) {
+    float e[4];
+    split(quotients(Vec<E>::pair(v, 2 * i), inv), e[0], e[1]);
+    split(quotients(Vec<E>::pair(v, 2 * i + 1), inv), e[2], e[3]);
+    if (!finite) {  // by the division itself: 0, or NaN from what is not finite
+      split(Vec<E>::pair(v, 2 * i), e[0], e[1]);
+      split(Vec<E>::pair(v, 2 * i + 1), e[2], e[3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = fabsf(e[j]) < __uint_as_float(kInfBits) && s == s ? copysignf(0.f, e[j]) : s - s;
+    }
+    w[i] = pack_f8<kType>(e[0], e[1], e[2], e[3]);
+  }
   if (left >= kN) {
     if constexpr (kN == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(dst) = w[0];
@@ -125,79 +184,121 @@ __device__ __forceinline__ void put_codes(uint8_t* dst, const uint4& v, int left
   }
 }
 
-// Rows: a warp takes kSteps vectors a lane of one row: a group is 16 lanes (bf16) or 32.
-constexpr int kQThreads = 256, kSteps = 4;
-template <typename E>
+// Rows: a warp takes kSteps vectors a lane of one row at a time (a group is 16 lanes for
+// bf16, 32 for fp32), and has the next ones on their way meanwhile.
+constexpr int kQThreads = 256, kSteps = 4, kRowCtas = 6;  // CTAs an SM in a grid
+template <typename E, int kType>
 __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const __grid_constant__ QuantArgs a) {
   constexpr int kN = Vec<E>::kN, kLanes = LORA_F8_BLOCK / kN, kPer = 32 / kLanes;  // groups a step
   pdl_wait_then_release();
   const int lane = threadIdx.x & 31, in = lane % kLanes;
-  const long long unit = (long long)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5), r = unit / a.spans;
-  if (r >= a.q.rows) return;
-  const int g0 = (int)(unit - r * a.spans) * kSteps * kPer + lane / kLanes;
-  const E* const row = static_cast<const E*>(a.x) + r * a.ldx;
-  uint8_t* const codes = static_cast<uint8_t*>(a.q.codes) + r * a.q.ld;
-  uint4 v[kSteps];
-  uint32_t top[kSteps];
+  const long long stride = (long long)gridDim.x * (kQThreads / 32);
+  long long unit = (long long)blockIdx.x * (kQThreads / 32) + (threadIdx.x >> 5);
+  Place at{unit / a.spans, (int)(unit % a.spans)};
+  auto load = [&](bool on, const Place& p, uint4 (&v)[kSteps]) {
+    const int g0 = p.s * kSteps * kPer + lane / kLanes;
+    const E* const row = static_cast<const E*>(a.x) + p.r * a.ldx;
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int c = (g0 + u * kPer) * LORA_F8_BLOCK + in * kN;
-    v[u] = c < a.q.cols ? Vec<E>::load(row + c, a.q.cols - c, a.wide) : make_uint4(0, 0, 0, 0);
-  }
-#pragma unroll
-  for (int u = 0; u < kSteps; ++u) top[u] = Vec<E>::top(v[u]);
-#pragma unroll
-  for (int d = kLanes / 2; d > 0; d >>= 1)
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u) top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], d));
+    for (int u = 0; u < kSteps; ++u) {
+      const int c = (g0 + u * kPer) * LORA_F8_BLOCK + in * kN;
+      v[u] = on && c < a.q.cols ? Vec<E>::load(row + c, a.q.cols - c, a.wide) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  uint4 v[kSteps], next[kSteps];
+  load(unit < a.units, at, v);
   bool bad = false;
+  for (; unit < a.units; unit += stride) {
+    const long long r = at.r;
+    const int g0 = at.s * kSteps * kPer + lane / kLanes;
+    at.next(a.step_r, a.step_s, a.spans);
+    load(unit + stride < a.units, at, next);
+    uint8_t* const codes = static_cast<uint8_t*>(a.q.codes) + r * a.q.ld;
+    uint32_t top[kSteps];
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int g = g0 + u * kPer, c = g * LORA_F8_BLOCK + in * kN;
-    const float s = scale_of(top[u], a.q.type, a.pow2);
-    if (in == 0 && g < a.groups) a.q.scales[r * a.q.scale_row + g * a.q.scale_col] = s;
-    if (c < a.q.cols) put_codes<E>(codes + c, v[u], a.q.cols - c, inverse_of(s), a.q.type);
-    bad |= top[u] >= kInfBits;
+    for (int u = 0; u < kSteps; ++u) top[u] = Vec<E>::top(v[u]);
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1)
+#pragma unroll
+      for (int u = 0; u < kSteps; ++u) top[u] = max(top[u], __shfl_xor_sync(0xffffffffu, top[u], d));
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      const int g = g0 + u * kPer, c = g * LORA_F8_BLOCK + in * kN;
+      const float s = scale_of<kType>(top[u], a.pow2);
+      if (in == 0 && g < a.groups) a.q.scales[r * a.q.scale_row + g * a.q.scale_col] = s;
+      if (c < a.q.cols) put_codes<E, kType>(codes + c, v[u], a.q.cols - c, s, inverse_of(s));
+      bad |= top[u] >= kInfBits;
+      v[u] = next[u];
+    }
   }
   if (bad && in == 0) report(a.err, LORA_DERR_NONFINITE);
 }
 
-// Blocks: a CTA a block of 128 x 128, kept in registers between its maximum and its codes.
+// Blocks: a CTA a block of 128 x 128, kept in registers between its maximum and its codes
+// while the next one's values are on their way.
+// Threads of its CTA: eight vectors each.
 template <typename E>
-__global__ void __launch_bounds__(kQThreads) quantize_block_kernel(const __grid_constant__ QuantArgs a) {
-  constexpr int kN = Vec<E>::kN, kLanes = LORA_F8_BLOCK / kN, kRows = kQThreads / kLanes, kVec = LORA_F8_BLOCK / kRows;
-  __shared__ uint32_t part[kQThreads / 32];
+constexpr int kBThreads = LORA_F8_BLOCK * LORA_F8_BLOCK / 8 / Vec<E>::kN;
+template <typename E, int kType>
+__global__ void __launch_bounds__(kBThreads<E>, 512 / kBThreads<E>) quantize_block_kernel(const __grid_constant__ QuantArgs a) {
+  constexpr int kN = Vec<E>::kN, kLanes = LORA_F8_BLOCK / kN, kRows = kBThreads<E> / kLanes, kVec = LORA_F8_BLOCK / kRows;
+  __shared__ uint32_t part[2][kBThreads<E> / 32];
   pdl_wait_then_release();
-  const long long b = blockIdx.x / a.groups, r0 = b * LORA_F8_BLOCK + threadIdx.x / kLanes;
-  const int g = blockIdx.x % a.groups, c = g * LORA_F8_BLOCK + threadIdx.x % kLanes * kN, left = a.q.cols - c;
-  uint4 v[kVec];
-  uint32_t top = 0;
+  const int in_row = threadIdx.x / kLanes, in_col = threadIdx.x % kLanes * kN;
+  auto load = [&](bool on, const Place& p, uint4 (&v)[kVec]) {
+    const long long r0 = p.r * LORA_F8_BLOCK + in_row;
+    const int c = p.s * LORA_F8_BLOCK + in_col, left = a.q.cols - c;
+    const E* const x = static_cast<const E*>(a.x) + c;
 #pragma unroll
-  for (int u = 0; u < kVec; ++u) {
-    const long long r = r0 + u * kRows;
-    v[u] = left > 0 && r < a.q.rows ? Vec<E>::load(static_cast<const E*>(a.x) + r * a.ldx + c, left, a.wide) : make_uint4(0, 0, 0, 0);
-  }
+    for (int u = 0; u < kVec; ++u) {
+      const long long r = r0 + u * kRows;
+      v[u] = on && left > 0 && r < a.q.rows ? Vec<E>::load(x + r * a.ldx, left, a.wide) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  uint4 v[kVec], next[kVec];
+  Place at{blockIdx.x / a.spans, (int)(blockIdx.x % a.spans)};
+  load(true, at, v);
+  int turn = 0;
+  for (long long unit = blockIdx.x; unit < a.units; unit += gridDim.x, turn ^= 1) {
+    const long long b = at.r;
+    const int g = at.s;
+    at.next(a.step_r, a.step_s, a.spans);
+    load(unit + gridDim.x < a.units, at, next);
+    uint32_t top = 0;
 #pragma unroll
-  for (int u = 0; u < kVec; ++u) top = max(top, Vec<E>::top(v[u]));
-  top = __reduce_max_sync(0xffffffffu, top);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
-  __syncthreads();
+    for (int u = 0; u < kVec; ++u) top = max(top, Vec<E>::top(v[u]));
+    top = __reduce_max_sync(0xffffffffu, top);
+    // (two sets of places: a warp can be one block ahead of the slowest, not two)
+    if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = top;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kQThreads / 32; ++i) top = max(top, part[i]);
-  const float s = scale_of(top, a.q.type, a.pow2);
-  const Inverse inv = inverse_of(s);
-  if (threadIdx.x == 0) {
-    a.q.scales[b * a.q.scale_row + g * a.q.scale_col] = s;
-    if (top >= kInfBits) report(a.err, LORA_DERR_NONFINITE);
-  }
+    for (int i = 0; i < kBThreads<E> / 32; ++i) top = max(top, part[turn][i]);
+    const long long r0 = b * LORA_F8_BLOCK + in_row;
+    const int c = g * LORA_F8_BLOCK + in_col, left = a.q.cols - c;
+    const float s = scale_of<kType>(top, a.pow2);
+    const Inverse inv = inverse_of(s);
+    if (threadIdx.x == 0) {
+      a.q.scales[b * a.q.scale_row + g * a.q.scale_col] = s;
+      if (top >= kInfBits) report(a.err, LORA_DERR_NONFINITE);
+    }
 #pragma unroll
-  for (int u = 0; u < kVec; ++u) {
-    const long long r = r0 + u * kRows;
-    if (left > 0 && r < a.q.rows) put_codes<E>(static_cast<uint8_t*>(a.q.codes) + r * a.q.ld + c, v[u], left, inv, a.q.type);
+    for (int u = 0; u < kVec; ++u) {
+      const long long r = r0 + u * kRows;
+      if (left > 0 && r < a.q.rows) put_codes<E, kType>(static_cast<uint8_t*>(a.q.codes) + r * a.q.ld + c, v[u], left, s, inv);
+      v[u] = next[u];
+    }
   }
 }
 
 // -------------------------------------------------------------------- host --
+
+template <typename E>
+const void* rows_kernel(int type) {
+  return type == LORA_F8_E4M3 ? (const void*)quantize_rows_kernel<E, LORA_F8_E4M3> : (const void*)quantize_rows_kernel<E, LORA_F8_E5M2>;
+}
+template <typename E>
+const void* block_kernel(int type) {
+  return type == LORA_F8_E4M3 ? (const void*)quantize_block_kernel<E, LORA_F8_E4M3> : (const void*)quantize_block_kernel<E, LORA_F8_E5M2>;
+}
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -285,18 +386,16 @@ lora_status_t lora_f8_quantize(const void* x, int64_t ldx, int32_t dtype, const 
   a.err = dev_err;
   const bool bf16 = dtype == LORA_F8_FROM_BF16;
   a.wide = aligned_to(x, 16) && ldx * (bf16 ? 2 : 4) % 16 == 0;
-  const void* f;
-  long long ctas;
-  if (q->block_rows == 1) {
-    a.spans = (int)blocks_of(groups, kSteps * (bf16 ? 2 : 1));
-    ctas = blocks_of(rows * a.spans, kQThreads / 32);
-    f = bf16 ? (const void*)quantize_rows_kernel<uint16_t> : (const void*)quantize_rows_kernel<float>;
-  } else {
-    ctas = rows * groups;
-    f = bf16 ? (const void*)quantize_block_kernel<uint16_t> : (const void*)quantize_block_kernel<float>;
-  }
-  if (ctas > 0x7fffffffLL) return LORA_ERR_UNSUPPORTED;
-  return launch_pdl(f, dim3((unsigned)ctas), dim3(kQThreads), 0, (cudaStream_t)stream, 0, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  const bool by_rows = q->block_rows == 1;
+  a.spans = by_rows ? (int)blocks_of(groups, kSteps * (bf16 ? 2 : 1)) : a.groups;
+  a.units = rows * a.spans;
+  const int takers = by_rows ? kQThreads / 32 : 1;  // of a CTA
+  const long long ctas = std::min(blocks_of(a.units, takers), (long long)sm_count() * (by_rows ? kRowCtas : bf16 ? 2 : 1));
+  a.step_r = (int)(ctas * takers / a.spans);
+  a.step_s = (int)(ctas * takers % a.spans);
+  const void* f = by_rows ? (bf16 ? rows_kernel<uint16_t>(q->type) : rows_kernel<float>(q->type))
+                          : (bf16 ? block_kernel<uint16_t>(q->type) : block_kernel<float>(q->type));
+  return launch_pdl(f, dim3((unsigned)ctas), dim3((unsigned)(by_rows ? kQThreads : bf16 ? kBThreads<uint16_t> : kBThreads<float>)), 0, (cudaStream_t)stream, 0, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
 
 lora_status_t lora_base_f8(const lora_f8_matrix_t* x, const lora_f8_matrix_t* w, void* y, int64_t ldy, int32_t out_dtype,

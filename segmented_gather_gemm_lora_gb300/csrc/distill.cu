@@ -1,4 +1,4 @@
-// A teacher's top logits and the distillation loss (lora_train.h).
+// The distillation loss (lora_train.h).
 //
 // With d = log p - log q of an outcome, a term of a divergence is
 //     KL(p | q): p log(p / q) - p + q = p h(-d),   h(x) = e^x - 1 - x,
@@ -202,76 +202,6 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const __grid_constant
   }
 }
 
-// --------------------------------------------------------------------- top k --
-
-struct TopkArgs {
-  const void* logits;
-  long long ld;
-  const int32_t* labels;
-  int T, V, k;
-  float inv;  // 1 / temperature
-  int32_t* ids;
-  float* values;
-  float* tail;
-  int32_t* err;
-};
-
-// Keys that order as the listing does: by value (a NaN first, -0 as +0), then by rising index.
-__device__ __forceinline__ uint32_t key_of(float x) {
-  if (x != x) return 0xffffffffu;
-  const uint32_t b = __float_as_uint(x + 0.f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-
-template <typename E>
-__global__ void __launch_bounds__(kThreads) topk_kernel(const __grid_constant__ TopkArgs a) {
-  __shared__ unsigned long long best[kWarps];
-  __shared__ float sh[kWarps];
-  pdl_wait_then_release();
-  const int t = blockIdx.x, tid = threadIdx.x, V = a.V;
-  const E* row = static_cast<const E*>(a.logits) + (long long)t * a.ld;
-  const long long o = (long long)t * a.k;
-  if (a.labels != nullptr && a.labels[t] < 0) {
-    if (tid < a.k) {
-      a.ids[o + tid] = -1;
-      a.values[o + tid] = -INF_F;
-    }
-    if (tid == 0 && a.tail != nullptr) a.tail[t] = -INF_F;
-    return;
-  }
-  unsigned long long last = ~0ull;
-  for (int j = 0; j < a.k; ++j) {
-    unsigned long long top = 0;
-    for (int v = tid; v < V; v += kThreads) {
-      const unsigned long long key = (unsigned long long)key_of(Elem<E>::get(row[v])) << 32 | (uint32_t)~v;
-      if ((j == 0 || key < last) && key > top) top = key;
-    }
-    for (int d = 16; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    __syncthreads();
-    if ((tid & 31) == 0) best[tid >> 5] = top;
-    __syncthreads();
-    for (int i = 0; i < kWarps; ++i) top = max(top, best[i]);
-    last = top;
-    if (tid == 0) {
-      const int v = (int)~(uint32_t)top;
-      const float x = Elem<E>::get(row[v]);
-      a.ids[o + j] = x == -INF_F ? -1 : v;
-      a.values[o + j] = x;
-    }
-  }
-  if (a.tail == nullptr) return;
-  auto listed = [&](int v) { return ((unsigned long long)key_of(Elem<E>::get(row[v])) << 32 | (uint32_t)~v) >= last; };
-  float top = -INF_F;
-  for (int v = tid; v < V; v += kThreads)
-    if (!listed(v)) top = fmaxf(top, Elem<E>::get(row[v]));
-  top = base_of(block_max(top, sh));
-  float s = 0.f;
-  for (int v = tid; v < V; v += kThreads)
-    if (!listed(v)) s += expf((Elem<E>::get(row[v]) - top) * a.inv);
-  s = block_add(s, sh);
-  if (tid == 0) a.tail[t] = top * a.inv + logf(s);
-}
-
 }  // namespace
 
 }  // namespace lora
@@ -279,33 +209,6 @@ __global__ void __launch_bounds__(kThreads) topk_kernel(const __grid_constant__ 
 using namespace lora;
 
 extern "C" {
-
-lora_status_t lora_topk_logits(const void* logits, int64_t ld, int32_t dtype, const int32_t* labels, int32_t T, int32_t V,
-                               int32_t k, float temperature, int32_t* ids, float* values, float* tail, int32_t* dev_err,
-                               lora_stream_t stream) {
-  // labels may be missing: the logits' own address stands for them in the check
-  const lora_status_t st = check_logits(logits, ld, dtype, labels != nullptr ? labels : ids, T, V);
-  if (st != LORA_OK) return st;
-  if (k < 1 || k > V || !(temperature > 0.f) || temperature == INFINITY) return LORA_ERR_INVALID_ARG;
-  if (k > LORA_TOPK_MAX) return LORA_ERR_UNSUPPORTED;
-  if (T == 0) return LORA_OK;
-  if (!f32_ok(ids) || !f32_ok(values) || !aligned_to(tail, 4)) return LORA_ERR_INVALID_ARG;
-  TopkArgs a;
-  memset(&a, 0, sizeof(a));
-  a.logits = logits;
-  a.ld = ld;
-  a.labels = labels;
-  a.T = T;
-  a.V = V;
-  a.k = k;
-  a.inv = 1.f / temperature;
-  a.ids = ids;
-  a.values = values;
-  a.tail = tail;
-  a.err = dev_err;
-  const void* f = dtype == LORA_LOGITS_BF16 ? (const void*)topk_kernel<uint16_t> : (const void*)topk_kernel<float>;
-  return launch_pdl(f, dim3((unsigned)T), dim3(kThreads), 0, (cudaStream_t)stream, 0, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
-}
 
 lora_status_t lora_distill_loss(const void* logits, int64_t ld, int32_t dtype, const int32_t* ids, const float* values,
                                 const float* tail, int32_t k, const int32_t* labels, const float* weight, int32_t T,

@@ -1,17 +1,16 @@
 // A teacher's top logits (lora_train.h): the k largest entries of each row, and the
 // log of the sum of exponentials of the others.
 //
-// A row is read once, by one CTA or by the CTAs of a cluster, in chunks of four vectors
-// a thread with the next chunk on its way.  Each warp keeps the 32 largest of its entries
-// seen so far in order across its lanes.  With m = k / 8 rounded up, the least of the
-// eight warps' m-th entries has k entries at or above it: what is below this threshold,
-// which the warps exchange every few chunks, is not listed and goes into the sum at
-// once.  The few others go to the warp's segment of a list in shared memory.  At the end
-// the k-th largest of the CTA's 256 ranked entries is a threshold that passes few more
-// than k; what it stops goes into the sum too, the rest is placed by counting.  A segment
-// that would overflow (rising rows, ties by the thousand) is cut to the warp's k best,
-// found bit by bit.  So the sum is of exactly the entries that are not listed, no
-// difference of large sums; and every place and every sum's order is fixed.
+// A row is read by one CTA or by the CTAs of a cluster.  A thread reads its vectors in up
+// to sixteen slots and leaves of each slot only its largest entry and its sum of
+// exponentials over that: no entry is looked at by itself.  The k-th largest of the
+// slots' maxima has k entries at or above it, so a slot below it has nothing to list and
+// its sum stands; the others, k and those that tie with them, are read again and their
+// entries below the threshold summed.  So the sum is of exactly the entries that are not
+// listed, no difference of large sums.  What is listed is placed by counting.
+// A row in which too many entries tie or crowd in few slots takes the slow way: a radix
+// selection of the k best by passes over the row.
+// Places and orders of sums are fixed: the same inputs give the same bits.
 //
 // Keys are the values' bits made to order as integers; composite keys order as the
 // listing does, no two alike.
@@ -35,11 +34,10 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kVec = 4;                           // vectors a thread takes at once
-constexpr int kSeg = 320;                         // entries of a warp's segment: its k best and some more
-constexpr int kSlots = kWarps * kSeg / kThreads;  // entries a thread looks after in a cut
-static_assert(kSlots * kThreads >= kMaxCluster * LORA_TOPK_MAX, "the cluster's entries too");
-constexpr int kKept = LORA_TOPK_MAX / kWarps;     // of a segment, after a cut
-static_assert(kSeg >= LORA_TOPK_MAX, "a warp's k best");
+constexpr int kRows = 16;                         // slots of a thread; one more for the row's edges
+constexpr int kListed = 512;                      // slots that are read again
+constexpr int kBest = kMaxCluster * LORA_TOPK_MAX;  // entries that are placed
+constexpr int kSlots = kBest / kThreads;          // of them, a thread's in a cut
 constexpr int kResident = 3;                      // CTAs an SM
 constexpr float kLowest = -3.402823466e38f;  // below it only -inf, which is not listed
 
@@ -67,13 +65,6 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   if (key == 0xffffffffu) return __int_as_float(0x7fffffff);
   return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
-// A threshold at or below the values of keys from `key` on.
-__device__ __forceinline__ float threshold_of(uint32_t key) {
-  if (key >= 0xff800000u) return INF_F;  // +inf's key, or a NaN's
-  const float x = value_of(key);
-  return x >= kLowest ? x : kLowest;
-}
-
 struct alignas(8) Entry {  // (read across the cluster in one piece)
   uint32_t key;
   int idx;
@@ -86,21 +77,21 @@ __device__ __forceinline__ Entry entry_of(unsigned long long c) { return Entry{(
 
 struct TopShared {
   uint64_t probe_bar;
-  Entry list[kWarps * kSeg];
-  int count[kWarps];  // entries of each segment
+  float2 slot[kRows + 1][kThreads];  // the largest entry; sum of exponentials over it
+  alignas(16) uint32_t key[kListed];  // of the slots that may be read again
+  uint16_t which[kListed];
   uint32_t hist[2][256];
   int scan[kWarps];
   Sum part[kWarps];
   alignas(8) Sum sum;              // the CTA's
-  uint32_t least[2][kWarps];       // the warps' m-th keys
-  alignas(16) uint32_t ranked[kThreads];  // the warps' 32 largest
+  uint32_t least[kWarps];          // the warps' m-th keys
   uint32_t bound[kMaxCluster];     // the cluster's CTAs' thresholds
+  uint32_t threshold[2];           // of k entries, of a CTA's share of them
   int total;                       // entries in best
-  alignas(16) unsigned long long best[kMaxCluster * LORA_TOPK_MAX + 2];  // composite keys, then two zeros
+  alignas(16) unsigned long long best[kBest + 2];  // composite keys, then two zeros
 };
-
-static_assert(offsetof(TopShared, best) % 16 == 0 && offsetof(TopShared, list) % 8 == 0 && offsetof(TopShared, sum) % 8 == 0,
-              "eight bytes at a time");
+static_assert(offsetof(TopShared, best) % 16 == 0 && offsetof(TopShared, key) % 16 == 0 && offsetof(TopShared, sum) % 8 == 0,
+              "read in one piece");
 
 // Terms exp((x - base) / temperature).
 struct Terms {
@@ -111,6 +102,10 @@ struct Terms {
     const float base = base_of(r.m);
     r.s = x.s * expf((x.m - base) * inv) + y.s * expf((y.m - base) * inv);
     return r;
+  }
+  __device__ __forceinline__ float power(float x, float base) const {  // of finite base
+    const float d = x - base;
+    return ex2(fmaf(d, hi, d * lo));
   }
   __device__ __forceinline__ Sum add(const Sum& t, float x) const {
     return join(t, Sum{x, x == x ? (x == -INF_F ? 0.f : x == INF_F ? x : 1.f) : x});
@@ -160,32 +155,6 @@ __device__ __forceinline__ float top_nan(const uint4& v, float) {
   return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
 }
 
-// Which elements of a vector do not lie below `least`, and a vector without some.
-__device__ __forceinline__ uint32_t reaching(const uint4& v, float least, uint16_t) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t w = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
-    m |= (bf_lo(w) < least ? 0u : 1u << (2 * k)) | (bf_hi(w) < least ? 0u : 2u << (2 * k));
-  }
-  return m;
-}
-__device__ __forceinline__ uint32_t reaching(const uint4& v, float least, float) {
-  return (__uint_as_float(v.x) < least ? 0u : 1u) | (__uint_as_float(v.y) < least ? 0u : 2u) |
-         (__uint_as_float(v.z) < least ? 0u : 4u) | (__uint_as_float(v.w) < least ? 0u : 8u);
-}
-__device__ __forceinline__ uint32_t without(uint32_t w, uint32_t which) {  // of a word's two
-  if (which & 1) w = (w & 0xffff0000u) | 0xff80u;
-  if (which & 2) w = (w & 0xffffu) | 0xff800000u;
-  return w;
-}
-__device__ __forceinline__ uint4 without(const uint4& v, uint32_t m, uint16_t) {
-  return make_uint4(without(v.x, m), without(v.y, m >> 2), without(v.z, m >> 4), without(v.w, m >> 6));
-}
-__device__ __forceinline__ uint4 without(const uint4& v, uint32_t m, float) {
-  return make_uint4(m & 1 ? 0xff800000u : v.x, m & 2 ? 0xff800000u : v.y, m & 4 ? 0xff800000u : v.z, m & 8 ? 0xff800000u : v.w);
-}
-
 // The warp's keys in falling order (a bitonic network).
 __device__ __forceinline__ uint32_t sort_lanes(uint32_t key, int lane) {
 #pragma unroll
@@ -196,17 +165,6 @@ __device__ __forceinline__ uint32_t sort_lanes(uint32_t key, int lane) {
       const bool up = (lane & size) != 0 && size < 32, low = (lane & d) == 0;
       key = low != up ? max(key, o) : min(key, o);
     }
-  return key;
-}
-
-// The 32 largest of two lists of 32, both in falling order across the lanes.
-__device__ __forceinline__ uint32_t merge_lanes(uint32_t a, uint32_t b, int lane) {
-  uint32_t key = max(a, __shfl_sync(0xffffffffu, b, 31 - lane));  // rises and falls, or the other way round
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    const uint32_t o = __shfl_xor_sync(0xffffffffu, key, d);
-    key = (lane & d) == 0 ? max(key, o) : min(key, o);
-  }
   return key;
 }
 
@@ -275,92 +233,119 @@ __device__ __forceinline__ unsigned long long digits(const Entry& e) {
 }
 template <typename E>
 constexpr int kFirstDigit = sizeof(E) == 2 ? 40 : 56;
-template <typename E>
-__device__ __forceinline__ uint32_t key_of_digits(unsigned long long d) {
-  // (a negative bf16's key ends in ones: the zeros are below it)
-  return sizeof(E) == 2 ? (uint32_t)(d >> 32) << 16 : (uint32_t)(d >> 32);
-}
-
-// Cut entries (a thread's e[i] where `on` has bit i; `total` in all) to the k best; what
-// goes is added to *t, what stays is put(place, entry) in the order of (thread, i), with a
-// barrier between the last read and the first put.  Returns the new threshold (or the old
-// one, of no more than k).
-template <typename E, typename Put>
-__device__ __forceinline__ float cut(TopShared* sh, const Entry (&e)[kSlots], uint32_t on, int total, int k, float threshold,
-                                     const Terms& terms, Sum* t, Put put) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (total > k) {
-    unsigned long long c[kSlots];
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i) c[i] = digits<E>(e[i]);
-    const unsigned long long least = select_top<kSlots, kFirstDigit<E>, 0>(c, [&](int i) { return on >> i & 1; }, k, sh);
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if ((on >> i & 1) && c[i] < least) {
-        on &= ~(1u << i);
-        if (terms.inv > 0.f) *t = terms.add(*t, value_of(e[i].key));
-      }
-    threshold = fmaxf(threshold, threshold_of(key_of_digits<E>(least)));
-  }
-  const int mine = __popc(on);
+// Where this thread's `mine` places begin among the CTA's, in the order of threads, and
+// how many there are.  (Two barriers.)
+__device__ __forceinline__ int places(int mine, TopShared* sh, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int before = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int o = __shfl_up_sync(0xffffffffu, before, d);
     if (lane >= d) before += o;
   }
+  __syncthreads();
   if (lane == 31) sh->scan[warp] = before;
+  __syncthreads();
   before -= mine;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) before += sh->scan[w];
+  int all = 0;
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i)
-    if (on >> i & 1) put(before++, e[i]);
-  return threshold;
-}
-
-// The list cut to its k best: segment w then has entries 32 w .. of them.
-template <typename E>
-__device__ __noinline__ float cut_list(TopShared* sh, int k, float threshold, const Terms& terms, Sum* t) {
-  const int tid = threadIdx.x;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sh->count[w];
-  Entry e[kSlots];
-  uint32_t on = 0;
-#pragma unroll
-  for (int i = 0; i < kSlots; ++i) {
-    const int slot = i * kThreads + tid, seg = slot / kSeg;
-    e[i] = sh->list[slot];
-    if (slot - seg * kSeg < sh->count[seg]) on |= 1u << i;
+  for (int w = 0; w < kWarps; ++w) {
+    before += w < warp ? sh->scan[w] : 0;
+    all += sh->scan[w];
   }
-  threshold = cut<E>(sh, e, on, total, k, threshold, terms, t,
-                     [&](int at, const Entry& x) { sh->list[at / kKept * kSeg + at % kKept] = x; });
-  if (tid < kWarps) sh->count[tid] = min(max(min(total, k) - tid * kKept, 0), kKept);
-  __syncthreads();
-  return threshold;
+  *total = all;
+  return before;
 }
 
-// The entries of best, N of them, cut to the k best.
+// The entries of best, `total` of them and more than k, cut to the k best; what goes is
+// added to *t.
 template <typename E>
-__device__ __noinline__ void cut_best(TopShared* sh, int N, int k, const Terms& terms, Sum* t) {
+__device__ __noinline__ void cut_best(TopShared* sh, int total, int k, const Terms& terms, Sum* t) {
+  unsigned long long c[kSlots];
   Entry e[kSlots];
-  uint32_t on = 0;
+  int on = 0;
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
     const int at = i * kThreads + threadIdx.x;
-    e[i] = at < N ? entry_of(sh->best[at]) : Entry{0, 0};
-    if (at < N) on |= 1u << i;
+    e[i] = entry_of(at < total ? sh->best[at] : 0);
+    if (at < total) on |= 1 << i;
+    c[i] = digits<E>(e[i]);
   }
-  cut<E>(sh, e, on, N, k, kLowest, terms, t, [&](int at, const Entry& x) { sh->best[at] = composite(x); });
+  const unsigned long long least = select_top<kSlots, kFirstDigit<E>, 0>(c, [&](int i) { return on >> i & 1; }, k, sh);
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if ((on >> i & 1) && c[i] < least) {
+      on &= ~(1 << i);
+      if (terms.inv > 0.f) *t = terms.add(*t, value_of(e[i].key));
+    }
+  int at = places(__popc(on), sh, &total);
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (on >> i & 1) sh->best[at++] = composite(e[i]);
   __syncthreads();
+}
+
+// The slow way: the k best of this CTA's share of a row into best by passes over it, the
+// others into *t.  Returns how many there are.
+template <typename E>
+__device__ __noinline__ int select_share(const Cut<E>& c, int V, int k, TopShared* sh, const Terms& terms, Sum* t) {
+  constexpr int kN = Elem<E>::kN;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // entries in rounds of a thread's one: the middle's, then the edges
+  const int middle = (c.v1 - c.v0) * kN, rounds = (middle + kThreads - 1) / kThreads + 1;
+  auto entry = [&](int round) {
+    int idx = round * kThreads + tid;
+    idx = round + 1 < rounds ? (idx < middle ? c.head + c.v0 * kN + idx : -1) : edge_of(c, V, tid);
+    const float x = idx >= 0 ? Elem<E>::get(c.row[idx]) : -INF_F;
+    return Entry{x < kLowest ? 0 : key_of(x), idx};  // key 0: nothing to list
+  };
+  int listed = 0;
+  for (int i = 0; i < rounds; ++i) listed += entry(i).key != 0;
+  int total;
+  places(listed, sh, &total);
+  const int n = min(total, k);
+  unsigned long long least = 0, mask = 0;
+  if (total > k) {
+    int want = k;
+    for (int shift = kFirstDigit<E>; shift >= 0; shift -= 8) {
+      __syncthreads();
+      sh->hist[0][tid] = 0;
+      __syncthreads();
+      for (int i = 0; i < rounds; ++i) {
+        const Entry e = entry(i);
+        const unsigned long long d = digits<E>(e);
+        const bool in = e.key != 0 && (d & mask) == least;
+        // lanes of one bin add once
+        const uint32_t bin = in ? (uint32_t)(d >> shift) & 255 : 256;
+        const uint32_t same = __match_any_sync(0xffffffffu, bin);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&sh->hist[0][bin], (uint32_t)__popc(same));
+      }
+      __syncthreads();
+      int bin = 255;
+      for (; bin > 0 && (int)sh->hist[0][bin] < want; --bin) want -= (int)sh->hist[0][bin];
+      least |= (unsigned long long)bin << shift;
+      mask |= 255ull << shift;
+      if ((int)sh->hist[0][bin] == want) break;
+    }
+  }
+  int at = 0;
+  for (int i = 0; i < rounds; ++i) {
+    const Entry e = entry(i);
+    const bool in = e.key != 0 && digits<E>(e) >= least;
+    int some;
+    const int to = at + places(in, sh, &some);
+    if (in) sh->best[to] = composite(e);
+    else if (e.key != 0 && terms.inv > 0.f) *t = terms.add(*t, value_of(e.key));
+    at += some;
+  }
+  return n;
 }
 
 template <typename E>
 __global__ void __launch_bounds__(kThreads, kResident) topk_kernel(const __grid_constant__ TopkArgs a) {
   constexpr int kN = Elem<E>::kN;
-  __shared__ TopShared sh;
+  extern __shared__ __align__(16) uint8_t shared_bytes[];
+  TopShared& sh = *reinterpret_cast<TopShared*>(shared_bytes);
   const int n = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait_then_release();
@@ -408,197 +393,160 @@ __global__ void __launch_bounds__(kThreads, kResident) topk_kernel(const __grid_
     continue;
   }
   Sum t{-INF_F, 0.f};
-  float threshold = kLowest;
-  int count = 0;  // of this warp's segment
-
-  uint32_t ranked = 0;  // lane l: the warp's entry l from the top
-  int turn = 0;
-  // Entries of some vectors to the list or into the sum: element j of vector u is entry
-  // first + u * kThreads * kN + j.  (The first chunk's are ranked before.)
-  auto take = [&](uint4 (&r)[kVec], int first, bool rank_them) {
-    auto place = [&](int b) { return first + b / kN * (kThreads * kN) + b % kN; };
-    // to the list what `which` (bit u * kN + j) says, which fits, a lane's entries in rising
-    // order; they are read again by their place (registers have no index)
-    auto append = [&](uint32_t which) {
+  int total = 0;
+  const int chunks = (c.v1 - c.v0 + kVec * kThreads - 1) / (kVec * kThreads), group = (chunks + kRows - 1) / kRows;  // chunks of a slot
+  const int slots = group > 0 ? (chunks + group - 1) / group : 0;
+  for (int s = 0, chunk = 0; s < slots; ++s) {
+    Sum w{-INF_F, 0.f};
+    float top = -INF_F;  // w's maximum, or a NaN
+    for (int g = 0; g < group && chunk < chunks; ++g, ++chunk) {
+      load(c, c.v0 + tid + (chunk + 1) * kVec * kThreads, next);
+      float m = top_nan(r[0], E{});
 #pragma unroll
-      for (int u = 0; u < kVec; ++u)
-        if (which >> (u * kN) & ((1u << kN) - 1)) r[u] = without(r[u], which >> (u * kN) & ((1u << kN) - 1), E{});
-      uint32_t some;
-      while ((some = __ballot_sync(0xffffffffu, which != 0)) != 0) {
-        uint32_t key = 0;
-        if (which != 0) {
-          const int idx = place(__ffs(which) - 1);
-          which &= which - 1;
-          key = key_of(Elem<E>::get(c.row[idx]));
-          sh.list[warp * kSeg + count + __popc(some & ((1u << lane) - 1))] = Entry{key, idx};
-        }
-        count += __popc(some);
-        if (!rank_them) continue;
-        some &= __ballot_sync(0xffffffffu, key > __shfl_sync(0xffffffffu, ranked, 31));
-        if (__popc(some) > 5) {
-          ranked = merge_lanes(ranked, sort_lanes(key, lane), lane);
-        } else {
-          for (; some != 0; some &= some - 1) {
-            const uint32_t x = __shfl_sync(0xffffffffu, key, __ffs(some) - 1);
-            const int at = __popc(__ballot_sync(0xffffffffu, ranked >= x));
-            const uint32_t up = __shfl_up_sync(0xffffffffu, ranked, 1);
-            ranked = lane > at ? up : lane == at ? x : ranked;
-          }
-        }
-      }
-    };
-    float top = top_nan(r[0], E{});
+      for (int u = 1; u < kVec; ++u) m = max_nan(m, top_nan(r[u], E{}));
+      top = max_nan(top, m);
+      if (terms.inv > 0.f) w = add_vectors<E>(terms, w, r, m);
 #pragma unroll
-    for (int u = 1; u < kVec; ++u) top = max_nan(top, top_nan(r[u], E{}));
-    if (__any_sync(0xffffffffu, !(top < threshold))) {
-      uint32_t which = 0;
-#pragma unroll
-      for (int u = 0; u < kVec; ++u) which |= reaching(r[u], threshold, E{}) << (u * kN);
-      if (count + __reduce_add_sync(0xffffffffu, __popc(which)) > kSeg) {
-        // the warp's k best, of its segment and of these, bit by bit
-        unsigned long long least = 0;
-        auto some_reach = [&](unsigned long long higher) {
-          int some = 0;
-          for (uint32_t w = which; w != 0; w &= w - 1) {
-            const int idx = place(__ffs(w) - 1);
-            some += digits<E>(Entry{key_of(Elem<E>::get(c.row[idx])), idx}) >= higher;
-          }
-          for (int i = lane; i < count; i += 32) some += digits<E>(sh.list[warp * kSeg + i]) >= higher;
-          return __reduce_add_sync(0xffffffffu, some);
-        };
-        __syncwarp();
-        for (int bit = kFirstDigit<E> + 7; bit >= 0; --bit) {
-          const unsigned long long higher = least | 1ull << bit;
-          const int some = some_reach(higher);
-          if (some >= k) least = higher;
-          if (some == k) break;
-        }
-        int kept = 0;
-        for (int i = lane; i - lane < count; i += 32) {
-          const Entry e = i < count ? sh.list[warp * kSeg + i] : Entry{0, 0};
-          const bool in = i < count && digits<E>(e) >= least;
-          const uint32_t some = __ballot_sync(0xffffffffu, in);
-          if (in) sh.list[warp * kSeg + kept + __popc(some & ((1u << lane) - 1))] = e;
-          else if (i < count && terms.inv > 0.f) t = terms.add(t, value_of(e.key));
-          kept += __popc(some);
-        }
-        count = kept;
-        uint32_t best = 0;
-        for (uint32_t w = which; w != 0; w &= w - 1) {
-          const int idx = place(__ffs(w) - 1);
-          if (digits<E>(Entry{key_of(Elem<E>::get(c.row[idx])), idx}) >= least) best |= w & -w;
-        }
-        which = best;
-        threshold = fmaxf(threshold, threshold_of(key_of_digits<E>(least)));
-      }
-      append(which);
-      top = -INF_F;
-#pragma unroll
-      for (int u = 0; u < kVec; ++u) top = fmaxf(top, top_nan(r[u], E{}));
+      for (int u = 0; u < kVec; ++u) r[u] = next[u];
     }
-    if (terms.inv > 0.f) t = add_vectors<E>(terms, t, r, top);
-  };
-  // The least of the warps' m-th entries so far: a threshold for all of them.
-  auto exchange = [&] {
-    if (lane == m - 1) sh.least[turn][warp] = ranked;
-    __syncthreads();
-    uint32_t least = sh.least[turn][0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) least = min(least, sh.least[turn][w]);
-    threshold = fmaxf(threshold, threshold_of(least));
-    turn ^= 1;
-  };
-
-  for (int i0 = c.v0, turns = 0; i0 < c.v1; i0 += kVec * kThreads, ++turns) {
-    const int i = i0 + tid;
-    load(c, i + kVec * kThreads, next);
-    if (turns == 0) {
-      // the largest of the chunk's vectors' maxima are ranked, for a threshold to begin with
-      uint32_t top[kVec];
-#pragma unroll
-      for (int u = 0; u < kVec; ++u) top[u] = sort_lanes(key_of(top_nan(r[u], E{})), lane);
-      ranked = merge_lanes(merge_lanes(top[0], top[1], lane), merge_lanes(top[2], top[3], lane), lane);
-      exchange();
-    }
-    take(r, c.head + i * kN, turns > 0);
-    if (turns == 1 || (turns & 3) == 3) exchange();
-#pragma unroll
-    for (int u = 0; u < kVec; ++u) r[u] = next[u];
+    sh.slot[s][tid] = make_float2(top, w.s);
   }
-  if ((c.first && c.head > 0) || (c.last && c.tail0 < a.V)) {
+  {
     const int e = edge_of(c, a.V, tid);
-#pragma unroll
-    for (int u = 0; u < kVec; ++u) r[u] = low_vector<E>();
-    if (e >= 0) {
-      const float x = Elem<E>::get(c.row[e]);
-      if (sizeof(E) == 2) r[0].x = 0xff800000u | __float_as_uint(x) >> 16;
-      else r[0].x = __float_as_uint(x);
-    }
-    take(r, e, true);
+    const float x = e >= 0 ? Elem<E>::get(c.row[e]) : -INF_F;
+    sh.slot[slots][tid] = make_float2(x, x == -INF_F ? 0.f : x == INF_F ? x : 1.f);
   }
   load_next();
 
-  // The threshold at the end: the largest of the warps' first 2 m + 2 ranked entries that has
-  // enough of them at or above it, k, or of each of a cluster's CTAs an equal share.
-  const int tops = min(2 * m + 2, 32);
-  if (lane < tops) sh.ranked[warp * tops + lane] = ranked;
-  if (tid < n) sh.bound[tid] = 0;
+  // A threshold to begin with: the least of the warps' m-th lanes' largest entries, above
+  // -inf; then the slots that reach it.
+  float mine = -INF_F;
+  for (int s = 0; s <= slots; ++s) mine = max_nan(mine, sh.slot[s][tid].x);
+  const uint32_t sorted = sort_lanes(key_of(mine), lane);
+  if (lane == m - 1) sh.least[warp] = sorted;
   __syncthreads();
-  if (tid < kWarps * tops) {
-    const uint32_t ranked = sh.ranked[tid];
-    int above = 0, same = 0;
-#pragma unroll 4
-    for (int j = 0; j < kWarps * tops; j += 4) {
-      const uint4 x = *reinterpret_cast<const uint4*>(&sh.ranked[j]);
-      above += (x.x > ranked) + (x.y > ranked) + (x.z > ranked) + (x.w > ranked);
-      same += (x.x == ranked) + (x.y == ranked) + (x.z == ranked) + (x.w == ranked);
+  uint32_t floor_ = sh.least[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) floor_ = min(floor_, sh.least[w]);
+  floor_ = max(floor_, key_of(kLowest));
+  // x reaches key `least` (a NaN reaches every key, and only a NaN a NaN's)
+  auto reaches = [](float x, float least) { return least == least ? !(x < least) : x != x; };
+  auto reaching = [&](uint32_t least) {
+    const float v = value_of(least);
+    int some = 0;
+    for (int s = 0; s <= slots; ++s) some += reaches(sh.slot[s][tid].x, v);
+    return some;
+  };
+  int n_listed;
+  int at = places(reaching(floor_), &sh, &n_listed);
+  if (n_listed > kListed) {
+    // bit by bit up to the k-th largest (its upper 16 bits)
+    uint32_t step = 1u << 31;
+    for (uint32_t high = 0; step >= 1u << 16; step >>= 1) {
+      const uint32_t next_key = high | step;
+      places(reaching(next_key), &sh, &n_listed);
+      if (n_listed >= k) high = next_key;
+      if (step == 1u << 16) floor_ = max(floor_, high);
     }
-    const int share = (k + n - 1) / n;
-    if (above < share && share <= above + same) sh.least[0][0] = ranked;  // alike where several write
+    at = places(reaching(floor_), &sh, &n_listed);
   }
-  __syncthreads();
-  uint32_t bound = sh.least[0][0];
-  if (n > 1) {
+  bool slow = n_listed > kListed;  // the same for all threads
+  uint32_t bound = floor_;
+  if (!slow) {
+    const float least = value_of(floor_);
+    for (int s = 0; s <= slots; ++s) {
+      const float x = sh.slot[s][tid].x;
+      if (reaches(x, least)) {
+        sh.key[at] = key_of(x);
+        sh.which[at++] = (uint16_t)(s * kThreads + tid);
+      }
+    }
+    const int padded = (n_listed + 3) & ~3;
+    if (tid < padded - n_listed) sh.key[n_listed + tid] = 0;
+    if (tid < 2) sh.threshold[tid] = floor_;
+    __syncthreads();
+    const int share = (k + n - 1) / n;
+    for (int i = tid; i < n_listed; i += kThreads) {
+      const uint32_t own = sh.key[i];
+      int above = 0, same = 0;
+#pragma unroll 4
+      for (int j = 0; j < padded; j += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(&sh.key[j]);
+        above += (x.x > own) + (x.y > own) + (x.z > own) + (x.w > own);
+        same += (x.x == own) + (x.y == own) + (x.z == own) + (x.w == own);
+      }
+      if (above < k && k <= above + same) sh.threshold[0] = own;  // alike where several write
+      if (above < share && share <= above + same) sh.threshold[1] = own;
+    }
+    __syncthreads();
+    bound = sh.threshold[1];
+  }
+  if (n > 1) {  // entries of the whole row, a share of k from each CTA, that reach the least of the bounds
     cluster_sync();  // every CTA's places are there
     if (tid < n) st_dsmem_u32(mapa(smem_u32(&sh.bound[rank]), tid), bound);
     cluster_sync();
     for (int i = 0; i < n; ++i) bound = min(bound, sh.bound[i]);
-  }
-  threshold = fmaxf(threshold, threshold_of(bound));
-  // (a warp's own may be higher: its k best are above it)
-  auto stays = [&](const Entry& e) { return !(value_of(e.key) < threshold); };
-  int left = 0;
-  for (int i = lane; i < count; i += 32) left += stays(sh.list[warp * kSeg + i]);
-  left = __reduce_add_sync(0xffffffffu, left);
-  if (lane == 0) sh.scan[warp] = left;
-  __syncthreads();
-  int total = 0, at = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    at += w < warp ? sh.scan[w] : 0;
-    total += sh.scan[w];
-  }
-  if (total > LORA_TOPK_MAX * (n > 1 ? 1 : kMaxCluster)) {  // more than there is room for
-    if (lane == 0) sh.count[warp] = count;
-    cut_list<E>(&sh, k, threshold, terms, &t);
-    total = 0, at = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      at += w < warp ? sh.count[w] : 0;
-      total += sh.count[w];
-    }
-    count = sh.count[warp];
-    for (int i = lane; i < count; i += 32) sh.best[at + i] = composite(sh.list[warp * kSeg + i]);
   } else {
-    for (int i = lane; i - lane < count; i += 32) {
-      const Entry e = i < count ? sh.list[warp * kSeg + i] : Entry{0, 0};
-      const bool in = i < count && stays(e);
-      const uint32_t some = __ballot_sync(0xffffffffu, in);
-      if (in) sh.best[at + __popc(some & ((1u << lane) - 1))] = composite(e);
-      else if (i < count && terms.inv > 0.f) t = terms.add(t, value_of(e.key));
-      at += __popc(some);
+    bound = 0;
+  }
+  const uint32_t threshold = slow ? 0 : max(bound, sh.threshold[0]);
+  if (!slow) {
+    // the entries that reach it, of the slots that do; a slot's other entries into the sum
+    auto each = [&](int id, auto f) {
+      const int s = id / kThreads, v = id % kThreads;
+      if (s == slots) {
+        const int e = edge_of(c, a.V, v);
+        if (e >= 0) f(e, Elem<E>::get(c.row[e]));
+        return;
+      }
+      for (int i = s * group * kVec, end = min(s + 1, kRows) * group * kVec; i < end; ++i) {
+        const int vec = c.v0 + v + i * kThreads;
+        if (vec >= c.v1) break;
+        const uint4 x = reinterpret_cast<const uint4*>(c.row + c.head)[vec];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) f(c.head + vec * kN + j, Elem<E>::get(Elem<E>::entry(x, j)));
+      }
+    };
+    const float least = value_of(threshold);
+    int some = 0;
+    float top = -INF_F;  // of those below it
+    for (int i = tid; i < n_listed; i += kThreads)
+      if (sh.key[i] >= threshold)
+        each(sh.which[i], [&](int, float x) {
+          const bool in = reaches(x, least);
+          some += in;
+          top = fmaxf(top, in ? -INF_F : x);
+        });
+    at = places(some, &sh, &total);
+    slow = total > kBest;
+    if (!slow) {
+      const float base = base_of(top);
+      float rest = 0.f;
+      for (int i = tid; i < n_listed; i += kThreads)
+        if (sh.key[i] >= threshold)
+          each(sh.which[i], [&](int idx, float x) {
+            if (reaches(x, least)) sh.best[at++] = composite(Entry{key_of(x), idx});
+            else rest += terms.power(x, base);
+          });
+      if (terms.inv > 0.f) {
+        for (int s = 0; s <= slots; ++s) {
+          const float x = sh.slot[s][tid].x;
+          top = fmaxf(top, reaches(x, least) ? -INF_F : x);
+        }
+        t = Sum{top, rest == 0.f ? 0.f : rest * terms.power(base, base_of(top))};
+        for (int s = 0; s <= slots; ++s) {
+          const float2 w = sh.slot[s][tid];
+          if (w.x != -INF_F && !reaches(w.x, least)) t.s += w.y * terms.power(base_of(w.x), base_of(top));
+        }
+      }
+      __syncthreads();
+      if (n > 1 && total > LORA_TOPK_MAX) {
+        cut_best<E>(&sh, total, k, terms, &t);
+        total = k;
+      }
     }
   }
+  if (slow) total = select_share<E>(c, a.V, k, &sh, terms, &t);
   // A CTA's entries are in best.  The first CTA takes the others'.
   auto cta_sum = [&] {
     const Sum w = terms.across(t);
@@ -650,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, kResident) topk_kernel(const __grid_
   if (total > 2 * kThreads) {
     __syncthreads();
     cut_best<E>(&sh, total, k, terms, &t);
-    total = min(total, k);
+    total = k;
   }
   // an entry's place is the number of entries before it
   if (tid < 2) sh.best[total + tid] = 0;
@@ -734,6 +682,7 @@ extern "C" lora_status_t lora_topk_logits(const void* logits, int64_t ld, int32_
   const bool bf16 = dtype == LORA_LOGITS_BF16;
   const void* f = bf16 ? (const void*)topk_kernel<uint16_t> : (const void*)topk_kernel<float>;
   const int n = ctas_of(T, V, bf16 ? 8 : 4);
+  if (ensure_smem_attr(f, sizeof(TopShared)) != cudaSuccess) return LORA_ERR_CUDA;
   const int ctas = n > 1 ? T * n : std::min(T, kResident * sm_count());
-  return launch_pdl(f, dim3((unsigned)ctas), dim3(kThreads), 0, (cudaStream_t)stream, n, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  return launch_pdl(f, dim3((unsigned)ctas), dim3(kThreads), sizeof(TopShared), (cudaStream_t)stream, n, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }

@@ -2,6 +2,9 @@
 // exponentials, and the checks that every call on logits makes of its rows.
 #pragma once
 
+#include <algorithm>
+#include <cmath>
+
 #include "common.cuh"
 #include "lora_train.h"
 #include "pairs.cuh"
@@ -204,7 +207,87 @@ __device__ __forceinline__ bool on_boundary(const E* out, const Cut<E>& c) {
   return (reinterpret_cast<uintptr_t>(out + c.head) & 15) == 0;
 }
 
+// Terms exp((x - base) / temperature): log2(e) / temperature in two parts, and the temperature's inverse.
+struct Terms {
+  float hi, lo, inv;
+  __device__ __forceinline__ Sum join(const Sum& x, const Sum& y) const {
+    Sum r;
+    r.m = fmaxf(x.m, y.m);
+    const float base = base_of(r.m);
+    r.s = x.s * expf((x.m - base) * inv) + y.s * expf((y.m - base) * inv);
+    return r;
+  }
+  __device__ __forceinline__ float power(float x, float base) const {  // of finite base
+    const float d = x - base;
+    return ex2(fmaf(d, hi, d * lo));
+  }
+  __device__ __forceinline__ Sum add(const Sum& t, float x) const {
+    return join(t, Sum{x, x == x ? (x == -INF_F ? 0.f : x == INF_F ? x : 1.f) : x});
+  }
+  __device__ __forceinline__ Sum across(const Sum& t) const {  // the warp's lanes
+    const float m = warp_max(t.m);
+    return Sum{m, warp_add(t.s * expf((t.m - base_of(m)) * inv))};
+  }
+};
+
+// The sum of exp((x - base) / temperature) over some vectors.
+template <typename E, int N>
+__device__ __forceinline__ float power_sum(const Terms& e, const uint4 (&r)[N], float base) {
+  constexpr int kPairs = Elem<E>::kPairs;
+  const uint64_t hi = pair_of(e.hi, e.hi), lo = pair_of(e.lo, e.lo), nb = pair_of(-base, -base);
+  uint64_t part = pair_of(0.f, 0.f);
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+      const uint64_t d = add2(Elem<E>::pair(r[u], k), nb);
+      float a, b;
+      split(fma2(d, hi, mul2(d, lo)), a, b);
+      part = add2(part, pair_of(ex2(a), ex2(b)));
+    }
+  }
+  float a, b;
+  split(part, a, b);
+  return a + b;
+}
+
+// Some vectors, whose largest element is top, joined to t.
+template <typename E, int N>
+__device__ __forceinline__ Sum add_vectors(const Terms& e, Sum t, const uint4 (&r)[N], float top) {
+  const float m = fmaxf(t.m, top), base = base_of(m);
+  const float s = power_sum<E>(e, r, base);
+  if (m != t.m) t.s *= expf((t.m - base) * e.inv);
+  return Sum{m, t.s + s};
+}
+
+// The largest element of a vector, NaN if one is.
+__device__ __forceinline__ float top_nan(const uint4& v, uint16_t) {
+  const __nv_bfloat162 t = __hmax2_nan(__hmax2_nan(Elem<uint16_t>::word(v.x), Elem<uint16_t>::word(v.y)),
+                                       __hmax2_nan(Elem<uint16_t>::word(v.z), Elem<uint16_t>::word(v.w)));
+  const __nv_bfloat16 m = __hmax_nan(__low2bfloat16(t), __high2bfloat16(t));
+  return __bfloat162float(m);
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float top_nan(const uint4& v, float) {
+  return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+
 // ------------------------------------------------------------------- host --
+
+// The terms of a temperature.  Neither part of the factor is 0: -inf times both is -inf.
+inline Terms terms_of(float temperature) {
+  const double per = 1.4426950408889634 / (double)temperature;
+  Terms t;
+  t.hi = (float)per;
+  if ((double)t.hi > per) t.hi = std::nextafter(t.hi, 0.f);
+  t.lo = std::max((float)(per - (double)t.hi), 1e-30f);
+  t.inv = 1.f / temperature;
+  return t;
+}
 
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 

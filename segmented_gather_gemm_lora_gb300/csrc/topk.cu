@@ -46,8 +46,7 @@ struct TopkArgs {
   long long ld;
   const int32_t* labels;
   int T, V, k;
-  float hi, lo;  // log2(e) / temperature in two parts
-  float inv;     // 1 / temperature
+  Terms terms;
   int32_t* ids;
   float* values;
   float* tail;
@@ -92,68 +91,6 @@ struct TopShared {
 };
 static_assert(offsetof(TopShared, best) % 16 == 0 && offsetof(TopShared, key) % 16 == 0 && offsetof(TopShared, sum) % 8 == 0,
               "read in one piece");
-
-// Terms exp((x - base) / temperature).
-struct Terms {
-  float hi, lo, inv;
-  __device__ __forceinline__ Sum join(const Sum& x, const Sum& y) const {
-    Sum r;
-    r.m = fmaxf(x.m, y.m);
-    const float base = base_of(r.m);
-    r.s = x.s * expf((x.m - base) * inv) + y.s * expf((y.m - base) * inv);
-    return r;
-  }
-  __device__ __forceinline__ float power(float x, float base) const {  // of finite base
-    const float d = x - base;
-    return ex2(fmaf(d, hi, d * lo));
-  }
-  __device__ __forceinline__ Sum add(const Sum& t, float x) const {
-    return join(t, Sum{x, x == x ? (x == -INF_F ? 0.f : x == INF_F ? x : 1.f) : x});
-  }
-  __device__ __forceinline__ Sum across(const Sum& t) const {  // the warp's lanes
-    const float m = warp_max(t.m);
-    return Sum{m, warp_add(t.s * expf((t.m - base_of(m)) * inv))};
-  }
-};
-
-// Some vectors, whose largest element is top, joined to t.
-template <typename E, int N>
-__device__ __forceinline__ Sum add_vectors(const Terms& e, Sum t, const uint4 (&r)[N], float top) {
-  constexpr int kPairs = Elem<E>::kPairs;
-  const float m = fmaxf(t.m, top), base = base_of(m);
-  const uint64_t hi = pair_of(e.hi, e.hi), lo = pair_of(e.lo, e.lo), nb = pair_of(-base, -base);
-  uint64_t part = pair_of(0.f, 0.f);
-#pragma unroll
-  for (int u = 0; u < N; ++u) {
-#pragma unroll
-    for (int k = 0; k < kPairs; ++k) {
-      const uint64_t d = add2(Elem<E>::pair(r[u], k), nb);
-      float a, b;
-      split(fma2(d, hi, mul2(d, lo)), a, b);
-      part = add2(part, pair_of(ex2(a), ex2(b)));
-    }
-  }
-  float a, b;
-  split(part, a, b);
-  if (m != t.m) t.s *= expf((t.m - base) * e.inv);
-  return Sum{m, t.s + (a + b)};
-}
-
-// The largest element of a vector, NaN if one is.
-__device__ __forceinline__ float top_nan(const uint4& v, uint16_t) {
-  const __nv_bfloat162 t = __hmax2_nan(__hmax2_nan(Elem<uint16_t>::word(v.x), Elem<uint16_t>::word(v.y)),
-                                       __hmax2_nan(Elem<uint16_t>::word(v.z), Elem<uint16_t>::word(v.w)));
-  const __nv_bfloat16 m = __hmax_nan(__low2bfloat16(t), __high2bfloat16(t));
-  return __bfloat162float(m);
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float top_nan(const uint4& v, float) {
-  return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
-}
 
 // The warp's keys in falling order (a bitonic network).
 __device__ __forceinline__ uint32_t sort_lanes(uint32_t key, int lane) {
@@ -354,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, kResident) topk_kernel(const __grid_
     return;
   }
   const int k = a.k, m = (k + kWarps - 1) / kWarps;
-  const Terms terms{a.hi, a.lo, a.tail != nullptr ? a.inv : 0.f};
+  const Terms terms{a.terms.hi, a.terms.lo, a.tail != nullptr ? a.terms.inv : 0.f};
   auto cut_at = [&](int row) { return cut_row(static_cast<const E*>(a.logits) + (long long)row * a.ld, a.V, rank, n); };
   auto load = [&](const Cut<E>& c, int i, uint4 (&r)[kVec]) {
     const uint4* const mid = reinterpret_cast<const uint4*>(c.row + c.head);
@@ -629,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, kResident) topk_kernel(const __grid_
 #pragma unroll
     for (int q = 1; q < kMaxCluster; ++q)
       if (q < n) all = terms.join(all, others[q]);
-    a.tail[row] = all.s == 0.f ? -INF_F : base_of(all.m) * a.inv + logf(all.s);
+    a.tail[row] = all.s == 0.f ? -INF_F : base_of(all.m) * a.terms.inv + logf(all.s);
   }
   }
   if (next_row >= a.T) return;
@@ -669,11 +606,7 @@ extern "C" lora_status_t lora_topk_logits(const void* logits, int64_t ld, int32_
   a.T = T;
   a.V = V;
   a.k = k;
-  const double per = 1.4426950408889634 / (double)temperature;
-  a.hi = (float)per;
-  if ((double)a.hi > per) a.hi = std::nextafter(a.hi, 0.f);
-  a.lo = std::max((float)(per - (double)a.hi), 1e-30f);  // above 0: -inf times both parts is -inf
-  a.inv = 1.f / temperature;
+  a.terms = terms_of(temperature);
   a.ids = ids;
   a.values = values;
   a.tail = tail;

@@ -97,7 +97,7 @@ struct DistillArgs {
 };
 
 // What the rows' gradients are made of: entry v (not listed, not the label) is
-//     kd 2^((x - base) hi - l2) + ce 2^((x - base) log2 e - l2_plain).
+//     kd 2^((x - base) log2(e) / temperature - l2) + ce 2^((x - base) log2 e - l2_plain).
 struct Slope {
   float base, kd, l2, ce, l2_plain;
 };
@@ -105,7 +105,7 @@ struct Slope {
 template <typename E, bool kBoth>
 __device__ __forceinline__ uint4 slope_vector(const uint4& x, const Slope& g, const Terms& terms, const Terms& plain) {
   constexpr int kPairs = Elem<E>::kPairs;
-  const uint64_t nb = pair_of(-g.base, -g.base), hi = pair_of(terms.hi, terms.hi), nl = pair_of(-g.l2, -g.l2);
+  const uint64_t nb = pair_of(-g.base, -g.base), hi = pair_of(terms.near, terms.near), nl = pair_of(-g.l2, -g.l2);
   const uint64_t c = pair_of(g.kd, g.kd);
   uint64_t f[kPairs];
 #pragma unroll
@@ -115,7 +115,7 @@ __device__ __forceinline__ uint4 slope_vector(const uint4& x, const Slope& g, co
     split(fma2(d, hi, nl), a, b);
     f[j] = mul2(c, pair_of(ex2(a), ex2(b)));
     if (kBoth) {
-      split(fma2(d, pair_of(plain.hi, plain.hi), pair_of(-g.l2_plain, -g.l2_plain)), a, b);
+      split(fma2(d, pair_of(plain.near, plain.near), pair_of(-g.l2_plain, -g.l2_plain)), a, b);
       f[j] = fma2(pair_of(g.ce, g.ce), pair_of(ex2(a), ex2(b)), f[j]);
     }
   }
@@ -124,8 +124,8 @@ __device__ __forceinline__ uint4 slope_vector(const uint4& x, const Slope& g, co
 template <bool kBoth>
 __device__ __forceinline__ float slope_entry(float x, const Slope& g, const Terms& terms, const Terms& plain) {
   const float d = x - g.base;
-  float f = g.kd * ex2(fmaf(d, terms.hi, -g.l2));
-  if (kBoth) f = fmaf(g.ce, ex2(fmaf(d, plain.hi, -g.l2_plain)), f);
+  float f = g.kd * ex2(fmaf(d, terms.near, -g.l2));
+  if (kBoth) f = fmaf(g.ce, ex2(fmaf(d, plain.near, -g.l2_plain)), f);
   return f;
 }
 
@@ -613,114 +613,321 @@ __global__ void __launch_bounds__(kG + 32, kG > 256 ? 1 : kVec > 8 ? 2 : 3) held
   if (n > 1) cluster_sync();
 }
 
-// ----------------------------------------------------------------- long rows --
-
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-
-__device__ __forceinline__ float block_max(float x, float* sh) {
-  x = warp_max(x);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = sh[0];
-  for (int i = 1; i < kWarps; ++i) x = fmaxf(x, sh[i]);
-  return x;
+// A vector without the elements that `m` says.
+__device__ __forceinline__ uint32_t word_without(uint32_t w, uint32_t m) {
+  if (m & 1) w = (w & 0xffff0000u) | 0xff80u;
+  if (m & 2) w = (w & 0xffffu) | 0xff800000u;
+  return w;
 }
-__device__ __forceinline__ float block_add(float x, float* sh) {
-  x = warp_add(x);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = sh[0];
-  for (int i = 1; i < kWarps; ++i) x += sh[i];
-  return x;
+__device__ __forceinline__ uint4 without(const uint4& v, uint32_t m, uint16_t) {
+  return make_uint4(word_without(v.x, m), word_without(v.y, m >> 2), word_without(v.z, m >> 4), word_without(v.w, m >> 6));
+}
+__device__ __forceinline__ uint4 without(const uint4& v, uint32_t m, float) {
+  return make_uint4(m & 1 ? 0xff800000u : v.x, m & 2 ? 0xff800000u : v.y, m & 4 ? 0xff800000u : v.z, m & 8 ? 0xff800000u : v.w);
 }
 
-// Rows longer than the held form takes: a CTA a row, which it reads three times, with a
-// bit a logit that says whether it is listed.
-template <typename E>
-__global__ void __launch_bounds__(kThreads) long_row_kernel(const __grid_constant__ DistillArgs a) {
-  extern __shared__ uint32_t bits[];
-  __shared__ float sh[kWarps];
-  __shared__ int bad;
-  __shared__ uint64_t probe_bar;
+// -------------------------------------------------------------- streamed form --
+//
+// Many rows, or rows longer than the held form takes: a CTA a row, which it reads for its
+// sum and again for its gradient.  Few rows are under way (one or two an SM), so the
+// second read finds the row in L2; outputs are written past it.  A row costs its barriers
+// once, not once in each of a cluster's CTAs, and its CTA has no other to wait for.
+//
+// Listed entries: a bit an entry and a bit a vector.  A vector with a listed entry is left
+// out of the sum as it goes by; the thread of the lowest entry of such a vector adds what
+// is not listed of it.
+
+constexpr int kStream = 512;  // threads
+constexpr int kStreamWarps = kStream / 32;
+#ifndef PROMOTE
+#define PROMOTE 4
+#endif
+constexpr int kBatch = PROMOTE;  // vectors a thread takes at once
+
+struct StreamShared {
+  uint64_t probe_bar;
+  float4 part[kStreamWarps];          // m, the sum, its sum at temperature 1
+  float4 lists[kMaxList / 32];        // a warp's entries: teacher's maximum and sum, student's
+  float lists_plain[kMaxList / 32];
+  float2 outcomes[kMaxList / 32 + 1];  // kd, mass; the rest's last
+};
+
+// What L2 does with lines: keeps those that will be read again, gives up the others first.
+__device__ __forceinline__ uint64_t keep_lines() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t drop_lines() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint4 load_as(const uint4* p, uint64_t policy) {
+  uint4 v;
+  asm volatile("ld.global.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p), "l"(policy)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_as(void* p, const uint4& v, uint64_t policy) {
+  asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w),
+               "l"(policy)
+               : "memory");
+}
+
+template <typename E, bool kBoth>
+__global__ void __launch_bounds__(kStream, 2) stream_kernel(const __grid_constant__ DistillArgs a) {
+  constexpr int kN = Elem<E>::kN;
+  extern __shared__ uint32_t bits[];  // of the entries, then of the vectors
+  __shared__ StreamShared sh;
+  const int id = (int)threadIdx.x, lane = id & 31, warp = id >> 5;
+  uint32_t* const flags = bits + (a.V + 31) / 32;
+  const int words = (a.V + 31) / 32 + (a.V / kN / (kBatch * kStream) + 1) * kBatch * kStreamWarps;
+  for (int i = id; i < words; i += kStream) bits[i] = 0;
   pdl_wait_then_release();
   if (a.probe > 0) {
-    if (threadIdx.x == 0 && !wait_probe(&probe_bar, a.probe)) report(a.err, LORA_DERR_TIMEOUT);
+    if (id == 0 && !wait_probe(&sh.probe_bar, a.probe)) report(a.err, LORA_DERR_TIMEOUT);
     return;
   }
-  const int t = blockIdx.x, tid = threadIdx.x, V = a.V;
-  const E* row = static_cast<const E*>(a.logits) + (long long)t * a.ld;
-  E* out = a.dlogits == nullptr ? nullptr : static_cast<E*>(a.dlogits) + (long long)t * a.ldd;
-  for (int i = tid; i < (V + 31) / 32; i += kThreads) bits[i] = 0;
-  if (tid == 0) bad = 0;
+  const bool forward = a.opt.kind == LORA_DISTILL_FORWARD, lists = warp * 32 < a.k;
+  const Terms terms = a.terms, plain = a.plain;
   __syncthreads();
-  int id = tid < a.k ? a.ids[(long long)t * a.k + tid] : -1;
-  float value = id >= 0 ? a.values[(long long)t * a.k + tid] : -INF_F;
-  if (value == -INF_F) id = -1;
-  const int label = a.labels == nullptr ? -1 : a.labels[t];
-  const bool counts = a.labels == nullptr || label >= 0;
-  if (counts) {
-    if (id >= V || (a.labels != nullptr && label >= V)) bad = 1;
-    else if (id >= 0 && (atomicOr(&bits[id >> 5], 1u << (id & 31)) >> (id & 31) & 1)) bad = 1;
-  }
-  __syncthreads();
-  const float w = a.weight == nullptr ? 1.f : a.weight[t];
-  if (!counts || bad) {
-    if (tid == 0 && bad) report(a.err, LORA_DERR_BAD_LABEL);
-    if (out != nullptr)
-      for (int v = tid; v < V; v += kThreads) out[v] = Elem<E>::put(0.f);
-    if (tid == 0) put_nothing(a, t);
-    return;
-  }
-  const float inv = 1.f / a.opt.temperature;
-  // the student
-  float top = -INF_F;
-  for (int v = tid; v < V; v += kThreads) top = fmaxf(top, Elem<E>::get(row[v]));
-  top = base_of(block_max(top, sh));
-  float rest = 0.f, all = 0.f;
-  for (int v = tid; v < V; v += kThreads) {
-    const float x = Elem<E>::get(row[v]) - top;
-    if (!(bits[v >> 5] >> (v & 31) & 1)) rest += expf(x * inv);
-    if (a.opt.ce_weight > 0.f) all += expf(x);
-  }
-  rest = block_add(rest, sh);
-  if (a.opt.ce_weight > 0.f) all = block_add(all, sh);
-  const float x = id >= 0 ? Elem<E>::get(row[id]) - top : 0.f, xl = label >= 0 ? Elem<E>::get(row[label]) - top : 0.f;
-  const float total = rest + block_add(id >= 0 ? expf(x * inv) : 0.f, sh), lt = logf(total);
-  // the teacher
-  const float tail = a.tail == nullptr ? -INF_F : a.tail[t];
-  const float high = base_of(fmaxf(block_max(value * inv, sh), tail));  // in the tail's measure
-  const float mass = block_add(id >= 0 ? expf(value * inv - high) : 0.f, sh) + expf(tail - high), lm = logf(mass);
-  Outcome o{0.f, 0.f, 0.f}, r = o;
-  const float dt = tail - high - lm - (logf(rest) - lt);
-  if (mass != 0.f && total != 0.f) {
-    if (id >= 0) o = outcome(a.opt.kind, a.opt.mix, value * inv - high - lm, x * inv - lt);
-    r = outcome(a.opt.kind, a.opt.mix, tail - high - lm, logf(rest) - lt);
-  }
-  const float kd = block_add(o.kd, sh) + r.kd, C = block_add(o.mass, sh) + r.mass;
-  bool none = total == 0.f;  // nothing is visible
-  const float ce = a.opt.ce_weight > 0.f ? (none ? INF_F : logf(all) - xl) : 0.f;
-  if (tid == 0) put_losses(a, t, RowIn{label, w, tail}, none && mass > 0.f ? INF_F : kd, ce);
-  if (out == nullptr) return;
-  __syncthreads();
-  none = none || w == 0.f;
-  const bool zero = fabsf(C) == INF_F;
-  const float gs = a.opt.grad_scale * w, kw = gs * a.opt.kd_weight * inv, cw = a.opt.ce_weight > 0.f ? gs * a.opt.ce_weight : 0.f;
-  const float slope = rest == 0.f || mass == 0.f ? 0.f : slope_of(a.opt.kind, a.opt.mix, dt) - C;
-  const float mine = id >= 0 ? o.share - (a.opt.kind == LORA_DISTILL_FORWARD ? 0.f : expf(x * inv - lt) * C) : 0.f;
-  for (int v = tid; v < V; v += kThreads) {
-    const float y = Elem<E>::get(row[v]) - top;
-    float g = zero ? 0.f : kw * slope * expf(y * inv - lt);
-    if (cw != 0.f && !none) g += cw * (expf(y) / all - (v == label ? 1.f : 0.f));
-    out[v] = Elem<E>::put(none ? 0.f : g);
-  }
-  __syncthreads();
-  if (id >= 0 && !none) {
-    float g = zero ? 0.f : kw * mine;
-    if (cw != 0.f) g += cw * (expf(x) / all - (id == label ? 1.f : 0.f));
-    out[id] = Elem<E>::put(g);
+  auto row_at = [&](long long t) { return static_cast<const E*>(a.logits) + t * a.ld; };
+  // batch i0 .. of a row's middle
+  uint4 next[kBatch];
+  const uint64_t keep = keep_lines(), drop = drop_lines();
+  auto load = [&](const uint4* mid, int nvec, int i0, uint64_t policy) {
+    const uint4* const p = mid + i0 + id;
+    if (i0 + kBatch * kStream <= nvec) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) next[u] = load_as(p + u * kStream, policy);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) next[u] = i0 + u * kStream + id < nvec ? load_as(p + u * kStream, policy) : low_vector<E>();
+    }
+  };
+  long long loaded = -1;  // the row whose first batch is in next
+  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const int label = a.labels != nullptr ? a.labels[t] : -1;
+    const E* const row = row_at(t);
+    E* const out = a.dlogits == nullptr ? nullptr : static_cast<E*>(a.dlogits) + t * a.ldd;
+    const Cut<E> c = cut_row(row, a.V, 0, 1);
+    if (a.labels != nullptr && (label < 0 || label >= a.V)) {
+      if (id == 0) {
+        if (label >= a.V) report(a.err, LORA_DERR_BAD_LABEL);
+        put_nothing(a, t);
+      }
+      if (out != nullptr) zero_share<E, kStream>(c, out, a.V, id);
+      continue;
+    }
+    const uint4* const mid = reinterpret_cast<const uint4*>(row + c.head);
+    if (loaded != t) load(mid, c.nvec, 0, keep);
+    const RowIn in = row_in(a, t, label);
+    // the list
+    int v = -1;
+    float value = -INF_F, x = -INF_F;
+    if (id < a.k) {
+      v = a.ids[t * a.k + id];
+      value = a.values[t * a.k + id];
+      if (value == -INF_F) v = -1;
+      if (v < 0) value = -INF_F;
+    }
+    const float xl = label >= 0 ? Elem<E>::get(row[label]) : 0.f;
+    const int e = edge_of(c, a.V, id);
+    float xe = e >= 0 ? Elem<E>::get(row[e]) : -INF_F;
+    bool bad = v >= a.V;
+    const bool on = v >= 0 && !bad;
+    const int vec = on && v >= c.head && v < c.tail0 ? (v - c.head) / kN : -1;
+    if (on) {
+      x = Elem<E>::get(row[v]);
+      bad = (atomicOr(&bits[v >> 5], 1u << (v & 31)) >> (v & 31) & 1) != 0;
+      if (vec >= 0) atomicOr(&flags[vec >> 5], 1u << (vec & 31));
+    }
+    if (lists) {
+      const float mv = warp_max(value), sv = warp_add(v >= 0 ? expf((value - base_of(mv)) * terms.inv) : 0.f);
+      const float mx = warp_max(x), sx = warp_add(on ? expf((x - base_of(mx)) * terms.inv) : 0.f);
+      const float s1 = kBoth ? warp_add(on ? expf(x - base_of(mx)) : 0.f) : 0.f;
+      if (lane == 0) {
+        sh.lists[warp] = make_float4(mv, sv, mx, sx);
+        sh.lists_plain[warp] = s1;
+      }
+    }
+    if (__syncthreads_or(bad)) {
+      if (id == 0) {
+        report(a.err, LORA_DERR_BAD_LABEL);
+        put_nothing(a, t);
+      }
+      if (out != nullptr) zero_share<E, kStream>(c, out, a.V, id);
+      if (on) bits[v >> 5] = 0;
+      if (vec >= 0) flags[vec >> 5] = 0;
+      __syncthreads();
+      continue;
+    }
+    auto listed = [&](int i) { return (bits[i >> 5] >> (i & 31) & 1) != 0; };
+    if (e >= 0 && listed(e)) xe = -INF_F;
+    const bool label_listed = label >= 0 && listed(label);
+    // the rest's sum
+    Sum s{-INF_F, 0.f};
+    float s1 = 0.f;  // over the same base
+    auto add = [&](const auto& r, float top) {
+      const float m = fmaxf(s.m, top), base = base_of(m);
+      const float more = power_sum<E>(terms, r, base), more1 = kBoth ? power_sum<E>(plain, r, base) : 0.f;
+      if (m != s.m) {
+        s.s *= expf((s.m - base) * terms.inv);
+        if (kBoth) s1 *= expf(s.m - base);
+      }
+      s = Sum{m, s.s + more};
+      s1 += more1;
+    };
+    for (int i0 = 0; i0 < c.nvec; i0 += kBatch * kStream) {
+      uint4 r[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) r[u] = next[u];
+      // the next batch, or the gradient's first
+      const int i1 = i0 + kBatch * kStream;
+      load(mid, c.nvec, i1 < c.nvec ? i1 : 0, i1 < c.nvec ? keep : drop);
+      // (the words are the warp's, a bit a lane; those past the row's end are 0)
+      uint32_t some[kBatch], any = 0;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) any |= some[u] = flags[(i0 >> 5) + u * kStreamWarps + warp];
+      if (any != 0)
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          if (some[u] >> lane & 1) r[u] = low_vector<E>();
+      add(r, Elem<E>::top(r));
+    }
+    {  // a listed entry's vector, and the edges
+      uint4 r[1] = {low_vector<E>()};
+      if (vec >= 0) {
+        uint32_t which = 0;
+        const int from = c.head + vec * kN;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) which |= (uint32_t)listed(from + j) << j;
+        if (v == from + __ffs(which) - 1) r[0] = without(mid[vec], which, E{});
+      }
+      add(r, Elem<E>::top(r));
+      if (e >= 0) {
+        const float m = fmaxf(s.m, xe), base = base_of(m), fall = s.m - base;
+        s = Sum{m, s.s * expf(fall * terms.inv) + expf((xe - base) * terms.inv)};
+        if (kBoth) s1 = s1 * expf(fall) + expf(xe - base);
+      }
+    }
+    {
+      const float m = warp_max(s.m), fall = s.m - base_of(m);
+      const float sum = warp_add(s.s * expf(fall * terms.inv)), sum1 = kBoth ? warp_add(s1 * expf(fall)) : 0.f;
+      if (lane == 0) sh.part[warp] = make_float4(m, sum, sum1, 0.f);
+    }
+    __syncthreads();
+    if (on) bits[v >> 5] = 0;
+    if (vec >= 0) flags[vec >> 5] = 0;
+    // the row's sums and the lists', as every warp works them out
+    const RowSum rs = join_parts(sh.part, kStreamWarps, terms, kBoth, lane);
+    float4 list;
+    float list_plain;
+    {
+      const bool has = lane * 32 < a.k;
+      const float4 q = has ? sh.lists[lane] : make_float4(-INF_F, 0.f, -INF_F, 0.f);
+      const float high = base_of(fmaxf(warp_max(q.x), in.tail * a.opt.temperature)), mx = base_of(warp_max(q.z));
+      const float mass = warp_add(q.y * expf((base_of(q.x) - high) * terms.inv)) + expf(in.tail - high * terms.inv);
+      list = make_float4(high, logf(mass), mx, warp_add(q.w * expf((base_of(q.z) - mx) * terms.inv)));
+      list_plain = kBoth ? warp_add(has ? sh.lists_plain[lane] * expf(base_of(q.z) - mx) : 0.f) : 0.f;
+    }
+    const RowTotal r = row_total(rs, list, list_plain, terms, kBoth);
+    const float tail_p = in.tail - list.x * terms.inv - list.y, tail_q = r.lr;
+    // the outcomes: the entries', and the rest's by the last warp
+    Outcome o{0.f, 0.f, 0.f};
+    if (r.taught && (lists ? v >= 0 : id == kStream - 1)) {
+      const float lp = lists ? (value - list.x) * terms.inv - list.y : tail_p;
+      const float lq = lists ? (x - r.base) * terms.inv - r.lt : tail_q;
+      o = forward ? outcome(LORA_DISTILL_FORWARD, 0.f, lp, lq) : other_outcome(a.opt.kind, a.opt.mix, lp, lq);
+    }
+    if (lists || warp == kStreamWarps - 1) {
+      const float kd = warp_add(o.kd), mass = warp_add(o.mass);
+      if (lane == 0) sh.outcomes[lists ? warp : kMaxList / 32] = make_float2(kd, mass);
+    }
+    auto all_outcomes = [&] {
+      const float2 q = lane * 32 < a.k || lane == kMaxList / 32 ? sh.outcomes[lane] : make_float2(0.f, 0.f);
+      return make_float2(warp_add(q.x), warp_add(q.y));
+    };
+    float C = 0.f;
+    if (!forward) {
+      __syncthreads();
+      C = all_outcomes().y;
+    }
+    const float gs = r.none || in.weight == 0.f ? 0.f : a.opt.grad_scale * in.weight;
+    const float kw = gs != 0.f && fabsf(C) != INF_F ? gs * a.opt.kd_weight * terms.inv : 0.f;
+    const float cw = a.opt.ce_weight > 0.f ? gs * a.opt.ce_weight : 0.f;
+    const float slope =
+        kw != 0.f && r.taught && !(r.rest == 0.f) ? slope_of(a.opt.kind, a.opt.mix, tail_p - tail_q) - C : 0.f;
+    Slope g{r.base, kw != 0.f ? kw * slope : 0.f, r.lt * kLog2e + r.lt * kLog2eLo, cw, r.l1 * kLog2e + r.l1 * kLog2eLo};
+    if (!kBoth) g.kd += cw;
+    if (out != nullptr) {
+      if (g.kd == 0.f && (!kBoth || cw == 0.f)) {
+        zero_share<E, kStream>(c, out, a.V, id);
+      } else {
+        const bool wide = on_boundary(out, c);
+        E* const dst = out + c.head;
+        for (int i0 = 0; i0 < c.nvec; i0 += kBatch * kStream) {
+          uint4 y[kBatch];
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) y[u] = next[u];
+          const int i1 = i0 + kBatch * kStream;
+          if (i1 < c.nvec) {
+            load(mid, c.nvec, i1, drop);
+          } else if (t + gridDim.x < a.T) {  // the next row's first
+            loaded = t + gridDim.x;
+            const Cut<E> d = cut_row(row_at(loaded), a.V, 0, 1);
+            load(reinterpret_cast<const uint4*>(d.row + d.head), d.nvec, 0, keep);
+          }
+          E* const to = dst + (long long)(i0 + id) * kN;
+          if (wide && i1 <= c.nvec) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) store_as(to + u * kStream * kN, slope_vector<E, kBoth>(y[u], g, terms, plain), drop);
+          } else {
+            for (int u = 0; u < kBatch && i0 + u * kStream + id < c.nvec; ++u) {
+              uint4 x = y[0];
+#pragma unroll
+              for (int k = 1; k < kBatch; ++k) x = u == k ? y[k] : x;
+              const uint4 z = slope_vector<E, kBoth>(x, g, terms, plain);
+              if (wide) {
+                store_as(to + u * kStream * kN, z, drop);
+              } else {
+#pragma unroll
+                for (int j = 0; j < kN; ++j) to[u * kStream * kN + j] = Elem<E>::entry(z, j);
+              }
+            }
+          }
+        }
+        // (the edge's logit again: the sum's may be taken out)
+        if (e >= 0) out[e] = Elem<E>::put(slope_entry<kBoth>(xe, g, terms, plain));
+      }
+    }
+    __syncthreads();  // the listed places are written last
+    if (out != nullptr && (kw != 0.f || cw != 0.f)) {
+      if (on) {
+        const float d = x - r.base;
+        float y = kw != 0.f && r.taught ? kw * o.share : 0.f;
+        if (!forward || cw != 0.f) {
+          const float q = expf(d * terms.inv - r.lt);
+          if (!forward && kw != 0.f) y -= kw * q * C;
+          if (cw != 0.f) y += cw * ((kBoth ? expf(d - r.l1) : q) - (v == label ? 1.f : 0.f));
+        }
+        out[v] = Elem<E>::put(y);
+      }
+      if (id == kStream - 1 && label >= 0 && !label_listed && cw != 0.f) {
+        const float d = xl - r.base, q = expf(d * terms.inv - r.lt);
+        out[label] = Elem<E>::put(kw * slope * q + cw * ((kBoth ? expf(d - r.l1) : q) - 1.f));
+      }
+    }
+    if (warp == kStreamWarps - 1) {
+      const float kd = all_outcomes().x;
+      if (lane == 0) {
+        const float ce = a.opt.ce_weight > 0.f ? (r.none ? INF_F : r.l1 - (xl - r.base)) : 0.f;
+        put_losses(a, t, in, r.none ? (list.y != -INF_F ? INF_F : 0.f) : kd, ce);
+      }
+    }
   }
 }
 
@@ -736,10 +943,24 @@ lora_status_t launch_held(DistillArgs& a, int n, cudaStream_t s) {
   return launch_pdl(f, dim3((unsigned)ctas), dim3(kG + 32), smem, s, n, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
 
+template <typename E>
+lora_status_t launch_stream(DistillArgs& a, cudaStream_t s) {
+  const void* f = a.both ? (const void*)stream_kernel<E, true> : (const void*)stream_kernel<E, false>;
+  const size_t batch = (size_t)kBatch * kStream;  // flags for whole batches
+  const size_t smem = 4 * (((size_t)a.V + 31) / 32 + (a.V / Elem<E>::kN / batch + 1) * (batch / 32));
+  if (smem > 200000) return LORA_ERR_UNSUPPORTED;
+  if (ensure_smem_attr(f, smem) != cudaSuccess) return LORA_ERR_CUDA;
+  int per = 2;
+  if (getenv("DPER")) per = atoi(getenv("DPER"));
+  const int ctas = std::min(a.T, per * sm_count());
+  return launch_pdl(f, dim3((unsigned)ctas), dim3(kStream), smem, s, 0, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+}
+
 // The form of the rows, as the policy loss's are chosen (logits.cu): CTAs of four, then
 // eight vectors a thread while a row to each group leaves SMs idle, else of sixteen.
 template <typename E>
 lora_status_t launch(DistillArgs& a, cudaStream_t s) {
+  if (getenv("DSTREAM")) return launch_stream<E>(a, s);
   const long long vec = a.V / Elem<E>::kN, places = 2LL * sm_count();
   auto ctas = [&](int threads, int vecs) {
     int n = 1;
@@ -752,11 +973,7 @@ lora_status_t launch(DistillArgs& a, cudaStream_t s) {
     return launch_held<E, 256, 8>(a, ctas(256, 8), s);
   if (ctas(256, 16) <= kMaxCluster) return launch_held<E, 256, 16>(a, ctas(256, 16), s);
   if (ctas(512, 16) <= kMaxCluster) return launch_held<E, 512, 16>(a, ctas(512, 16), s);
-  const void* f = (const void*)long_row_kernel<E>;
-  const size_t smem = ((size_t)a.V + 31) / 32 * 4;
-  if (smem > 200000) return LORA_ERR_UNSUPPORTED;
-  if (ensure_smem_attr(f, smem) != cudaSuccess) return LORA_ERR_CUDA;
-  return launch_pdl(f, dim3((unsigned)a.T), dim3(kThreads), smem, s, 0, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  return launch_stream<E>(a, s);
 }
 
 }  // namespace

@@ -2,9 +2,6 @@
 // exponentials, and the checks that every call on logits makes of its rows.
 #pragma once
 
-#include <algorithm>
-#include <cmath>
-
 #include "common.cuh"
 #include "lora_train.h"
 #include "pairs.cuh"
@@ -207,9 +204,9 @@ __device__ __forceinline__ bool on_boundary(const E* out, const Cut<E>& c) {
   return (reinterpret_cast<uintptr_t>(out + c.head) & 15) == 0;
 }
 
-// Terms exp((x - base) / temperature): log2(e) / temperature in two parts, and the temperature's inverse.
+// Terms exp((x - base) / temperature): log2(e) / temperature rounded, and the temperature's inverse.
 struct Terms {
-  float hi, lo, inv;
+  float near, inv;
   __device__ __forceinline__ Sum join(const Sum& x, const Sum& y) const {
     Sum r;
     r.m = fmaxf(x.m, y.m);
@@ -218,8 +215,7 @@ struct Terms {
     return r;
   }
   __device__ __forceinline__ float power(float x, float base) const {  // of finite base
-    const float d = x - base;
-    return ex2(fmaf(d, hi, d * lo));
+    return ex2((x - base) * near);
   }
   __device__ __forceinline__ Sum add(const Sum& t, float x) const {
     return join(t, Sum{x, x == x ? (x == -INF_F ? 0.f : x == INF_F ? x : 1.f) : x});
@@ -230,19 +226,20 @@ struct Terms {
   }
 };
 
-// The sum of exp((x - base) / temperature) over some vectors.
+// The sum of exp((x - base) / temperature) over some vectors.  The factor is its greater part
+// alone: the difference comes first, so what that leaves out moves a term by 1e-8 (x - base)
+// of itself, and the terms that make the sum have small differences.
 template <typename E, int N>
 __device__ __forceinline__ float power_sum(const Terms& e, const uint4 (&r)[N], float base) {
   constexpr int kPairs = Elem<E>::kPairs;
-  const uint64_t hi = pair_of(e.hi, e.hi), lo = pair_of(e.lo, e.lo), nb = pair_of(-base, -base);
+  const uint64_t hi = pair_of(e.near, e.near), nb = pair_of(-base, -base);
   uint64_t part = pair_of(0.f, 0.f);
 #pragma unroll
   for (int u = 0; u < N; ++u) {
 #pragma unroll
     for (int k = 0; k < kPairs; ++k) {
-      const uint64_t d = add2(Elem<E>::pair(r[u], k), nb);
       float a, b;
-      split(fma2(d, hi, mul2(d, lo)), a, b);
+      split(mul2(add2(Elem<E>::pair(r[u], k), nb), hi), a, b);
       part = add2(part, pair_of(ex2(a), ex2(b)));
     }
   }
@@ -278,16 +275,7 @@ __device__ __forceinline__ float top_nan(const uint4& v, float) {
 
 // ------------------------------------------------------------------- host --
 
-// The terms of a temperature.  Neither part of the factor is 0: -inf times both is -inf.
-inline Terms terms_of(float temperature) {
-  const double per = 1.4426950408889634 / (double)temperature;
-  Terms t;
-  t.hi = (float)per;
-  if ((double)t.hi > per) t.hi = std::nextafter(t.hi, 0.f);
-  t.lo = std::max((float)(per - (double)t.hi), 1e-30f);
-  t.inv = 1.f / temperature;
-  return t;
-}
+inline Terms terms_of(float temperature) { return Terms{(float)(1.4426950408889634 / (double)temperature), 1.f / temperature}; }
 
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 

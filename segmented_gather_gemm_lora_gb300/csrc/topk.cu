@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, kResident) topk_kernel(const __grid_
     return;
   }
   const int k = a.k, m = (k + kWarps - 1) / kWarps;
-  const Terms terms{a.terms.hi, a.terms.lo, a.tail != nullptr ? a.terms.inv : 0.f};
+  const Terms terms{a.terms.near, a.tail != nullptr ? a.terms.inv : 0.f};
   auto cut_at = [&](int row) { return cut_row(static_cast<const E*>(a.logits) + (long long)row * a.ld, a.V, rank, n); };
   auto load = [&](const Cut<E>& c, int i, uint4 (&r)[kVec]) {
     const uint4* const mid = reinterpret_cast<const uint4*>(c.row + c.head);

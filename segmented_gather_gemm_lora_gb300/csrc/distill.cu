@@ -174,6 +174,7 @@ __device__ __forceinline__ void put_losses(const DistillArgs& a, long long t, co
 // row's barriers, which the other CTA of the SM hides.
 
 constexpr int kMaxCluster = 8;
+constexpr int kHeld = 256;  // threads that hold a row's share
 constexpr int kMaxList = LORA_TOPK_MAX;
 
 template <int kG>
@@ -264,7 +265,7 @@ __device__ __forceinline__ RowTotal row_total(const RowSum& s, const float4& lis
 }
 
 template <typename E, int kG, int kVec, bool kBoth>
-__global__ void __launch_bounds__(kG + 32, kG > 256 ? 1 : kVec > 8 ? 2 : 3) held_kernel(const __grid_constant__ DistillArgs a) {
+__global__ void __launch_bounds__(kG + 32, kVec > 8 ? 2 : 3) held_kernel(const __grid_constant__ DistillArgs a) {
   constexpr int kN = Elem<E>::kN, kAll = kG + 32;
   using Shared = HeldShared<kG>;
   extern __shared__ __align__(128) uint4 coming[];  // the coming row's share, then its bits
@@ -628,8 +629,8 @@ __device__ __forceinline__ uint4 without(const uint4& v, uint32_t m, float) {
 
 // -------------------------------------------------------------- streamed form --
 //
-// Many rows, or rows longer than the held form takes: a CTA a row, which it reads for its
-// sum and again for its gradient.  Few rows are under way (one or two an SM), so the
+// Many rows, short rows and the longest: a CTA a row, which it reads for its
+// sum and again for its gradient.  Few rows are under way (one to eight an SM), so the
 // second read finds the row in L2; outputs are written past it.  A row costs its barriers
 // once, not once in each of a cluster's CTAs, and its CTA has no other to wait for.
 //
@@ -637,16 +638,12 @@ __device__ __forceinline__ uint4 without(const uint4& v, uint32_t m, float) {
 // out of the sum as it goes by; the thread of the lowest entry of such a vector adds what
 // is not listed of it.
 
-constexpr int kStream = 512;  // threads
-constexpr int kStreamWarps = kStream / 32;
-#ifndef PROMOTE
-#define PROMOTE 4
-#endif
-constexpr int kBatch = PROMOTE;  // vectors a thread takes at once
+constexpr int kBatch = 4;  // vectors a thread takes at once
 
+template <int kT>
 struct StreamShared {
   uint64_t probe_bar;
-  float4 part[kStreamWarps];          // m, the sum, its sum at temperature 1
+  float4 part[kT / 32];               // m, the sum, its sum at temperature 1
   float4 lists[kMaxList / 32];        // a warp's entries: teacher's maximum and sum, student's
   float lists_plain[kMaxList / 32];
   float2 outcomes[kMaxList / 32 + 1];  // kd, mass; the rest's last
@@ -677,15 +674,15 @@ __device__ __forceinline__ void store_as(void* p, const uint4& v, uint64_t polic
                : "memory");
 }
 
-template <typename E, bool kBoth>
-__global__ void __launch_bounds__(kStream, 2) stream_kernel(const __grid_constant__ DistillArgs a) {
-  constexpr int kN = Elem<E>::kN;
+template <typename E, int kT, bool kBoth>
+__global__ void __launch_bounds__(kT, 1024 / kT) stream_kernel(const __grid_constant__ DistillArgs a) {
+  constexpr int kN = Elem<E>::kN, kW = kT / 32;
   extern __shared__ uint32_t bits[];  // of the entries, then of the vectors
-  __shared__ StreamShared sh;
+  __shared__ StreamShared<kT> sh;
   const int id = (int)threadIdx.x, lane = id & 31, warp = id >> 5;
   uint32_t* const flags = bits + (a.V + 31) / 32;
-  const int words = (a.V + 31) / 32 + (a.V / kN / (kBatch * kStream) + 1) * kBatch * kStreamWarps;
-  for (int i = id; i < words; i += kStream) bits[i] = 0;
+  const int words = (a.V + 31) / 32 + (a.V / kN / (kBatch * kT) + 1) * kBatch * kW;
+  for (int i = id; i < words; i += kT) bits[i] = 0;
   pdl_wait_then_release();
   if (a.probe > 0) {
     if (id == 0 && !wait_probe(&sh.probe_bar, a.probe)) report(a.err, LORA_DERR_TIMEOUT);
@@ -700,12 +697,12 @@ __global__ void __launch_bounds__(kStream, 2) stream_kernel(const __grid_constan
   const uint64_t keep = keep_lines(), drop = drop_lines();
   auto load = [&](const uint4* mid, int nvec, int i0, uint64_t policy) {
     const uint4* const p = mid + i0 + id;
-    if (i0 + kBatch * kStream <= nvec) {
+    if (i0 + kBatch * kT <= nvec) {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) next[u] = load_as(p + u * kStream, policy);
+      for (int u = 0; u < kBatch; ++u) next[u] = load_as(p + u * kT, policy);
     } else {
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) next[u] = i0 + u * kStream + id < nvec ? load_as(p + u * kStream, policy) : low_vector<E>();
+      for (int u = 0; u < kBatch; ++u) next[u] = i0 + u * kT + id < nvec ? load_as(p + u * kT, policy) : low_vector<E>();
     }
   };
   long long loaded = -1;  // the row whose first batch is in next
@@ -719,7 +716,7 @@ __global__ void __launch_bounds__(kStream, 2) stream_kernel(const __grid_constan
         if (label >= a.V) report(a.err, LORA_DERR_BAD_LABEL);
         put_nothing(a, t);
       }
-      if (out != nullptr) zero_share<E, kStream>(c, out, a.V, id);
+      if (out != nullptr) zero_share<E, kT>(c, out, a.V, id);
       continue;
     }
     const uint4* const mid = reinterpret_cast<const uint4*>(row + c.head);
@@ -759,7 +756,7 @@ __global__ void __launch_bounds__(kStream, 2) stream_kernel(const __grid_constan
         report(a.err, LORA_DERR_BAD_LABEL);
         put_nothing(a, t);
       }
-      if (out != nullptr) zero_share<E, kStream>(c, out, a.V, id);
+      if (out != nullptr) zero_share<E, kT>(c, out, a.V, id);
       if (on) bits[v >> 5] = 0;
       if (vec >= 0) flags[vec >> 5] = 0;
       __syncthreads();
@@ -781,17 +778,17 @@ __global__ void __launch_bounds__(kStream, 2) stream_kernel(const __grid_constan
       s = Sum{m, s.s + more};
       s1 += more1;
     };
-    for (int i0 = 0; i0 < c.nvec; i0 += kBatch * kStream) {
+    for (int i0 = 0; i0 < c.nvec; i0 += kBatch * kT) {
       uint4 r[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) r[u] = next[u];
       // the next batch, or the gradient's first
-      const int i1 = i0 + kBatch * kStream;
+      const int i1 = i0 + kBatch * kT;
       load(mid, c.nvec, i1 < c.nvec ? i1 : 0, i1 < c.nvec ? keep : drop);
       // (the words are the warp's, a bit a lane; those past the row's end are 0)
       uint32_t some[kBatch], any = 0;
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) any |= some[u] = flags[(i0 >> 5) + u * kStreamWarps + warp];
+      for (int u = 0; u < kBatch; ++u) any |= some[u] = flags[(i0 >> 5) + u * kW + warp];
       if (any != 0)
 #pragma unroll
         for (int u = 0; u < kBatch; ++u)
@@ -823,7 +820,7 @@ __global__ void __launch_bounds__(kStream, 2) stream_kernel(const __grid_constan
     if (on) bits[v >> 5] = 0;
     if (vec >= 0) flags[vec >> 5] = 0;
     // the row's sums and the lists', as every warp works them out
-    const RowSum rs = join_parts(sh.part, kStreamWarps, terms, kBoth, lane);
+    const RowSum rs = join_parts(sh.part, kW, terms, kBoth, lane);
     float4 list;
     float list_plain;
     {
@@ -838,12 +835,12 @@ __global__ void __launch_bounds__(kStream, 2) stream_kernel(const __grid_constan
     const float tail_p = in.tail - list.x * terms.inv - list.y, tail_q = r.lr;
     // the outcomes: the entries', and the rest's by the last warp
     Outcome o{0.f, 0.f, 0.f};
-    if (r.taught && (lists ? v >= 0 : id == kStream - 1)) {
+    if (r.taught && (lists ? v >= 0 : id == kT - 1)) {
       const float lp = lists ? (value - list.x) * terms.inv - list.y : tail_p;
       const float lq = lists ? (x - r.base) * terms.inv - r.lt : tail_q;
       o = forward ? outcome(LORA_DISTILL_FORWARD, 0.f, lp, lq) : other_outcome(a.opt.kind, a.opt.mix, lp, lq);
     }
-    if (lists || warp == kStreamWarps - 1) {
+    if (lists || warp == kW - 1) {
       const float kd = warp_add(o.kd), mass = warp_add(o.mass);
       if (lane == 0) sh.outcomes[lists ? warp : kMaxList / 32] = make_float2(kd, mass);
     }
@@ -865,15 +862,15 @@ __global__ void __launch_bounds__(kStream, 2) stream_kernel(const __grid_constan
     if (!kBoth) g.kd += cw;
     if (out != nullptr) {
       if (g.kd == 0.f && (!kBoth || cw == 0.f)) {
-        zero_share<E, kStream>(c, out, a.V, id);
+        zero_share<E, kT>(c, out, a.V, id);
       } else {
         const bool wide = on_boundary(out, c);
         E* const dst = out + c.head;
-        for (int i0 = 0; i0 < c.nvec; i0 += kBatch * kStream) {
+        for (int i0 = 0; i0 < c.nvec; i0 += kBatch * kT) {
           uint4 y[kBatch];
 #pragma unroll
           for (int u = 0; u < kBatch; ++u) y[u] = next[u];
-          const int i1 = i0 + kBatch * kStream;
+          const int i1 = i0 + kBatch * kT;
           if (i1 < c.nvec) {
             load(mid, c.nvec, i1, drop);
           } else if (t + gridDim.x < a.T) {  // the next row's first
@@ -884,18 +881,18 @@ __global__ void __launch_bounds__(kStream, 2) stream_kernel(const __grid_constan
           E* const to = dst + (long long)(i0 + id) * kN;
           if (wide && i1 <= c.nvec) {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) store_as(to + u * kStream * kN, slope_vector<E, kBoth>(y[u], g, terms, plain), drop);
+            for (int u = 0; u < kBatch; ++u) store_as(to + u * kT * kN, slope_vector<E, kBoth>(y[u], g, terms, plain), drop);
           } else {
-            for (int u = 0; u < kBatch && i0 + u * kStream + id < c.nvec; ++u) {
+            for (int u = 0; u < kBatch && i0 + u * kT + id < c.nvec; ++u) {
               uint4 x = y[0];
 #pragma unroll
               for (int k = 1; k < kBatch; ++k) x = u == k ? y[k] : x;
               const uint4 z = slope_vector<E, kBoth>(x, g, terms, plain);
               if (wide) {
-                store_as(to + u * kStream * kN, z, drop);
+                store_as(to + u * kT * kN, z, drop);
               } else {
 #pragma unroll
-                for (int j = 0; j < kN; ++j) to[u * kStream * kN + j] = Elem<E>::entry(z, j);
+                for (int j = 0; j < kN; ++j) to[u * kT * kN + j] = Elem<E>::entry(z, j);
               }
             }
           }
@@ -916,12 +913,12 @@ __global__ void __launch_bounds__(kStream, 2) stream_kernel(const __grid_constan
         }
         out[v] = Elem<E>::put(y);
       }
-      if (id == kStream - 1 && label >= 0 && !label_listed && cw != 0.f) {
+      if (id == kT - 1 && label >= 0 && !label_listed && cw != 0.f) {
         const float d = xl - r.base, q = expf(d * terms.inv - r.lt);
         out[label] = Elem<E>::put(kw * slope * q + cw * ((kBoth ? expf(d - r.l1) : q) - 1.f));
       }
     }
-    if (warp == kStreamWarps - 1) {
+    if (warp == kW - 1) {
       const float kd = all_outcomes().x;
       if (lane == 0) {
         const float ce = a.opt.ce_weight > 0.f ? (r.none ? INF_F : r.l1 - (xl - r.base)) : 0.f;
@@ -943,37 +940,46 @@ lora_status_t launch_held(DistillArgs& a, int n, cudaStream_t s) {
   return launch_pdl(f, dim3((unsigned)ctas), dim3(kG + 32), smem, s, n, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
 
-template <typename E>
+template <typename E, int kT>
 lora_status_t launch_stream(DistillArgs& a, cudaStream_t s) {
-  const void* f = a.both ? (const void*)stream_kernel<E, true> : (const void*)stream_kernel<E, false>;
-  const size_t batch = (size_t)kBatch * kStream;  // flags for whole batches
+  const void* f = a.both ? (const void*)stream_kernel<E, kT, true> : (const void*)stream_kernel<E, kT, false>;
+  const size_t batch = (size_t)kBatch * kT;  // flags for whole batches
   const size_t smem = 4 * (((size_t)a.V + 31) / 32 + (a.V / Elem<E>::kN / batch + 1) * (batch / 32));
   if (smem > 200000) return LORA_ERR_UNSUPPORTED;
   if (ensure_smem_attr(f, smem) != cudaSuccess) return LORA_ERR_CUDA;
-  int per = 2;
-  if (getenv("DPER")) per = atoi(getenv("DPER"));
-  const int ctas = std::min(a.T, per * sm_count());
-  return launch_pdl(f, dim3((unsigned)ctas), dim3(kStream), smem, s, 0, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  const int ctas = std::min(a.T, 1024 / kT * sm_count());
+  return launch_pdl(f, dim3((unsigned)ctas), dim3(kT), smem, s, 0, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
 
-// The form of the rows, as the policy loss's are chosen (logits.cu): CTAs of four, then
-// eight vectors a thread while a row to each group leaves SMs idle, else of sixteen.
+// The form of the rows (device times in us on a GB300, 64 listed, forward; streamed with 256 /
+// 512 / 1024 threads a row, 4 / 2 / 1 rows an SM at once):
+//  - held while the rows' clusters of 16 vectors a thread are one wave and a row is more than
+//    64 KB.  16 x 128256 bf16: 8.6, streamed 17.7 / 15.3 / 15.9; 64: 12.5, 21.4 / 16.6 / 16.7;
+//    150 (two waves): 27.2, 23.4 / 19.0 / 18.4.  64 x 32000: 8.7, 8.1 / 8.0 / 9.1.
+//  - else streamed, with so many rows at once that L2 holds them.  8192 x 32000 bf16: 216 / 308 /
+//    463 (held 245); 4000 x 50257 with jsd 181 / 224 / 350 (270); 8192 x 128256 929 / 808 / 933
+//    (935); 2000 x 151936 fp32 584 / 545 / 509.
+//  - of short rows more at once: 8192 x 1000 with 128 threads 50, 256 90.
+// The last warp has no entries: it works out the rest.
 template <typename E>
 lora_status_t launch(DistillArgs& a, cudaStream_t s) {
-  if (getenv("DSTREAM")) return launch_stream<E>(a, s);
-  const long long vec = a.V / Elem<E>::kN, places = 2LL * sm_count();
-  auto ctas = [&](int threads, int vecs) {
+  const int sms = sm_count(), last = 32;
+  const long long vec = a.V / Elem<E>::kN, places = 2LL * sms, bytes = (long long)a.V * (long long)sizeof(E);
+  auto ctas = [&](int vecs) {
     int n = 1;
-    while (vec > (long long)n * threads * vecs) n *= 2;
+    while (vec > (long long)n * kHeld * vecs) n *= 2;
     return n;
   };
-  if (vec <= 1024) return launch_held<E, 256, 4>(a, 1, s);
-  if (ctas(256, 4) <= kMaxCluster && (long long)a.T * ctas(256, 4) <= places) return launch_held<E, 256, 4>(a, ctas(256, 4), s);
-  if (vec <= 2048 || (ctas(256, 8) <= kMaxCluster && (long long)a.T * ctas(256, 8) <= places))
-    return launch_held<E, 256, 8>(a, ctas(256, 8), s);
-  if (ctas(256, 16) <= kMaxCluster) return launch_held<E, 256, 16>(a, ctas(256, 16), s);
-  if (ctas(512, 16) <= kMaxCluster) return launch_held<E, 512, 16>(a, ctas(512, 16), s);
-  return launch_stream<E>(a, s);
+  if (bytes > 65536 && ctas(16) <= kMaxCluster && a.T * ctas(16) <= places) {
+    for (int vecs = 4; vecs <= 8; vecs *= 2)
+      if (ctas(vecs) <= kMaxCluster && a.T * ctas(vecs) <= places)
+        return vecs == 4 ? launch_held<E, kHeld, 4>(a, ctas(4), s) : launch_held<E, kHeld, 8>(a, ctas(8), s);
+    return launch_held<E, kHeld, 16>(a, ctas(16), s);
+  }
+  if (bytes <= 8192 && a.T > 4 * sms && a.k <= 128 - last) return launch_stream<E, 128>(a, s);
+  if (a.k <= 256 - last && bytes * 4 * sms <= 64 << 20 && (a.T > sms || bytes <= 32768)) return launch_stream<E, 256>(a, s);
+  if (bytes * 2 * sms <= 96 << 20) return launch_stream<E, 512>(a, s);
+  return launch_stream<E, 1024>(a, s);
 }
 
 }  // namespace

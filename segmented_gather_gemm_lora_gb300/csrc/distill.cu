@@ -614,19 +614,6 @@ __global__ void __launch_bounds__(kG + 32, kVec > 8 ? 2 : 3) held_kernel(const _
   if (n > 1) cluster_sync();
 }
 
-// A vector without the elements that `m` says.
-__device__ __forceinline__ uint32_t word_without(uint32_t w, uint32_t m) {
-  if (m & 1) w = (w & 0xffff0000u) | 0xff80u;
-  if (m & 2) w = (w & 0xffffu) | 0xff800000u;
-  return w;
-}
-__device__ __forceinline__ uint4 without(const uint4& v, uint32_t m, uint16_t) {
-  return make_uint4(word_without(v.x, m), word_without(v.y, m >> 2), word_without(v.z, m >> 4), word_without(v.w, m >> 6));
-}
-__device__ __forceinline__ uint4 without(const uint4& v, uint32_t m, float) {
-  return make_uint4(m & 1 ? 0xff800000u : v.x, m & 2 ? 0xff800000u : v.y, m & 4 ? 0xff800000u : v.z, m & 8 ? 0xff800000u : v.w);
-}
-
 // -------------------------------------------------------------- streamed form --
 //
 // Many rows, short rows and the longest: a CTA a row, which it reads for its

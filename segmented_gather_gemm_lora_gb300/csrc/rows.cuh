@@ -273,6 +273,34 @@ __device__ __forceinline__ float top_nan(const uint4& v, float) {
   return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
 }
 
+// Which elements of a vector do not lie below `least` (a NaN does not).
+__device__ __forceinline__ uint32_t reaching(const uint4& v, float least, uint16_t) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
+    m |= (bf_lo(w) < least ? 0u : 1u << (2 * k)) | (bf_hi(w) < least ? 0u : 2u << (2 * k));
+  }
+  return m;
+}
+__device__ __forceinline__ uint32_t reaching(const uint4& v, float least, float) {
+  return (__uint_as_float(v.x) < least ? 0u : 1u) | (__uint_as_float(v.y) < least ? 0u : 2u) |
+         (__uint_as_float(v.z) < least ? 0u : 4u) | (__uint_as_float(v.w) < least ? 0u : 8u);
+}
+
+// A vector without the elements that `m` says.
+__device__ __forceinline__ uint32_t word_without(uint32_t w, uint32_t m) {
+  if (m & 1) w = (w & 0xffff0000u) | 0xff80u;
+  if (m & 2) w = (w & 0xffffu) | 0xff800000u;
+  return w;
+}
+__device__ __forceinline__ uint4 without(const uint4& v, uint32_t m, uint16_t) {
+  return make_uint4(word_without(v.x, m), word_without(v.y, m >> 2), word_without(v.z, m >> 4), word_without(v.w, m >> 6));
+}
+__device__ __forceinline__ uint4 without(const uint4& v, uint32_t m, float) {
+  return make_uint4(m & 1 ? 0xff800000u : v.x, m & 2 ? 0xff800000u : v.y, m & 4 ? 0xff800000u : v.z, m & 8 ? 0xff800000u : v.w);
+}
+
 // ------------------------------------------------------------------- host --
 
 inline Terms terms_of(float temperature) { return Terms{(float)(1.4426950408889634 / (double)temperature), 1.f / temperature}; }

@@ -368,24 +368,24 @@ __global__ void __launch_bounds__(kThreads, kResident) topk_kernel(const __grid_
   floor_ = max(floor_, key_of(kLowest));
   // x reaches key `least` (a NaN reaches every key, and only a NaN a NaN's)
   auto reaches = [](float x, float least) { return least == least ? !(x < least) : x != x; };
-  auto reaching = [&](uint32_t least) {
+  auto slots_from = [&](uint32_t least) {
     const float v = value_of(least);
     int some = 0;
     for (int s = 0; s <= slots; ++s) some += reaches(sh.slot[s][tid].x, v);
     return some;
   };
   int n_listed;
-  int at = places(reaching(floor_), &sh, &n_listed);
+  int at = places(slots_from(floor_), &sh, &n_listed);
   if (n_listed > kListed) {
     // bit by bit up to the k-th largest (its upper 16 bits)
     uint32_t step = 1u << 31;
     for (uint32_t high = 0; step >= 1u << 16; step >>= 1) {
       const uint32_t next_key = high | step;
-      places(reaching(next_key), &sh, &n_listed);
+      places(slots_from(next_key), &sh, &n_listed);
       if (n_listed >= k) high = next_key;
       if (step == 1u << 16) floor_ = max(floor_, high);
     }
-    at = places(reaching(floor_), &sh, &n_listed);
+    at = places(slots_from(floor_), &sh, &n_listed);
   }
   bool slow = n_listed > kListed;  // the same for all threads
   uint32_t bound = floor_;
@@ -428,31 +428,54 @@ __global__ void __launch_bounds__(kThreads, kResident) topk_kernel(const __grid_
   }
   const uint32_t threshold = slow ? 0 : max(bound, sh.threshold[0]);
   if (!slow) {
-    // the entries that reach it, of the slots that do; a slot's other entries into the sum
+    // The entries that reach it, of the slots that do; a slot's other entries into the sum.
+    // A thread a slot; f(vectors, what reaches of them, the place of an element of them).
+    const float least = value_of(threshold);
+    const uint4* const mid = reinterpret_cast<const uint4*>(c.row + c.head);
     auto each = [&](int id, auto f) {
-      const int s = id / kThreads, v = id % kThreads;
+      const int s = id / kThreads, thread = id % kThreads;
+      uint4 x[kVec];
       if (s == slots) {
-        const int e = edge_of(c, a.V, v);
-        if (e >= 0) f(e, Elem<E>::get(c.row[e]));
+        const int e = edge_of(c, a.V, thread);
+#pragma unroll
+        for (int u = 0; u < kVec; ++u) x[u] = low_vector<E>();
+        const float v = e >= 0 ? Elem<E>::get(c.row[e]) : -INF_F;
+        x[0].x = sizeof(E) == 2 ? 0xff800000u | __float_as_uint(v) >> 16 : __float_as_uint(v);
+        f(x, reaches(v, least) ? 1u : 0u, [&](int) { return e; });
         return;
       }
-      for (int i = s * group * kVec, end = min(s + 1, kRows) * group * kVec; i < end; ++i) {
-        const int vec = c.v0 + v + i * kThreads;
-        if (vec >= c.v1) break;
-        const uint4 x = reinterpret_cast<const uint4*>(c.row + c.head)[vec];
+      for (int chunk = s * group; chunk < min(chunks, (s + 1) * group); ++chunk) {
+        const int i = c.v0 + chunk * kVec * kThreads + thread;
+        uint32_t which = 0;
 #pragma unroll
-        for (int j = 0; j < kN; ++j) f(c.head + vec * kN + j, Elem<E>::get(Elem<E>::entry(x, j)));
+        for (int u = 0; u < kVec; ++u) x[u] = i + u * kThreads < c.v1 ? mid[i + u * kThreads] : low_vector<E>();
+        if (least == least) {
+#pragma unroll
+          for (int u = 0; u < kVec; ++u) which |= reaching(x[u], least, E{}) << (u * kN);
+        } else {  // NaNs alone: what is not below +inf, but +inf itself
+#pragma unroll
+          for (int u = 0; u < kVec; ++u)
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+              const float v = Elem<E>::get(Elem<E>::entry(x[u], j));
+              which |= (v != v ? 1u : 0u) << (u * kN + j);
+            }
+        }
+        f(x, which, [&](int b) { return c.head + (i + b / kN * kThreads) * kN + b % kN; });
       }
     };
-    const float least = value_of(threshold);
+    auto hide = [&](uint4 (&x)[kVec], uint32_t which) {
+#pragma unroll
+      for (int u = 0; u < kVec; ++u) x[u] = without(x[u], which >> (u * kN) & ((1u << kN) - 1), E{});
+    };
     int some = 0;
     float top = -INF_F;  // of those below it
     for (int i = tid; i < n_listed; i += kThreads)
       if (sh.key[i] >= threshold)
-        each(sh.which[i], [&](int, float x) {
-          const bool in = reaches(x, least);
-          some += in;
-          top = fmaxf(top, in ? -INF_F : x);
+        each(sh.which[i], [&](uint4 (&x)[kVec], uint32_t which, auto) {
+          some += __popc(which);
+          hide(x, which);
+          top = fmaxf(top, Elem<E>::top(x));
         });
     at = places(some, &sh, &total);
     slow = total > kBest;
@@ -461,9 +484,13 @@ __global__ void __launch_bounds__(kThreads, kResident) topk_kernel(const __grid_
       float rest = 0.f;
       for (int i = tid; i < n_listed; i += kThreads)
         if (sh.key[i] >= threshold)
-          each(sh.which[i], [&](int idx, float x) {
-            if (reaches(x, least)) sh.best[at++] = composite(Entry{key_of(x), idx});
-            else rest += terms.power(x, base);
+          each(sh.which[i], [&](uint4 (&x)[kVec], uint32_t which, auto place) {
+            for (uint32_t w = which; w != 0; w &= w - 1) {
+              const int idx = place(__ffs(w) - 1);
+              sh.best[at++] = composite(Entry{key_of(Elem<E>::get(c.row[idx])), idx});
+            }
+            hide(x, which);
+            if (terms.inv > 0.f) rest += power_sum<E>(terms, x, base);
           });
       if (terms.inv > 0.f) {
         for (int s = 0; s <= slots; ++s) {
@@ -540,14 +567,17 @@ __global__ void __launch_bounds__(kThreads, kResident) topk_kernel(const __grid_
   // an entry's place is the number of entries before it
   if (tid < 2) sh.best[total + tid] = 0;
   __syncthreads();
-  for (int i = tid; i < total; i += kThreads) {
-    const unsigned long long mine = sh.best[i];
+  const int parts = total <= kThreads / 4 ? 4 : total <= kThreads / 2 ? 2 : 1;  // threads that share an entry's counting
+  for (int i = tid / parts; i - tid / parts < total; i += kThreads / parts) {
+    const unsigned long long mine = i < total ? sh.best[i] : ~0ull;
     int place = 0;
 #pragma unroll 4
-    for (int j = 0; j < total; j += 2) {
+    for (int j = 2 * (tid % parts); j < total; j += 2 * parts) {
       const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&sh.best[j]);
       place += (two.x > mine) + (two.y > mine);
     }
+    for (int d = 1; d < parts; d <<= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
+    if (i >= total || tid % parts != 0) continue;
     const Entry e = entry_of(mine);
     if (place < k) {
       a.ids[out + place] = e.idx;

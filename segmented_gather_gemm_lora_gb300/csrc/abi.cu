@@ -74,7 +74,7 @@ cudaError_t ensure_smem_attr(const void* func, size_t bytes) {
   // Raised even below 48 KB: the default limit covers dynamic and static shared
   // memory together, so a kernel with static shared memory of its own needs the
   // attribute for a dynamic size just under 48 KB too.
-  static SmemLimits<64, kMaxDevices> limits;
+  static SmemLimits<128, kMaxDevices> limits;
   auto set = [&] { return (int)cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); };
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);

@@ -957,9 +957,9 @@ lora_status_t launch(DistillArgs& a, cudaStream_t s) {
     while (vec > (long long)n * kHeld * vecs) n *= 2;
     return n;
   };
-  if (bytes > 65536 && ctas(16) <= kMaxCluster && a.T * ctas(16) <= places) {
+  if (bytes > 65536 && ctas(16) <= kMaxCluster && (long long)a.T * ctas(16) <= places) {
     for (int vecs = 4; vecs <= 8; vecs *= 2)
-      if (ctas(vecs) <= kMaxCluster && a.T * ctas(vecs) <= places)
+      if (ctas(vecs) <= kMaxCluster && (long long)a.T * ctas(vecs) <= places)
         return vecs == 4 ? launch_held<E, kHeld, 4>(a, ctas(4), s) : launch_held<E, kHeld, 8>(a, ctas(8), s);
     return launch_held<E, kHeld, 16>(a, ctas(16), s);
   }

@@ -315,12 +315,16 @@ long long scale_bytes(const lora_f8_matrix_t& m) {
   return 4 * ((blocks_of(m.rows, m.block_rows) - 1) * m.scale_row + (blocks_of(m.cols, LORA_F8_BLOCK) - 1) * m.scale_col + 1);
 }
 
+// Rows and columns of tiles, the last one's ends too, stay within 32 bits.
+constexpr int kMostRows = 0x7fff0000;
+
 lora_status_t check_f8(const lora_f8_matrix_t* m) {
   if (m == nullptr || m->rows < 0 || m->cols < 1) return LORA_ERR_INVALID_ARG;
   if (m->type != LORA_F8_E4M3 && m->type != LORA_F8_E5M2) return LORA_ERR_INVALID_ARG;
   if (m->block_rows != 1 && m->block_rows != LORA_F8_BLOCK) return LORA_ERR_INVALID_ARG;
   if (m->ld < m->cols || m->ld % 16 != 0 || m->scale_row < 0 || m->scale_col < 0) return LORA_ERR_INVALID_ARG;
   if (m->rows == 0) return LORA_OK;
+  if (m->rows > kMostRows || m->cols > kMostRows) return LORA_ERR_UNSUPPORTED;
   const long long most = 1LL << 40;
   if (m->ld > most / m->rows || m->scale_row > most / m->rows || m->scale_col > most / m->cols) return LORA_ERR_INVALID_ARG;
   if (m->codes == nullptr || !aligned_to(m->codes, 16)) return LORA_ERR_INVALID_ARG;
@@ -395,7 +399,9 @@ lora_status_t lora_f8_quantize(const void* x, int64_t ldx, int32_t dtype, const 
   a.step_s = (int)(ctas * takers % a.spans);
   const void* f = by_rows ? (bf16 ? rows_kernel<uint16_t>(q->type) : rows_kernel<float>(q->type))
                           : (bf16 ? block_kernel<uint16_t>(q->type) : block_kernel<float>(q->type));
-  return launch_pdl(f, dim3((unsigned)ctas), dim3((unsigned)(by_rows ? kQThreads : bf16 ? kBThreads<uint16_t> : kBThreads<float>)), 0, (cudaStream_t)stream, 0, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  const int threads = by_rows ? kQThreads : bf16 ? kBThreads<uint16_t> : kBThreads<float>;
+  return launch_pdl(f, dim3((unsigned)ctas), dim3((unsigned)threads), 0, (cudaStream_t)stream, 0, &a) == cudaSuccess ? LORA_OK
+                                                                                                                     : LORA_ERR_CUDA;
 }
 
 lora_status_t lora_base_f8(const lora_f8_matrix_t* x, const lora_f8_matrix_t* w, void* y, int64_t ldy, int32_t out_dtype,

@@ -65,7 +65,7 @@ __device__ __forceinline__ bool probe_passes(const GemmArgs& a) {
   return probe_ok != 0;
 }
 
-// Sixteen or so bytes of outputs from fp32 values, one rounding each.
+// Sixteen bytes of outputs from fp32 values, one rounding each.
 template <typename O>
 __device__ __forceinline__ uint4 pack_out(const float* f);
 template <>
@@ -606,7 +606,6 @@ __global__ void __launch_bounds__(kMThreads, 1) f8_mid_kernel(const __grid_const
 }
 
 // -------------------------------------------------------------------- split --
-
 
 template <int kNT>
 struct Split {

@@ -307,301 +307,301 @@ __global__ void __launch_bounds__(kThreads, kResident) topk_kernel(const __grid_
   // (with clusters a row each, else rows in turn, each one's first chunk loaded before the
   // row before it is finished)
   for (;;) {
-  const int next_row = n == 1 ? row + (int)gridDim.x : a.T;
-  const long long out = (long long)row * k;
-  const Cut<E> c = cut_at(row);
-  auto load_next = [&] {
-    if (next_row < a.T) {
-      const Cut<E> d = cut_at(next_row);
-      load(d, d.v0 + tid, r);
-    }
-  };
-  if (a.labels != nullptr && a.labels[row] < 0) {  // the whole cluster agrees
-    if (rank == 0) {
-      if (tid < k) {
-        a.ids[out + tid] = -1;
-        a.values[out + tid] = -INF_F;
+    const int next_row = n == 1 && row < a.T - (int)gridDim.x ? row + (int)gridDim.x : a.T;
+    const long long out = (long long)row * k;
+    const Cut<E> c = cut_at(row);
+    auto load_next = [&] {
+      if (next_row < a.T) {
+        const Cut<E> d = cut_at(next_row);
+        load(d, d.v0 + tid, r);
       }
-      if (tid == 0 && a.tail != nullptr) a.tail[row] = -INF_F;
+    };
+    if (a.labels != nullptr && a.labels[row] < 0) {  // the whole cluster agrees
+      if (rank == 0) {
+        if (tid < k) {
+          a.ids[out + tid] = -1;
+          a.values[out + tid] = -INF_F;
+        }
+        if (tid == 0 && a.tail != nullptr) a.tail[row] = -INF_F;
+      }
+      load_next();
+      if (next_row >= a.T) return;
+      row = next_row;
+      continue;
+    }
+    Sum t{-INF_F, 0.f};
+    int total = 0;
+    const int chunks = (c.v1 - c.v0 + kVec * kThreads - 1) / (kVec * kThreads), group = (chunks + kRows - 1) / kRows;  // chunks of a slot
+    const int slots = group > 0 ? (chunks + group - 1) / group : 0;
+    for (int s = 0, chunk = 0; s < slots; ++s) {
+      Sum w{-INF_F, 0.f};
+      float top = -INF_F;  // w's maximum, or a NaN
+      for (int g = 0; g < group && chunk < chunks; ++g, ++chunk) {
+        load(c, c.v0 + tid + (chunk + 1) * kVec * kThreads, next);
+        float m = top_nan(r[0], E{});
+#pragma unroll
+        for (int u = 1; u < kVec; ++u) m = max_nan(m, top_nan(r[u], E{}));
+        top = max_nan(top, m);
+        if (terms.inv > 0.f) w = add_vectors<E>(terms, w, r, m);
+#pragma unroll
+        for (int u = 0; u < kVec; ++u) r[u] = next[u];
+      }
+      sh.slot[s][tid] = make_float2(top, w.s);
+    }
+    {
+      const int e = edge_of(c, a.V, tid);
+      const float x = e >= 0 ? Elem<E>::get(c.row[e]) : -INF_F;
+      sh.slot[slots][tid] = make_float2(x, x == -INF_F ? 0.f : x == INF_F ? x : 1.f);
     }
     load_next();
-    if (next_row >= a.T) return;
-    row = next_row;
-    continue;
-  }
-  Sum t{-INF_F, 0.f};
-  int total = 0;
-  const int chunks = (c.v1 - c.v0 + kVec * kThreads - 1) / (kVec * kThreads), group = (chunks + kRows - 1) / kRows;  // chunks of a slot
-  const int slots = group > 0 ? (chunks + group - 1) / group : 0;
-  for (int s = 0, chunk = 0; s < slots; ++s) {
-    Sum w{-INF_F, 0.f};
-    float top = -INF_F;  // w's maximum, or a NaN
-    for (int g = 0; g < group && chunk < chunks; ++g, ++chunk) {
-      load(c, c.v0 + tid + (chunk + 1) * kVec * kThreads, next);
-      float m = top_nan(r[0], E{});
-#pragma unroll
-      for (int u = 1; u < kVec; ++u) m = max_nan(m, top_nan(r[u], E{}));
-      top = max_nan(top, m);
-      if (terms.inv > 0.f) w = add_vectors<E>(terms, w, r, m);
-#pragma unroll
-      for (int u = 0; u < kVec; ++u) r[u] = next[u];
-    }
-    sh.slot[s][tid] = make_float2(top, w.s);
-  }
-  {
-    const int e = edge_of(c, a.V, tid);
-    const float x = e >= 0 ? Elem<E>::get(c.row[e]) : -INF_F;
-    sh.slot[slots][tid] = make_float2(x, x == -INF_F ? 0.f : x == INF_F ? x : 1.f);
-  }
-  load_next();
 
-  // A threshold to begin with: the least of the warps' m-th lanes' largest entries, above
-  // -inf; then the slots that reach it.
-  float mine = -INF_F;
-  for (int s = 0; s <= slots; ++s) mine = max_nan(mine, sh.slot[s][tid].x);
-  const uint32_t sorted = sort_lanes(key_of(mine), lane);
-  if (lane == m - 1) sh.least[warp] = sorted;
-  __syncthreads();
-  uint32_t floor_ = sh.least[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) floor_ = min(floor_, sh.least[w]);
-  floor_ = max(floor_, key_of(kLowest));
-  // x reaches key `least` (a NaN reaches every key, and only a NaN a NaN's)
-  auto reaches = [](float x, float least) { return least == least ? !(x < least) : x != x; };
-  auto slots_from = [&](uint32_t least) {
-    const float v = value_of(least);
-    int some = 0;
-    for (int s = 0; s <= slots; ++s) some += reaches(sh.slot[s][tid].x, v);
-    return some;
-  };
-  int n_listed;
-  int at = places(slots_from(floor_), &sh, &n_listed);
-  if (n_listed > kListed) {
-    // bit by bit up to the k-th largest (its upper 16 bits)
-    uint32_t step = 1u << 31;
-    for (uint32_t high = 0; step >= 1u << 16; step >>= 1) {
-      const uint32_t next_key = high | step;
-      places(slots_from(next_key), &sh, &n_listed);
-      if (n_listed >= k) high = next_key;
-      if (step == 1u << 16) floor_ = max(floor_, high);
-    }
-    at = places(slots_from(floor_), &sh, &n_listed);
-  }
-  bool slow = n_listed > kListed;  // the same for all threads
-  uint32_t bound = floor_;
-  if (!slow) {
-    const float least = value_of(floor_);
-    for (int s = 0; s <= slots; ++s) {
-      const float x = sh.slot[s][tid].x;
-      if (reaches(x, least)) {
-        sh.key[at] = key_of(x);
-        sh.which[at++] = (uint16_t)(s * kThreads + tid);
-      }
-    }
-    const int padded = (n_listed + 3) & ~3;
-    if (tid < padded - n_listed) sh.key[n_listed + tid] = 0;
-    if (tid < 2) sh.threshold[tid] = floor_;
+    // A threshold to begin with: the least of the warps' m-th lanes' largest entries, above
+    // -inf; then the slots that reach it.
+    float mine = -INF_F;
+    for (int s = 0; s <= slots; ++s) mine = max_nan(mine, sh.slot[s][tid].x);
+    const uint32_t sorted = sort_lanes(key_of(mine), lane);
+    if (lane == m - 1) sh.least[warp] = sorted;
     __syncthreads();
-    const int share = (k + n - 1) / n;
-    for (int i = tid; i < n_listed; i += kThreads) {
-      const uint32_t own = sh.key[i];
-      int above = 0, same = 0;
-#pragma unroll 4
-      for (int j = 0; j < padded; j += 4) {
-        const uint4 x = *reinterpret_cast<const uint4*>(&sh.key[j]);
-        above += (x.x > own) + (x.y > own) + (x.z > own) + (x.w > own);
-        same += (x.x == own) + (x.y == own) + (x.z == own) + (x.w == own);
+    uint32_t floor_ = sh.least[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) floor_ = min(floor_, sh.least[w]);
+    floor_ = max(floor_, key_of(kLowest));
+    // x reaches key `least` (a NaN reaches every key, and only a NaN a NaN's)
+    auto reaches = [](float x, float least) { return least == least ? !(x < least) : x != x; };
+    auto slots_from = [&](uint32_t least) {
+      const float v = value_of(least);
+      int some = 0;
+      for (int s = 0; s <= slots; ++s) some += reaches(sh.slot[s][tid].x, v);
+      return some;
+    };
+    int n_listed;
+    int at = places(slots_from(floor_), &sh, &n_listed);
+    if (n_listed > kListed) {
+      // bit by bit up to the k-th largest (its upper 16 bits)
+      uint32_t step = 1u << 31;
+      for (uint32_t high = 0; step >= 1u << 16; step >>= 1) {
+        const uint32_t next_key = high | step;
+        places(slots_from(next_key), &sh, &n_listed);
+        if (n_listed >= k) high = next_key;
+        if (step == 1u << 16) floor_ = max(floor_, high);
       }
-      if (above < k && k <= above + same) sh.threshold[0] = own;  // alike where several write
-      if (above < share && share <= above + same) sh.threshold[1] = own;
+      at = places(slots_from(floor_), &sh, &n_listed);
     }
-    __syncthreads();
-    bound = sh.threshold[1];
-  }
-  if (n > 1) {  // entries of the whole row, a share of k from each CTA, that reach the least of the bounds
-    cluster_sync();  // every CTA's places are there
-    if (tid < n) st_dsmem_u32(mapa(smem_u32(&sh.bound[rank]), tid), bound);
-    cluster_sync();
-    for (int i = 0; i < n; ++i) bound = min(bound, sh.bound[i]);
-  } else {
-    bound = 0;
-  }
-  const uint32_t threshold = slow ? 0 : max(bound, sh.threshold[0]);
-  if (!slow) {
-    // The entries that reach it, of the slots that do; a slot's other entries into the sum.
-    // A thread a slot; f(vectors, what reaches of them, the place of an element of them).
-    const float least = value_of(threshold);
-    const uint4* const mid = reinterpret_cast<const uint4*>(c.row + c.head);
-    auto each = [&](int id, auto f) {
-      const int s = id / kThreads, thread = id % kThreads;
-      uint4 x[kVec];
-      if (s == slots) {
-        const int e = edge_of(c, a.V, thread);
-#pragma unroll
-        for (int u = 0; u < kVec; ++u) x[u] = low_vector<E>();
-        const float v = e >= 0 ? Elem<E>::get(c.row[e]) : -INF_F;
-        x[0].x = sizeof(E) == 2 ? 0xff800000u | __float_as_uint(v) >> 16 : __float_as_uint(v);
-        f(x, reaches(v, least) ? 1u : 0u, [&](int) { return e; });
-        return;
-      }
-      for (int chunk = s * group; chunk < min(chunks, (s + 1) * group); ++chunk) {
-        const int i = c.v0 + chunk * kVec * kThreads + thread;
-        uint32_t which = 0;
-#pragma unroll
-        for (int u = 0; u < kVec; ++u) x[u] = i + u * kThreads < c.v1 ? mid[i + u * kThreads] : low_vector<E>();
-        if (least == least) {
-#pragma unroll
-          for (int u = 0; u < kVec; ++u) which |= reaching(x[u], least, E{}) << (u * kN);
-        } else {  // NaNs alone: what is not below +inf, but +inf itself
-#pragma unroll
-          for (int u = 0; u < kVec; ++u)
-#pragma unroll
-            for (int j = 0; j < kN; ++j) {
-              const float v = Elem<E>::get(Elem<E>::entry(x[u], j));
-              which |= (v != v ? 1u : 0u) << (u * kN + j);
-            }
-        }
-        f(x, which, [&](int b) { return c.head + (i + b / kN * kThreads) * kN + b % kN; });
-      }
-    };
-    auto hide = [&](uint4 (&x)[kVec], uint32_t which) {
-#pragma unroll
-      for (int u = 0; u < kVec; ++u) x[u] = without(x[u], which >> (u * kN) & ((1u << kN) - 1), E{});
-    };
-    int some = 0;
-    float top = -INF_F;  // of those below it
-    for (int i = tid; i < n_listed; i += kThreads)
-      if (sh.key[i] >= threshold)
-        each(sh.which[i], [&](uint4 (&x)[kVec], uint32_t which, auto) {
-          some += __popc(which);
-          hide(x, which);
-          top = fmaxf(top, Elem<E>::top(x));
-        });
-    at = places(some, &sh, &total);
-    slow = total > kBest;
+    bool slow = n_listed > kListed;  // the same for all threads
+    uint32_t bound = floor_;
     if (!slow) {
-      const float base = base_of(top);
-      float rest = 0.f;
-      for (int i = tid; i < n_listed; i += kThreads)
-        if (sh.key[i] >= threshold)
-          each(sh.which[i], [&](uint4 (&x)[kVec], uint32_t which, auto place) {
-            for (uint32_t w = which; w != 0; w &= w - 1) {
-              const int idx = place(__ffs(w) - 1);
-              sh.best[at++] = composite(Entry{key_of(Elem<E>::get(c.row[idx])), idx});
-            }
-            hide(x, which);
-            if (terms.inv > 0.f) rest += power_sum<E>(terms, x, base);
-          });
-      if (terms.inv > 0.f) {
-        for (int s = 0; s <= slots; ++s) {
-          const float x = sh.slot[s][tid].x;
-          top = fmaxf(top, reaches(x, least) ? -INF_F : x);
+      const float least = value_of(floor_);
+      for (int s = 0; s <= slots; ++s) {
+        const float x = sh.slot[s][tid].x;
+        if (reaches(x, least)) {
+          sh.key[at] = key_of(x);
+          sh.which[at++] = (uint16_t)(s * kThreads + tid);
         }
-        t = Sum{top, rest == 0.f ? 0.f : rest * terms.power(base, base_of(top))};
-        for (int s = 0; s <= slots; ++s) {
-          const float2 w = sh.slot[s][tid];
-          if (w.x != -INF_F && !reaches(w.x, least)) t.s += w.y * terms.power(base_of(w.x), base_of(top));
+      }
+      const int padded = (n_listed + 3) & ~3;
+      if (tid < padded - n_listed) sh.key[n_listed + tid] = 0;
+      if (tid < 2) sh.threshold[tid] = floor_;
+      __syncthreads();
+      const int share = (k + n - 1) / n;
+      for (int i = tid; i < n_listed; i += kThreads) {
+        const uint32_t own = sh.key[i];
+        int above = 0, same = 0;
+#pragma unroll 4
+        for (int j = 0; j < padded; j += 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(&sh.key[j]);
+          above += (x.x > own) + (x.y > own) + (x.z > own) + (x.w > own);
+          same += (x.x == own) + (x.y == own) + (x.z == own) + (x.w == own);
         }
+        if (above < k && k <= above + same) sh.threshold[0] = own;  // alike where several write
+        if (above < share && share <= above + same) sh.threshold[1] = own;
       }
       __syncthreads();
-      if (n > 1 && total > LORA_TOPK_MAX) {
-        cut_best<E>(&sh, total, k, terms, &t);
-        total = k;
-      }
+      bound = sh.threshold[1];
     }
-  }
-  if (slow) total = select_share<E>(c, a.V, k, &sh, terms, &t);
-  // A CTA's entries are in best.  The first CTA takes the others'.
-  auto cta_sum = [&] {
-    const Sum w = terms.across(t);
-    if (lane == 0) sh.part[warp] = w;
-    __syncthreads();
-    return terms.across(lane < kWarps ? sh.part[lane] : Sum{-INF_F, 0.f});
-  };
-  if (n > 1) {
-    if (terms.inv > 0.f && rank > 0) {
-      const Sum all = cta_sum();
-      if (tid == 0) sh.sum = all;
+    if (n > 1) {  // entries of the whole row, a share of k from each CTA, that reach the least of the bounds
+      cluster_sync();  // every CTA's places are there
+      if (tid < n) st_dsmem_u32(mapa(smem_u32(&sh.bound[rank]), tid), bound);
+      cluster_sync();
+      for (int i = 0; i < n; ++i) bound = min(bound, sh.bound[i]);
+    } else {
+      bound = 0;
     }
-    if (tid == 0) sh.total = total;
-    cluster_sync();
-    if (rank == 0) {
-      int more = 0;  // of CTA `lane`, then of it and the ones before
-      if (lane > 0 && lane < n)
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(more) : "r"(mapa(smem_u32(&sh.total), lane)) : "memory");
-      const int own = more;
+    const uint32_t threshold = slow ? 0 : max(bound, sh.threshold[0]);
+    if (!slow) {
+      // The entries that reach it, of the slots that do; a slot's other entries into the sum.
+      // A thread a slot; f(vectors, what reaches of them, the place of an element of them).
+      const float least = value_of(threshold);
+      const uint4* const mid = reinterpret_cast<const uint4*>(c.row + c.head);
+      auto each = [&](int id, auto f) {
+        const int s = id / kThreads, thread = id % kThreads;
+        uint4 x[kVec];
+        if (s == slots) {
+          const int e = edge_of(c, a.V, thread);
 #pragma unroll
-      for (int d = 1; d < kMaxCluster; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, more, d);
-        if (lane >= d) more += o;
-      }
-      if (warp > 0 && warp < n) {  // a warp a CTA
-        const int len = __shfl_sync(0xffffffffu, own, warp), to = total + __shfl_sync(0xffffffffu, more, warp) - len;
-        const uint32_t src = mapa(smem_u32(sh.best), warp);
-        for (int i = lane; i < len; i += 32) {
-          unsigned long long x;
-          asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(src + 8 * i) : "memory");
-          sh.best[to + i] = x;
+          for (int u = 0; u < kVec; ++u) x[u] = low_vector<E>();
+          const float v = e >= 0 ? Elem<E>::get(c.row[e]) : -INF_F;
+          x[0].x = sizeof(E) == 2 ? 0xff800000u | __float_as_uint(v) >> 16 : __float_as_uint(v);
+          f(x, reaches(v, least) ? 1u : 0u, [&](int) { return e; });
+          return;
+        }
+        for (int chunk = s * group; chunk < min(chunks, (s + 1) * group); ++chunk) {
+          const int i = c.v0 + chunk * kVec * kThreads + thread;
+          uint32_t which = 0;
+#pragma unroll
+          for (int u = 0; u < kVec; ++u) x[u] = i + u * kThreads < c.v1 ? mid[i + u * kThreads] : low_vector<E>();
+          if (least == least) {
+#pragma unroll
+            for (int u = 0; u < kVec; ++u) which |= reaching(x[u], least, E{}) << (u * kN);
+          } else {  // NaNs alone: what is not below +inf, but +inf itself
+#pragma unroll
+            for (int u = 0; u < kVec; ++u)
+#pragma unroll
+              for (int j = 0; j < kN; ++j) {
+                const float v = Elem<E>::get(Elem<E>::entry(x[u], j));
+                which |= (v != v ? 1u : 0u) << (u * kN + j);
+              }
+          }
+          f(x, which, [&](int b) { return c.head + (i + b / kN * kThreads) * kN + b % kN; });
+        }
+      };
+      auto hide = [&](uint4 (&x)[kVec], uint32_t which) {
+#pragma unroll
+        for (int u = 0; u < kVec; ++u) x[u] = without(x[u], which >> (u * kN) & ((1u << kN) - 1), E{});
+      };
+      int some = 0;
+      float top = -INF_F;  // of those below it
+      for (int i = tid; i < n_listed; i += kThreads)
+        if (sh.key[i] >= threshold)
+          each(sh.which[i], [&](uint4 (&x)[kVec], uint32_t which, auto) {
+            some += __popc(which);
+            hide(x, which);
+            top = fmaxf(top, Elem<E>::top(x));
+          });
+      at = places(some, &sh, &total);
+      slow = total > kBest;
+      if (!slow) {
+        const float base = base_of(top);
+        float rest = 0.f;
+        for (int i = tid; i < n_listed; i += kThreads)
+          if (sh.key[i] >= threshold)
+            each(sh.which[i], [&](uint4 (&x)[kVec], uint32_t which, auto place) {
+              for (uint32_t w = which; w != 0; w &= w - 1) {
+                const int idx = place(__ffs(w) - 1);
+                sh.best[at++] = composite(Entry{key_of(Elem<E>::get(c.row[idx])), idx});
+              }
+              hide(x, which);
+              if (terms.inv > 0.f) rest += power_sum<E>(terms, x, base);
+            });
+        if (terms.inv > 0.f) {
+          for (int s = 0; s <= slots; ++s) {
+            const float x = sh.slot[s][tid].x;
+            top = fmaxf(top, reaches(x, least) ? -INF_F : x);
+          }
+          t = Sum{top, rest == 0.f ? 0.f : rest * terms.power(base, base_of(top))};
+          for (int s = 0; s <= slots; ++s) {
+            const float2 w = sh.slot[s][tid];
+            if (w.x != -INF_F && !reaches(w.x, least)) t.s += w.y * terms.power(base_of(w.x), base_of(top));
+          }
+        }
+        __syncthreads();
+        if (n > 1 && total > LORA_TOPK_MAX) {
+          cut_best<E>(&sh, total, k, terms, &t);
+          total = k;
         }
       }
-      total += __shfl_sync(0xffffffffu, more, kMaxCluster - 1);
     }
-  }
-  Sum others[kMaxCluster];
-  if (n > 1) {
-    if (rank == 0 && tid == 0 && terms.inv > 0.f)
+    if (slow) total = select_share<E>(c, a.V, k, &sh, terms, &t);
+    // A CTA's entries are in best.  The first CTA takes the others'.
+    auto cta_sum = [&] {
+      const Sum w = terms.across(t);
+      if (lane == 0) sh.part[warp] = w;
+      __syncthreads();
+      return terms.across(lane < kWarps ? sh.part[lane] : Sum{-INF_F, 0.f});
+    };
+    if (n > 1) {
+      if (terms.inv > 0.f && rank > 0) {
+        const Sum all = cta_sum();
+        if (tid == 0) sh.sum = all;
+      }
+      if (tid == 0) sh.total = total;
+      cluster_sync();
+      if (rank == 0) {
+        int more = 0;  // of CTA `lane`, then of it and the ones before
+        if (lane > 0 && lane < n)
+          asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(more) : "r"(mapa(smem_u32(&sh.total), lane)) : "memory");
+        const int own = more;
 #pragma unroll
-      for (int q = 1; q < kMaxCluster; ++q)
-        if (q < n) {
-          const uint32_t src = mapa(smem_u32(&sh.sum), q);
-          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(others[q].m), "=f"(others[q].s) : "r"(src) : "memory");
+        for (int d = 1; d < kMaxCluster; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, more, d);
+          if (lane >= d) more += o;
         }
-    cluster_sync();  // nobody leaves before its entries are read
-    if (rank > 0) return;
-  }
-  if (total > 2 * kThreads) {
+        if (warp > 0 && warp < n) {  // a warp a CTA
+          const int len = __shfl_sync(0xffffffffu, own, warp), to = total + __shfl_sync(0xffffffffu, more, warp) - len;
+          const uint32_t src = mapa(smem_u32(sh.best), warp);
+          for (int i = lane; i < len; i += 32) {
+            unsigned long long x;
+            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(src + 8 * i) : "memory");
+            sh.best[to + i] = x;
+          }
+        }
+        total += __shfl_sync(0xffffffffu, more, kMaxCluster - 1);
+      }
+    }
+    Sum others[kMaxCluster];
+    if (n > 1) {
+      if (rank == 0 && tid == 0 && terms.inv > 0.f)
+#pragma unroll
+        for (int q = 1; q < kMaxCluster; ++q)
+          if (q < n) {
+            const uint32_t src = mapa(smem_u32(&sh.sum), q);
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(others[q].m), "=f"(others[q].s) : "r"(src) : "memory");
+          }
+      cluster_sync();  // nobody leaves before its entries are read
+      if (rank > 0) return;
+    }
+    if (total > 2 * kThreads) {
+      __syncthreads();
+      cut_best<E>(&sh, total, k, terms, &t);
+      total = k;
+    }
+    // an entry's place is the number of entries before it
+    if (tid < 2) sh.best[total + tid] = 0;
     __syncthreads();
-    cut_best<E>(&sh, total, k, terms, &t);
-    total = k;
-  }
-  // an entry's place is the number of entries before it
-  if (tid < 2) sh.best[total + tid] = 0;
-  __syncthreads();
-  const int parts = total <= kThreads / 4 ? 4 : total <= kThreads / 2 ? 2 : 1;  // threads that share an entry's counting
-  for (int i = tid / parts; i - tid / parts < total; i += kThreads / parts) {
-    const unsigned long long mine = i < total ? sh.best[i] : ~0ull;
-    int place = 0;
+    const int parts = total <= kThreads / 4 ? 4 : total <= kThreads / 2 ? 2 : 1;  // threads that share an entry's counting
+    for (int i = tid / parts; i - tid / parts < total; i += kThreads / parts) {
+      const unsigned long long mine = i < total ? sh.best[i] : ~0ull;
+      int place = 0;
 #pragma unroll 4
-    for (int j = 2 * (tid % parts); j < total; j += 2 * parts) {
-      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&sh.best[j]);
-      place += (two.x > mine) + (two.y > mine);
+      for (int j = 2 * (tid % parts); j < total; j += 2 * parts) {
+        const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&sh.best[j]);
+        place += (two.x > mine) + (two.y > mine);
+      }
+      for (int d = 1; d < parts; d <<= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
+      if (i >= total || tid % parts != 0) continue;
+      const Entry e = entry_of(mine);
+      if (place < k) {
+        a.ids[out + place] = e.idx;
+        a.values[out + place] = value_of(e.key);
+      } else if (terms.inv > 0.f) {
+        t = terms.add(t, value_of(e.key));
+      }
     }
-    for (int d = 1; d < parts; d <<= 1) place += __shfl_xor_sync(0xffffffffu, place, d);
-    if (i >= total || tid % parts != 0) continue;
-    const Entry e = entry_of(mine);
-    if (place < k) {
-      a.ids[out + place] = e.idx;
-      a.values[out + place] = value_of(e.key);
-    } else if (terms.inv > 0.f) {
-      t = terms.add(t, value_of(e.key));
+    if (tid >= total && tid < k) {
+      a.ids[out + tid] = -1;
+      a.values[out + tid] = -INF_F;
     }
-  }
-  if (tid >= total && tid < k) {
-    a.ids[out + tid] = -1;
-    a.values[out + tid] = -INF_F;
-  }
-  if (a.tail != nullptr) {
-  Sum all = cta_sum();
-  if (tid == 0) {
+    if (a.tail != nullptr) {
+      Sum all = cta_sum();
+      if (tid == 0) {
 #pragma unroll
-    for (int q = 1; q < kMaxCluster; ++q)
-      if (q < n) all = terms.join(all, others[q]);
-    a.tail[row] = all.s == 0.f ? -INF_F : base_of(all.m) * a.terms.inv + logf(all.s);
-  }
-  }
-  if (next_row >= a.T) return;
-  row = next_row;
-  __syncthreads();  // the row's places in shared memory are free
+        for (int q = 1; q < kMaxCluster; ++q)
+          if (q < n) all = terms.join(all, others[q]);
+        a.tail[row] = all.s == 0.f ? -INF_F : base_of(all.m) * a.terms.inv + logf(all.s);
+      }
+    }
+    if (next_row >= a.T) return;
+    row = next_row;
+    __syncthreads();  // the row's places in shared memory are free
   }
 }
 

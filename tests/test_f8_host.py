@@ -135,6 +135,14 @@ def test_product_refuses_bad_arguments(back):
         assert product(x, w, y=m.scales, back=back) == bad
 
 
+def test_more_rows_or_columns_than_tiles_can_count_are_refused():
+    many = 0x7fff0001
+    assert quantize(f8(rows=many, ld=16, cols=16), ldx=16) == B.LORA_ERR_UNSUPPORTED
+    assert quantize(f8(rows=4, cols=many), ldx=many) == B.LORA_ERR_UNSUPPORTED
+    assert product(f8(rows=many, cols=16, ld=16), f8(300, 16, 128, 1)) == B.LORA_ERR_UNSUPPORTED
+    assert product(f8(cols=16), f8(many, 16, 128, 1)) == B.LORA_ERR_UNSUPPORTED
+
+
 def test_no_rows_is_nothing_to_do():
     assert quantize(f8(rows=0, codes=None, scales=None), x=None) == B.LORA_OK
     assert product(f8(rows=0, codes=None, scales=None), f8(300, 256, 128, 1), y=None) == B.LORA_OK

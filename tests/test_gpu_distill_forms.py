@@ -1,0 +1,76 @@
+"""The distillation loss and the top logits over many rows: each form of the kernels at its borders (rows by a CTA of
+128 to 1024 threads, rows held by clusters), with rows in turn on a CTA and rows that do not count between them."""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import cuda_or_skip
+from segmented_gather_gemm_lora_gb300 import binding as B
+from test_gpu_distill import BF16, F32, batch, check_loss, check_topk, f32, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,V,k", [(700, 2000, 96), (700, 2001, 97), (640, 4099, 60), (400, 16500, 224), (400, 16500, 225),
+                                   (330, 33001, 224), (330, 33000, 256), (320, 70003, 40), (200, 180000, 256)])
+def test_rows_in_turn(T, V, k, dtype):
+    cuda_or_skip()
+    rng = np.random.default_rng(T + V + k)
+    x, ids, values, rest, labels = batch(rng, T, V, k)
+    labels = np.where(rng.random(T) < 0.25, -1, labels)
+    weight = np.where(rng.random(T) < 0.1, 0.0, rng.uniform(0.1, 2, T)).astype(np.float32)
+    check_loss(x, ids, values, rest, labels, weight, dtype, inplace=True, temperature=2.0, kd_weight=4.0)
+    check_loss(x[:160], ids[:160], values[:160], rest[:160], labels[:160], dtype=dtype, kind="jsd", mix=0.4, ce_weight=0.5,
+               temperature=1.5)
+
+
+@pytest.mark.parametrize("kind", ["forward", "reverse"])
+@pytest.mark.parametrize("T,V", [(38, 60000), (76, 60000), (150, 60000), (152, 33000), (160, 65000)])
+def test_rows_of_clusters(T, V, kind):
+    cuda_or_skip()
+    rng = np.random.default_rng(T + V)
+    x, ids, values, rest, labels = batch(rng, T, V, 256 if T < 100 else 70)
+    labels[rng.random(T) < 0.25] = -1
+    for dtype in (BF16, F32):
+        check_loss(x, ids, values, rest, labels, None, dtype, inplace=True, kind=kind, ce_weight=0.25, temperature=2.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,V,k", [(1000, 5000, 64), (600, 20000, 256), (520, 40001, 20), (70, 30000, 100), (150, 9000, 256)])
+def test_topk_of_rows_in_turn(T, V, k, dtype):
+    cuda_or_skip()
+    rng = np.random.default_rng(T + V + k)
+    x = rng.normal(size=(T, V)) * 3
+    x[::7] = np.round(x[::7])        # ties
+    x[3::11, 100:] = -np.inf         # little to list
+    check_topk(x, k, dtype, temperature=1.5, labels=np.where(rng.random(T) < 0.2, -1, 0), pad=3)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap share nothing."""
+    cuda_or_skip()
+    rng = np.random.default_rng(5)
+    x, ids, values, rest, _ = batch(rng, 300, 20000, 50)
+    logits, args, tail = torch.from_numpy(x).cuda().to(BF16), (i32(ids), f32(values)), f32(rest)
+
+    def run(stream):
+        out = [torch.empty(300, 64, dtype=torch.int32, device="cuda"), torch.empty(300, 64, device="cuda")]
+        out += [torch.empty(300, device="cuda") for _ in range(3)] + [torch.empty_like(logits)]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            B.lora_topk_logits(logits, out[0], out[1], out[2], stream=stream)
+            B.lora_distill_loss(logits, *args, out[3], out[4], out[5], tail=tail, kind=B.LORA_DISTILL_JSD, stream=stream)
+        return out
+
+    want = run(None)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append(run(s))
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))

@@ -1,4 +1,4 @@
-"""Train several tenants' adapters at once on preference pairs or sampled answers.
+"""Train several tenants' adapters at once on preference pairs, on sampled answers or after a teacher.
 
 One frozen projection with a LoRA adapter per tenant and a frozen head stand for a model:
 
@@ -14,7 +14,16 @@ A step runs, on one stream and without reading anything back:
 
 The reference model's log-probabilities come from lora_token_logprobs with every row on adapter -1.
 
-    python examples/train_adapters.py [--loss policy] [--state e4m3] [--steps 30]
+With --loss distill the tenants learn from a teacher's top logits (lora_topk_logits, listed once) on a base in 8-bit
+floating point, of two frozen projections with the adapters on the first:
+
+    lora_base_f8, lora_apply           y = x W0^T, each tenant's term added
+    lora_f8_quantize, lora_base_f8     z = y W1^T,  logits = z H^T
+    lora_distill_loss                  the loss and dL/dlogits, in the logits' place
+    lora_f8_quantize, lora_base_f8_backward    dy = dz W1
+    lora_sgmv_backward ...             as above
+
+    python examples/train_adapters.py [--loss policy|distill] [--state e4m3] [--steps 30]
 """
 
 import argparse
@@ -31,6 +40,7 @@ from segmented_gather_gemm_lora_gb300 import workloads as W  # noqa: E402
 RANKS = (8, 16, 4, 32)  # one tenant each
 D, V = 512, 1000
 ROWS = 24               # rows of an answer
+TOP = 32                # a teacher's listed logits
 
 
 class Trainer:
@@ -59,6 +69,10 @@ class Trainer:
         self.w0, self.head = (rnd(D, D) / D ** 0.5).bfloat16(), (rnd(V, D) / D ** 0.5).bfloat16()
         self.seg, none = B.Segments(T), torch.full_like(self.ids, -1)
         self.hu = torch.empty(2 * T, B.LORA_MAX_RANK, device="cuda")
+        if loss == "distill":
+            B.lora_segments_build(self.ids, n, self.seg, err=self.err)
+            self.distill_from((rnd(D, D) / D ** 0.5).bfloat16(), (self.w0 + 0.3 * rnd(D, D) / D ** 0.5).bfloat16())
+            return
 
         # the reference model: no adapter on any row
         self.ref, self.logp = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
@@ -74,30 +88,57 @@ class Trainer:
             side = torch.tensor([1.0, -1.0], device="cuda").repeat(n).repeat_interleave(ROWS)
             self.advantage, self.weight = side.contiguous(), torch.full((T,), 1.0 / T, device="cuda")
 
+    def distill_from(self, w1, teacher):
+        """The teacher, the base with `teacher` in W0's place, says its part; the base itself goes into 8 bits."""
+        T = self.x.shape[0]
+        self.top, self.top_values = torch.empty(T, TOP, dtype=torch.int32, device="cuda"), torch.empty(T, TOP, device="cuda")
+        self.tail, self.loss = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        B.lora_topk_logits(self.x @ teacher.t() @ w1.t() @ self.head.t(), self.top, self.top_values, self.tail,
+                           temperature=2.0, labels=self.labels, err=self.err)
+        self.q0, self.q1 = B.F8Matrix.empty(D, D, block_rows=128), B.F8Matrix.empty(D, D, block_rows=128)
+        self.qx, self.qy = B.F8Matrix.empty(T, D), B.F8Matrix.empty(T, D)
+        self.qdz = B.F8Matrix.empty(T, D, type=B.LORA_F8_E5M2)
+        for x, q in ((self.w0, self.q0), (w1, self.q1), (self.x, self.qx)):
+            B.lora_f8_quantize(x, q, err=self.err)
+        self.z, self.dy = torch.empty_like(self.x), torch.empty_like(self.x)
+
     def logits(self, ids):
+        if self.kind == "distill":
+            B.lora_base_f8(self.qx, self.q0, self.y, err=self.err)
+            B.lora_apply(self.x, self.y, self.seg, self.view, err=self.err)
+            B.lora_f8_quantize(self.y, self.qy, err=self.err)
+            B.lora_base_f8(self.qy, self.q1, self.z, err=self.err)
+            return self.z @ self.head.t()
         B.lora_base_apply(self.x, self.w0, self.y, ids, self.seg, self.view, err=self.err)
         return self.y @ self.head.t()
 
     def step(self):
         """One step of every tenant; the mean loss, still on the device."""
         logits = self.logits(self.ids)
-        if self.kind == "preference":
+        if self.kind == "distill":
+            B.lora_distill_loss(logits, self.top, self.top_values, self.loss, None, logits, tail=self.tail, labels=self.labels,
+                                temperature=2.0, kd_weight=4.0, grad_scale=1.0 / self.loss.numel(), err=self.err)
+        elif self.kind == "preference":
             B.lora_preference_loss(logits, self.labels, self.indptr, self.loss, self.seq_logp, logits, self.pref_space,
                                    ref_logp=self.ref, beta=0.1, grad_scale=1.0 / self.loss.numel(), err=self.err)
         else:
             B.lora_policy_loss(logits, self.labels, self.ref, self.advantage, self.logp, self.loss, self.kl, logits,
                                ref_logp=self.ref, weight=self.weight, kl_coef=0.02, err=self.err)
         dy = logits @ self.head  # the logits hold their gradient now
+        if self.kind == "distill":
+            B.lora_f8_quantize(dy, self.qdz, err=self.err)
+            B.lora_base_f8_backward(self.qdz, self.q1, self.dy, err=self.err)
+            dy = self.dy
         B.lora_sgmv_backward(self.x, dy, None, self.grad, self.hu, self.seg, self.view, err=self.err)
         self.hyper.view(torch.int32)[:, 0].add_(1)
         B.lora_grad_sumsq(self.train, self.tenants, self.sumsq, self.space, err=self.err)
         B.lora_adamw_step(self.train, self.tenants, self.hyper, sumsq=self.sumsq, zero_grad=True, err=self.err)
-        return self.loss.mean() if self.kind == "preference" else self.loss.sum()
+        return self.loss.sum() if self.kind == "policy" else self.loss.mean()
 
 
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
-    ap.add_argument("--loss", choices=("preference", "policy"), default="preference")
+    ap.add_argument("--loss", choices=("preference", "policy", "distill"), default="preference")
     ap.add_argument("--state", choices=("f32", "e4m3"), default="f32")
     ap.add_argument("--steps", type=int, default=30)
     a = ap.parse_args()

@@ -38,7 +38,8 @@ extern "C" {
 #define LORA_F8_FROM_F32 1
 #define LORA_F8_BLOCK 128
 
-/** An 8-bit matrix.  Groups at the right and lower edges may be short. */
+/** An 8-bit matrix.  Groups at the right and lower edges may be short.  More than
+ *  0x7fff0000 rows or columns are LORA_ERR_UNSUPPORTED. */
 typedef struct {
   void* codes;        /* device, one byte an element, 16-byte aligned; rows of ld bytes */
   int64_t ld;         /* >= cols, a multiple of 16 */
@@ -72,8 +73,8 @@ lora_status_t lora_f8_quantize(const void* x, int64_t ldx, int32_t dtype, const 
  * of LORA_F8_FROM_*; rounded once).  x: [T, d_in] with groups of one row; w:
  * [d_out, d_in] with blocks of 128 rows; either type of code each.  y: device,
  * rows of ldy >= d_out elements, aligned to the element.  The products of 128
- * consecutive k are summed in the tensor cores' fp32 and times both scales added
- * to an fp32 sum, in ascending order of k (in up to eight spans of k, added in
+ * consecutive k are summed in the tensor cores' fp32 and, times the fp32 product of
+ * both scales, added to an fp32 sum, in ascending order of k (in up to eight spans of k, added in
  * order, where a call has few tiles).  T = 0: nothing to do.  A wait inside the
  * kernel that ran out sets LORA_DERR_TIMEOUT; the tiles it concerned are not written.
  */

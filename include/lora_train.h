@@ -141,7 +141,7 @@ lora_status_t lora_policy_loss(const void* logits, int64_t ld, int32_t dtype, co
 /**
  * The k largest entries of each row: ids[t, j] (device int32 [T, k]) and
  * values[t, j] (device fp32 [T, k], the logits themselves), in falling order,
- * equal values by rising index (-0 equals +0, a NaN comes before +inf); and
+ * equal values by rising index (-0 equals +0 and is listed as that, a NaN comes before +inf); and
  *     tail[t] = log sum over the entries not listed of exp(logits[t, v] / temperature)
  * (device fp32 [T], may be NULL; -inf where nothing is left).  Entries of -inf are
  * not listed: their places hold id -1 and value -inf.  labels (may be NULL: every
@@ -188,7 +188,9 @@ typedef struct {
  * [T]) NULL stands for ones; weight 0: loss 0 and a zero gradient row.  An id >= V or
  * listed twice in a row sets LORA_DERR_BAD_LABEL and the row does not count.
  * Reverse needs tail.  loss: device fp32 [T]; kd, ce: fp32 [T] or NULL (ce is computed
- * only with ce_weight > 0, else 0); 1 <= k <= LORA_TOPK_MAX.
+ * only with ce_weight > 0, else 0); 1 <= k <= LORA_TOPK_MAX.  A row needs V / 8 bytes of
+ * a CTA's shared memory and a little more: V above 1.4 million (of bf16; 1.2 of fp32) is
+ * LORA_ERR_UNSUPPORTED.
  */
 lora_status_t lora_distill_loss(const void* logits, int64_t ld, int32_t dtype, const int32_t* ids, const float* values,
                                 const float* tail, int32_t k, const int32_t* labels, const float* weight, int32_t T,

@@ -74,3 +74,17 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+def test_the_longest_rows():
+    """Up to the documented length a row is right; above it the call is refused and nothing is written."""
+    cuda_or_skip()
+    for dtype, V in ((BF16, 1_400_000), (F32, 1_200_000)):
+        x, ids, values, rest, labels = batch(np.random.default_rng(6), 2, V, 40)
+        check_loss(x, ids, values, rest, labels, None, dtype, ce_weight=1.0)
+        logits = torch.zeros(1, 1_500_000, dtype=dtype, device="cuda")
+        loss, grad = torch.full((1,), 9.0, device="cuda"), torch.full_like(logits, 9.0)
+        with pytest.raises(B.LoraError):
+            B.lora_distill_loss(logits, i32(ids[:1]), f32(values[:1]), loss, None, grad)
+        torch.cuda.synchronize()
+        assert float(loss) == 9.0 and bool((grad == 9.0).all())

@@ -88,3 +88,47 @@ def test_the_longest_rows():
             B.lora_distill_loss(logits, i32(ids[:1]), f32(values[:1]), loss, None, grad)
         torch.cuda.synchronize()
         assert float(loss) == 9.0 and bool((grad == 9.0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,V,k", [(2000, 250, 20), (1100, 700, 8), (1000, 9000, 32), (1000, 9000, 33), (1000, 1000, 60),
+                                   (1000, 2500, 120), (500, 5000, 250), (20, 1000, 60), (300, 200, 100)])
+def test_topk_of_many_short_rows(T, V, k, dtype):
+    cuda_or_skip()
+    check_topk(np.random.default_rng(T + V + k).normal(size=(T, V)) * 3, k, dtype, temperature=0.7, first=3)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,V,k", [(1120, 3000, 30), (1120, 3000, 60), (560, 15000, 30), (980, 20000, 64), (504, 20000, 100),
+                                   (490, 33000, 128), (462, 20000, 256), (14, 128000, 64), (14, 128000, 256)])
+def test_topk_of_rows_that_are_hard_to_filter_in_each_form(T, V, k, dtype):
+    """Ties by the thousand, rising and falling rows, crowds in few places, all but a few hidden, NaNs, each between
+    ordinary rows."""
+    cuda_or_skip()
+    rng = np.random.default_rng(T + V + k)
+    few, crowd, nans = np.full(V, -np.inf), rng.normal(size=V), rng.normal(size=V)
+    few[rng.choice(V, 5, replace=False)] = rng.normal(size=5)
+    crowd[V // 2: V // 2 + 600] += 50
+    nans[::50] = np.nan
+    at = np.arange(V)
+    rows = [np.zeros(V), at / 64.0, -at / 64.0, rng.integers(0, 3, V) * 1.0, np.where(at % 2 == 0, 0.0, -0.0), few,
+            np.full(V, -np.inf), np.where(at < V // 2, -1e30, 1e30), np.where(at >= V - 3, 5.0, 1.0), crowd, nans,
+            rng.normal(size=V) * 1e-3 + 1e4, np.where(at % 32 == 0, 9.0, rng.normal(size=V)),
+            np.full(V, torch.finfo(torch.bfloat16).min)]
+    x = rng.normal(size=(T, V)) if T > 14 else np.zeros((T, V))
+    for i, r in enumerate(rows):
+        x[i * (T // 14)] = r
+    check_topk(x, k, dtype)
+
+
+@pytest.mark.parametrize("T,V,k", [(2000, 500, 20), (1000, 3000, 60), (600, 30000, 100), (500, 20000, 200), (16, 100000, 256)])
+def test_topk_in_each_form_does_not_depend_on_timing(T, V, k):
+    cuda_or_skip()
+    x = (torch.randn(T, V, device="cuda") * 3).to(BF16)
+    x[::5] = torch.round(x[::5])
+    want = None
+    for _ in range(6):
+        out = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda"), torch.empty(T, device="cuda")
+        B.lora_topk_logits(x, *out, temperature=1.5)
+        want = want or out
+        assert all(torch.equal(a, b) for a, b in zip(out, want))

@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kG + 32, kVec > 8 ? 2 : 3) held_kernel(const _
 // -------------------------------------------------------------- streamed form --
 //
 // Many rows, short rows and the longest: a CTA a row, which it reads for its
-// sum and again for its gradient.  Few rows are under way (one to eight an SM), so the
+// sum and again for its gradient.  Few rows are under way (one to sixteen an SM), so the
 // second read finds the row in L2; outputs are written past it.  A row costs its barriers
 // once, not once in each of a cluster's CTAs, and its CTA has no other to wait for.
 //
@@ -946,7 +946,9 @@ lora_status_t launch_stream(DistillArgs& a, cudaStream_t s) {
 //  - else streamed, with so many rows at once that L2 holds them.  8192 x 32000 bf16: 216 / 308 /
 //    463 (held 245); 4000 x 50257 with jsd 181 / 224 / 350 (270); 8192 x 128256 929 / 808 / 933
 //    (935); 2000 x 151936 fp32 584 / 545 / 509.
-//  - of short rows more at once: 8192 x 1000 with 128 threads 50, 256 90.
+//  - of short rows more at once, 64 / 128 / 256 threads: 8192 x 1000 32 / 50 / 87; 8192 x 5000 56 / 73 /
+//    99; 4096 x 10000 41 / 50 / 69; 4096 x 20000 74 / 72 / 88; 4096 x 32000 124 / 113 / 110. Few rows:
+//    600 x 5000 7.6 / 7.6 / 8.8, 300 x 10000 8.4 / 7.3 / 7.5.
 // The last warp has no entries: it works out the rest.
 template <typename E>
 lora_status_t launch(DistillArgs& a, cudaStream_t s) {
@@ -963,7 +965,8 @@ lora_status_t launch(DistillArgs& a, cudaStream_t s) {
         return vecs == 4 ? launch_held<E, kHeld, 4>(a, ctas(4), s) : launch_held<E, kHeld, 8>(a, ctas(8), s);
     return launch_held<E, kHeld, 16>(a, ctas(16), s);
   }
-  if (bytes <= 8192 && a.T > 4 * sms && a.k <= 128 - last) return launch_stream<E, 128>(a, s);
+  if (bytes <= 24000 && a.T > 2 * sms && a.k <= 64 - last) return launch_stream<E, 64>(a, s);
+  if (bytes <= 48000 && a.T > sms && a.k <= 128 - last) return launch_stream<E, 128>(a, s);
   if (a.k <= 256 - last && bytes * 4 * sms <= 64 << 20 && (a.T > sms || bytes <= 32768)) return launch_stream<E, 256>(a, s);
   if (bytes * 2 * sms <= 96 << 20) return launch_stream<E, 512>(a, s);
   return launch_stream<E, 1024>(a, s);

@@ -13,7 +13,8 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("T,V,k", [(700, 2000, 96), (700, 2001, 97), (640, 4099, 60), (400, 16500, 224), (400, 16500, 225),
+@pytest.mark.parametrize("T,V,k", [(700, 1000, 32), (700, 999, 33), (640, 10000, 20), (640, 20001, 50), (700, 2000, 96),
+                                   (700, 2001, 97), (640, 4099, 60), (400, 16500, 224), (400, 16500, 225),
                                    (330, 33001, 224), (330, 33000, 256), (320, 70003, 40), (200, 180000, 256)])
 def test_rows_in_turn(T, V, k, dtype):
     cuda_or_skip()

@@ -778,17 +778,20 @@ def lora_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch
                                   _rows(kl, T, f32, "kl"), dp, ldd, _addr(err), _handle(stream)), "lora_policy_loss")
 
 
-def _one_device(stream, first: torch.Tensor, *others: Optional[torch.Tensor]):
-    """Refuse tensors that do not share a CUDA device, or that of the current stream where none is given: the
-    library would read their addresses on the device the call runs on."""
+def _one_device(stream, first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
+    """The stream's handle.  Refuses tensors that do not share a CUDA device, or that of the current stream where none
+    is given: the library would read their addresses on the device the call runs on."""
     d = first.get_device()
     if d < 0:
         raise ValueError("expected tensors on a CUDA device")
-    if stream is None and d != torch.cuda.current_device():
-        raise ValueError("expected tensors on the current CUDA device (%d), or a stream of theirs" % torch.cuda.current_device())
     for t in others:
         if t is not None and t.get_device() != d:
             raise ValueError("expected tensors on one CUDA device")
+    if stream is not None:
+        return _handle(stream)
+    if d != torch._C._cuda_getDevice():
+        raise ValueError("expected tensors on the current CUDA device (%d), or a stream of theirs" % torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(d)
 
 
 def _err_word(err: Optional[torch.Tensor]) -> int:
@@ -805,7 +808,7 @@ def lora_topk_logits(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tens
     """The k largest logits of each row, largest first (ids int32 and values fp32 [T, k]; equal ones by rising
     index), and tail[t] = log of the sum of exp(logit / temperature) over the others.  labels int32 [T]: rows with a
     negative label list nothing.  See include/lora_train.h."""
-    _one_device(stream, logits, ids, values, tail, labels, err)
+    handle = _one_device(stream, logits, ids, values, tail, labels, err)
     p, ld, code, T, V = _logits(logits)
     if ids.dim() != 2 or ids.shape[0] != T:
         raise ValueError("ids: expected a row for each row of logits")
@@ -813,7 +816,7 @@ def lora_topk_logits(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tens
     i32, f32 = torch.int32, torch.float32
     _check(lib().lora_topk_logits(p, ld, code, _rows(labels, T, i32, "labels"), T, V, k, float(temperature),
                                   _rows(ids, T * k, i32, "ids"), _rows(values, T * k, f32, "values"),
-                                  _rows(tail, T, f32, "tail"), _err_word(err), _handle(stream)), "lora_topk_logits")
+                                  _rows(tail, T, f32, "tail"), _err_word(err), handle), "lora_topk_logits")
 
 
 def lora_distill_loss(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, loss: torch.Tensor,
@@ -825,7 +828,7 @@ def lora_distill_loss(logits: torch.Tensor, ids: torch.Tensor, values: torch.Ten
     """Divergence of a student's logits from a teacher's list (ids, values [T, k] and tail, as lora_topk_logits
     leaves them), with the labels' cross-entropy, per row, and its gradient (see include/lora_train.h).  dlogits may
     be the logits (the gradient takes their place) or None."""
-    _one_device(stream, logits, ids, values, loss, kd, dlogits, tail, labels, weight, ce, err)
+    handle = _one_device(stream, logits, ids, values, loss, kd, dlogits, tail, labels, weight, ce, err)
     p, ld, code, T, V = _logits(logits)
     if ids.dim() != 2 or ids.shape[0] != T:
         raise ValueError("ids: expected a row for each row of logits")
@@ -838,7 +841,7 @@ def lora_distill_loss(logits: torch.Tensor, ids: torch.Tensor, values: torch.Ten
                                    _rows(tail, T, f32, "tail"), k, _rows(labels, T, i32, "labels"),
                                    _rows(weight, T, f32, "weight"), T, V, opts, _rows(loss, T, f32, "loss"),
                                    _rows(kd, T, f32, "kd"), _rows(ce, T, f32, "ce"), dp, ldd, _err_word(err),
-                                   _handle(stream)), "lora_distill_loss")
+                                   handle), "lora_distill_loss")
 
 
 # --------------------------------------------------- training: optimizer step --
@@ -1004,21 +1007,21 @@ def _plain(t: torch.Tensor, rows: int, cols: int, what: str):
 
 def lora_f8_quantize(x: torch.Tensor, q: F8Matrix, pow2: bool = False, err: Optional[torch.Tensor] = None, stream=None):
     """Quantise x (bf16 or fp32, q's shape) into q; pow2: scales are powers of two (see include/lora_f8.h)."""
-    _one_device(stream, x, q.codes, q.scales, err)
+    handle = _one_device(stream, x, q.codes, q.scales, err)
     p, ld, code = _plain(x, q.c.rows, q.c.cols, "x")
-    _check(lib().lora_f8_quantize(p, ld, code, q.ref, LORA_F8_POW2 if pow2 else 0, _err_word(err), _handle(stream)),
+    _check(lib().lora_f8_quantize(p, ld, code, q.ref, LORA_F8_POW2 if pow2 else 0, _err_word(err), handle),
            "lora_f8_quantize")
 
 
 def lora_base_f8(x: F8Matrix, w: F8Matrix, y: torch.Tensor, err: Optional[torch.Tensor] = None, stream=None):
     """y = x W0^T, written only (bf16 or fp32): x [T, d_in] in groups of a row, w [d_out, d_in] in blocks of 128 rows."""
-    _one_device(stream, y, x.codes, x.scales, w.codes, w.scales, err)
+    handle = _one_device(stream, y, x.codes, x.scales, w.codes, w.scales, err)
     p, ld, code = _plain(y, x.c.rows, w.c.rows, "y")
-    _check(lib().lora_base_f8(x.ref, w.ref, p, ld, code, _err_word(err), _handle(stream)), "lora_base_f8")
+    _check(lib().lora_base_f8(x.ref, w.ref, p, ld, code, _err_word(err), handle), "lora_base_f8")
 
 
 def lora_base_f8_backward(dy: F8Matrix, w: F8Matrix, dx: torch.Tensor, err: Optional[torch.Tensor] = None, stream=None):
     """dx = dy W0, written only (bf16 or fp32): the gradient of lora_base_f8's input (the base is frozen)."""
-    _one_device(stream, dx, dy.codes, dy.scales, w.codes, w.scales, err)
+    handle = _one_device(stream, dx, dy.codes, dy.scales, w.codes, w.scales, err)
     p, ld, code = _plain(dx, dy.c.rows, w.c.cols, "dx")
-    _check(lib().lora_base_f8_backward(dy.ref, w.ref, p, ld, code, _err_word(err), _handle(stream)), "lora_base_f8_backward")
+    _check(lib().lora_base_f8_backward(dy.ref, w.ref, p, ld, code, _err_word(err), handle), "lora_base_f8_backward")

@@ -16,8 +16,8 @@
 // Keys are the values' bits made to order as integers; composite keys order as the
 // listing does, no two alike.
 //
-// What bounds it: of long rows memory and the exponentials (4096 x 128256 bf16, 64 listed: 243 us,
-// 4.3 TB/s; without tail less); of short ones what is done once a row, about ten barriers.
+// What bounds it: of long rows memory and the exponentials (4096 x 128256 bf16, 64 listed: 234 us,
+// 4.5 TB/s; without tail 211); of short ones what is done once a row, about ten barriers.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -38,7 +38,7 @@ template <int kT>
 constexpr int kListed = kT > 256 ? 2 * kT : 4 * kT;  // slots that are read again; entries that are placed at once
 template <int kT>
 constexpr int kAhead = kT > 256 ? 2 : 1;  // chunks under way: few rows wait for memory alone
-constexpr int kResident = 768;  // threads an SM
+constexpr int kResident = 896;  // threads an SM (4096 x 128256: 234 us; 640 258, 768 243, 1024, which spills, 310)
 constexpr float kLowest = -3.402823466e38f;  // below it only -inf, which is not listed
 
 struct TopkArgs {
@@ -544,7 +544,8 @@ lora_status_t launch(TopkArgs& a, cudaStream_t s) {
   return launch_pdl(f, dim3((unsigned)ctas), dim3(kT), sizeof(TopShared<kT>), s, 0, &a) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
 
-// The threads of a row (device times in us on a GB300, rows that fill the GPU unless said):
+// The threads of a row (device times in us on a GB300, rows that fill the GPU unless
+// said, 768 threads an SM):
 //  - the fewer, the more rows are under way and the less a row's fixed part costs: 8192 x 1000
 //    bf16 with 20 listed and 32 / 64 / 128 / 256 threads 28 / 44 / 63 / 145; 4096 x 20000 with 60
 //    listed - / 69 / 72 / 92;

@@ -9,15 +9,16 @@
 // the rest of them summed.  So the sum is of exactly the entries that are not listed, no
 // difference of large sums.  What is listed is put in order in runs of 32; an entry's place
 // is its place in its run and those that a search finds in the others.
-// A row in which too many entries tie or crowd in few slots takes the slow way: a radix
-// selection of the k best by passes over the row.
+// Where too many entries tie with the k-th largest (a mask's lowest value, say) those above it
+// are listed so, then the first of the ties.  A row in which too many crowd in few slots
+// takes the slow way: a radix selection of the k best by passes over the row.
 // Places and orders of sums are fixed: the same inputs give the same bits.
 //
 // Keys are the values' bits made to order as integers; composite keys order as the
 // listing does, no two alike.
 //
-// What bounds it: of long rows memory and the exponentials (4096 x 128256 bf16, 64 listed: 234 us,
-// 4.5 TB/s; without tail 211); of short ones what is done once a row, about ten barriers.
+// What bounds it: of long rows memory and the exponentials (4096 x 128256 bf16, 64 listed: 237 us,
+// 4.4 TB/s; without tail 211); of short ones what is done once a row, about ten barriers.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -354,16 +355,24 @@ __global__ void __launch_bounds__(kT, kT > kResident ? 1 : kResident / kT) topk_
         at = places<true>(slots_from(floor_), &sh, &n_listed);
       }
     }
+    // What is below these is one key to the row's values.
+    constexpr uint32_t kUnit = sizeof(E) == 2 ? 0x10000u : 1u;
+    auto above = [](uint32_t key) { return (key & ~(kUnit - 1)) + kUnit; };  // 0: nothing is
+    bool ties = false;  // too much ties with the k-th largest: what is above it is listed, and the first that tie
+    uint32_t kth = 0;
     if (n_listed > kListed<kT>) {
-      // bit by bit up to the k-th largest (its upper 16 bits)
-      uint32_t step = 1u << 31;
-      for (uint32_t high = 0; step >= 1u << 16; step >>= 1) {
-        const uint32_t next_key = high | step;
-        places<false>(slots_from(next_key), &sh, &n_listed);
-        if (n_listed >= k) high = next_key;
-        if (step == 1u << 16) floor_ = max(floor_, high);
+      // bit by bit up to the k-th largest
+      for (uint32_t step = 1u << 31; step >= kUnit; step >>= 1) {
+        places<false>(slots_from(kth | step), &sh, &n_listed);
+        if (n_listed >= k) kth |= step;
       }
+      floor_ = kth;
       at = places<false>(slots_from(floor_), &sh, &n_listed);
+      if (n_listed > kListed<kT> && above(kth) != 0) {
+        ties = true;
+        floor_ = above(kth);
+        at = places<false>(slots_from(floor_), &sh, &n_listed);
+      }
     }
     bool slow = n_listed > kListed<kT>;  // the same for all threads
     uint32_t threshold = floor_;
@@ -459,13 +468,22 @@ __global__ void __launch_bounds__(kT, kT > kResident ? 1 : kResident / kT) topk_
       }
       __syncthreads();
       // (a threshold of nothing but the least value: fewer slots than it takes, so all their entries reach it)
-      if (floor_ <= key_of(kLowest)) rank_slots();
+      if (!ties && floor_ <= key_of(kLowest)) rank_slots();
       total = collect(threshold);
-      if (total > kListed<kT>) {
+      if (total > kListed<kT> && !ties) {
         __syncthreads();
         if (tid == 0) sh.total = 0;
         rank_slots();
         total = collect(threshold);
+        if (total > kListed<kT> && above(threshold) != 0) {
+          __syncthreads();
+          if (tid == 0) sh.total = 0;
+          __syncthreads();
+          ties = true;
+          kth = threshold;
+          threshold = above(kth);
+          total = collect(threshold);
+        }
       }
       slow = total > kListed<kT>;
       if (!slow) {
@@ -483,6 +501,34 @@ __global__ void __launch_bounds__(kT, kT > kResident ? 1 : kResident / kT) topk_
           }
         }
       }
+    }
+    // The first entries of the tied value, in the row's order, fill the list.  Their slots' sums
+    // have them, so they are taken out of the row's: at least twice as many stay.
+    int taken = 0;
+    const float tied = sizeof(E) == 4 || (kth & 0x80000000u) ? value_of(kth & ~(kUnit - 1)) : value_of(kth | 0xffffu);
+    if (!slow && ties && total < k) {
+      taken = k - total;
+      int found = 0;
+      auto take = [&](uint32_t which, int from) {  // elements of this thread, in the order of threads
+        int some;
+        int to = found + places<false>(__popc(which), &sh, &some);
+        for (; which != 0 && to < taken; which &= which - 1, ++to)
+          sh.best[total + to] = composite(Entry{key_of(tied), from + __ffs(which) - 1});
+        found += some;
+      };
+      if (c.head > 0) take(tid < c.head && Elem<E>::get(c.row[tid]) == tied, tid);
+      for (int i0 = 0; i0 < c.nvec && found < taken; i0 += kT) {
+        uint32_t which = 0;
+        if (i0 + tid < c.nvec) {
+          const uint4 x = mid[i0 + tid];
+#pragma unroll
+          for (int j = 0; j < kN; ++j) which |= (Elem<E>::get(Elem<E>::entry(x, j)) == tied ? 1u : 0u) << j;
+        }
+        take(which, c.head + (i0 + tid) * kN);
+      }
+      if (found < taken) take(tid < a.V - c.tail0 && Elem<E>::get(c.row[c.tail0 + tid]) == tied, c.tail0 + tid);
+      total = k;
+      __syncthreads();
     }
     if (slow) t = Sum{-INF_F, 0.f};
     if (slow) total = select_row<E, kT>(c, a.V, k, &sh, terms, &t);
@@ -527,7 +573,8 @@ __global__ void __launch_bounds__(kT, kT > kResident ? 1 : kResident / kT) topk_
       const Sum w = terms.across(t);
       if (lane == 0) sh.part[warp] = w;
       __syncthreads();
-      const Sum all = terms.across(lane < kT / 32 ? sh.part[lane] : Sum{-INF_F, 0.f});
+      Sum all = terms.across(lane < kT / 32 ? sh.part[lane] : Sum{-INF_F, 0.f});
+      if (taken > 0 && all.m < INF_F) all.s -= (float)taken * terms.power(tied, base_of(all.m));
       if (tid == 0) a.tail[row] = all.s == 0.f ? -INF_F : base_of(all.m) * a.terms.inv + logf(all.s);
     }
     if (next_row >= a.T) return;

@@ -133,3 +133,26 @@ def test_topk_in_each_form_does_not_depend_on_timing(T, V, k):
         B.lora_topk_logits(x, *out, temperature=1.5)
         want = want or out
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,V,k", [(14, 40003, 64), (14, 130001, 256), (1400, 2005, 32), (700, 20003, 60), (700, 20003, 128)])
+def test_topk_of_rows_whose_ties_fill_the_list(T, V, k, dtype):
+    """The k-th largest is one of thousands that tie: some above it or none, few or many below, odd fractions, both
+    infinities, at any alignment; the first by index are listed and the tail has the others."""
+    cuda_or_skip()
+    rng = np.random.default_rng(T + V + k)
+    tie = lambda v, other: np.where(rng.random(V) < 0.7, v, other)  # noqa: E731
+    rows = [tie(0.1, rng.normal(size=V) - 9), tie(-0.3, -np.inf), tie(1e-40, -1.0), tie(np.inf, 0.0), tie(-1e30, -2e30),
+            tie(3.3, 3.2), np.full(V, -7.7), np.full(V, torch.finfo(torch.bfloat16).min)]
+    for n in (1, 5, k - 1, k, k + 3):
+        r = np.full(V, -1e30)
+        r[rng.choice(V, n, replace=False)] = rng.normal(size=n)
+        rows.append(r)
+    r = tie(0.1, -5.0)
+    r[V - 1], r[0], r[1] = 2.0, 1.0, 0.1
+    rows.append(r)
+    x = np.zeros((T, V))
+    for i in range(T):
+        x[i] = rows[i % len(rows)]
+    check_topk(x, k, dtype, pad=3, first=1)

@@ -156,3 +156,20 @@ def test_topk_of_rows_whose_ties_fill_the_list(T, V, k, dtype):
     for i in range(T):
         x[i] = rows[i % len(rows)]
     check_topk(x, k, dtype, pad=3, first=1)
+
+
+@pytest.mark.parametrize("T,V", [(3, 10), (3, 70000), (700, 300)])
+def test_lists_longer_than_the_row_and_absent_entries(T, V):
+    """An absent entry's id says nothing: not twice listed, not out of range."""
+    cuda_or_skip()
+    rng = np.random.default_rng(T + V)
+    x, ids, values, rest, labels = batch(rng, T, V, 6, absent=0.0)
+    k = 50
+    more_ids, more = np.full((T, k), -1), np.full((T, k), -np.inf, dtype=np.float32)
+    at = rng.choice(k, 6, replace=False)
+    more_ids[:, at], more[:, at] = ids, values
+    free = [j for j in range(k) if j not in at]
+    more_ids[:, free[0]], more_ids[:, free[1]], more_ids[:, free[2]] = ids[:, 0], V + 5, 2 ** 31 - 1  # value -inf
+    more_ids[:, free[3]], more[:, free[3]] = -7, 3.0                                              # a negative id
+    for kind in ("forward", "reverse", "jsd"):
+        check_loss(x, more_ids, more, rest, labels, kind=kind, ce_weight=0.3)

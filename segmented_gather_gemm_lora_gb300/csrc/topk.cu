@@ -230,6 +230,7 @@ __device__ __noinline__ int select_row(const Cut<E>& c, int V, int k, TopShared<
     else if (e.key != 0 && terms.inv > 0.f) *t = terms.add(*t, value_of(e.key));
     at += some;
   }
+  __syncthreads();  // the last round's entries (the edges, one warp's) are there for the warps that sort them
   return n;
 }
 

@@ -525,7 +525,8 @@ __global__ void __launch_bounds__(kG + 32, kVec > 8 ? 2 : 3) held_kernel(const _
       }
       bad = __any_sync(0xffffffffu, bad);
       // The loads of the row's logits are over before any CTA can write a gradient in their
-      // place, which takes this CTA's sums: they are in shared memory, the label's too.
+      // place, which takes this CTA's sums, sent after the barriers below: they are in shared
+      // memory, the label's too (read back from there, so that its load ends here).
       if (lane == 0) {
         sh.bad[turn] = bad;
         sh.label_logit = xl;
@@ -535,6 +536,7 @@ __global__ void __launch_bounds__(kG + 32, kVec > 8 ? 2 : 3) held_kernel(const _
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       meet<1, kAll>();
       meet<2, kAll>();
+      xl = sh.label_logit;
       for (int i = 0, j = lane; i < rounds; ++i, j += 32)
         if (mine(ids[j])) bits[(ids[j] - first) >> 5] = 0;
       load_logits(nt);

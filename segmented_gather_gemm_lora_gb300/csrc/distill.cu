@@ -816,9 +816,11 @@ __global__ void __launch_bounds__(kT, 1024 / kT) stream_kernel(const __grid_cons
       const bool has = lane * 32 < a.k;
       const float4 q = has ? sh.lists[lane] : make_float4(-INF_F, 0.f, -INF_F, 0.f);
       const float high = base_of(fmaxf(warp_max(q.x), in.tail * a.opt.temperature)), mx = base_of(warp_max(q.z));
-      const float mass = warp_add(q.y * expf((base_of(q.x) - high) * terms.inv)) + expf(in.tail - high * terms.inv);
-      list = make_float4(high, logf(mass), mx, warp_add(q.w * expf((base_of(q.z) - mx) * terms.inv)));
-      list_plain = kBoth ? warp_add(has ? sh.lists_plain[lane] * expf(base_of(q.z) - mx) : 0.f) : 0.f;
+      // (a part with nothing has base 0, which can lie above the row's by any amount: no factor for it)
+      auto part_of = [](float sum, float power) { return sum == 0.f ? 0.f : sum * expf(power); };
+      const float mass = warp_add(part_of(q.y, (base_of(q.x) - high) * terms.inv)) + expf(in.tail - high * terms.inv);
+      list = make_float4(high, logf(mass), mx, warp_add(part_of(q.w, (base_of(q.z) - mx) * terms.inv)));
+      list_plain = kBoth ? warp_add(has ? part_of(sh.lists_plain[lane], base_of(q.z) - mx) : 0.f) : 0.f;
     }
     const RowTotal r = row_total(rs, list, list_plain, terms, kBoth);
     const float tail_p = in.tail - list.x * terms.inv - list.y, tail_q = r.lr;

@@ -181,9 +181,13 @@ typedef struct {
  *     dlogits[t, v] = grad_scale dloss[t] / dlogits[t, v].
  * Terms are summed as p log(p / q) - p + q, none of which is negative, so a small
  * divergence is not a difference of large sums; the rest's share is summed without
- * the listed entries.  A kd that is infinite by the teacher giving nothing (reverse)
- * leaves the row a zero gradient, as does a row with nothing but -inf.  A list with
- * nothing in it (nor a tail) has kd 0.  labels (int32 [T]) may be NULL with ce_weight
+ * the listed entries.  What vanishes is told by logarithms: a share of p or q counts as
+ * nothing from e^-745 on (where 64 bits end too; a finite mask hides as -inf does), and
+ * above that kd and the gradient are what the formulas give, however small the share.
+ * A kd that is infinite by the teacher giving nothing (reverse) leaves the row a zero
+ * gradient, as does a row with nothing but -inf; one that is by the student hiding what
+ * the teacher lists (forward) keeps the entries' gradient -p.  A list with nothing in it
+ * (nor a tail) has kd 0.  labels (int32 [T]) may be NULL with ce_weight
  * 0: every row counts; else a negative label marks a row that does not.  weight (fp32
  * [T]) NULL stands for ones; weight 0: loss 0 and a zero gradient row.  An id >= V or
  * listed twice in a row sets LORA_DERR_BAD_LABEL and the row does not count.

@@ -8,6 +8,12 @@
 //     reverse: e = -d,                   C = sum of q e over the outcomes
 //     jsd:     e = -(1 - mix) log(m / q), C likewise
 // where q is the logit's own share and e its outcome's.
+//
+// What vanishes is told by logarithms: e^lq is 0 in fp32 from lq = -104 on, where p (lp - lq) is
+// still a number.  From -745 on, where 64 bits end too, a share counts as nothing, as that of
+// an entry at -inf does: a finite mask hides.
+// The rest's entries share its gradient by their part of the rest's sum, taken over the rest's own
+// largest logit, so nothing is divided by a share that has vanished.
 #include <algorithm>
 #include <cstring>
 
@@ -30,29 +36,32 @@ __device__ __forceinline__ float term(float p, float m, float x, float w) {
   return p == 0.f ? m : y;
 }
 
+constexpr float kNothing = -745.f;  // a logarithm below it is that of no share at all
+
 // One outcome of probabilities e^lp (teacher) and e^lq (student).
 struct Outcome {
   float kd;     // its term
   float mass;   // q e, of C
   float share;  // of its gradient: q (e - C) without C
 };
-// e of an outcome with d = log p - log q.
+// e of an outcome with d = log p - log q (reverse and jsd).
 __device__ __forceinline__ float slope_of(int kind, float mix, float d) {
   if (kind == LORA_DISTILL_REVERSE) return -d;
-  if (kind == LORA_DISTILL_FORWARD) return d < -80.f ? 1.f : -expm1f(d);
   return (mix - 1.f) * (d > 0.f ? d + log1pf((1.f - mix) * expm1f(-d)) : log1pf(mix * expm1f(d)));
 }
 __device__ __forceinline__ Outcome outcome(int kind, float mix, float lp, float lq) {
+  if (lp < kNothing) lp = -INF_F;
+  if (lq < kNothing) lq = -INF_F;
   const float p = expf(lp), q = expf(lq), d = lp - lq;
   Outcome o;
   if (kind == LORA_DISTILL_FORWARD) {
     const float w = expm1f(-d);  // q / p - 1
-    o.kd = q == 0.f ? INF_F : term(p, q, -d, w);
+    o.kd = lq == -INF_F ? INF_F : term(p, q, -d, w);
     o.mass = 0.f;
     o.share = p == 0.f || d < -80.f ? q - p : p * w;
   } else if (kind == LORA_DISTILL_REVERSE) {
-    o.kd = p == 0.f ? INF_F : term(q, p, d, expm1f(d));
-    o.mass = o.share = q == 0.f ? 0.f : q * -d;
+    o.kd = lp == -INF_F ? INF_F : term(q, p, d, expm1f(d));
+    o.mass = o.share = lq == -INF_F ? 0.f : lp == -INF_F ? INF_F : q * -d;
   } else {
     // u = log(m / q), v = log(m / p)
     float u, v;
@@ -67,8 +76,19 @@ __device__ __forceinline__ Outcome outcome(int kind, float mix, float lp, float 
     o.kd = mix * term(p, m, v, expm1f(v)) + (1.f - mix) * term(q, m, u, expm1f(u));
     o.mass = o.share = q == 0.f ? 0.f : q * (mix - 1.f) * u;
   }
-  if (p == 0.f && q == 0.f) o.kd = o.mass = o.share = 0.f;
+  if (lp == -INF_F && lq == -INF_F) o.kd = o.mass = o.share = 0.f;
   return o;
+}
+// q (e - C) of the rest, whose entries share it: 0 where the student gives the rest nothing.
+__device__ __forceinline__ float rest_share(int kind, float mix, float lp, float lq, float C) {
+  if (lq < kNothing) return 0.f;
+  const float d = lp - lq;
+  if (kind == LORA_DISTILL_FORWARD) {  // q - p by the greater of the two
+    const float s = expf(fmaxf(lp, lq)) * expm1f(-fabsf(d));
+    return d > 0.f ? s : -s;
+  }
+  const float q = expf(lq);
+  return q == 0.f ? 0.f : q * (slope_of(kind, mix, d) - C);
 }
 
 __device__ __noinline__ Outcome other_outcome(int kind, float mix, float lp, float lq) { return outcome(kind, mix, lp, lq); }
@@ -97,22 +117,22 @@ struct DistillArgs {
 };
 
 // What the rows' gradients are made of: entry v (not listed, not the label) is
-//     kd 2^((x - base) log2(e) / temperature - l2) + ce 2^((x - base) log2 e - l2_plain).
+//     kd 2^((x - base) log2(e) / temperature) + ce 2^((x - base) log2 e - l2_plain).
 struct Slope {
-  float base, kd, l2, ce, l2_plain;
+  float base, kd, ce, l2_plain;
 };
 
 template <typename E, bool kBoth>
 __device__ __forceinline__ uint4 slope_vector(const uint4& x, const Slope& g, const Terms& terms, const Terms& plain) {
   constexpr int kPairs = Elem<E>::kPairs;
-  const uint64_t nb = pair_of(-g.base, -g.base), hi = pair_of(terms.near, terms.near), nl = pair_of(-g.l2, -g.l2);
+  const uint64_t nb = pair_of(-g.base, -g.base), hi = pair_of(terms.near, terms.near);
   const uint64_t c = pair_of(g.kd, g.kd);
   uint64_t f[kPairs];
 #pragma unroll
   for (int j = 0; j < kPairs; ++j) {
     const uint64_t d = add2(Elem<E>::pair(x, j), nb);
     float a, b;
-    split(fma2(d, hi, nl), a, b);
+    split(mul2(d, hi), a, b);
     f[j] = mul2(c, pair_of(ex2(a), ex2(b)));
     if (kBoth) {
       split(fma2(d, pair_of(plain.near, plain.near), pair_of(-g.l2_plain, -g.l2_plain)), a, b);
@@ -124,7 +144,7 @@ __device__ __forceinline__ uint4 slope_vector(const uint4& x, const Slope& g, co
 template <bool kBoth>
 __device__ __forceinline__ float slope_entry(float x, const Slope& g, const Terms& terms, const Terms& plain) {
   const float d = x - g.base;
-  float f = g.kd * ex2(fmaf(d, terms.near, -g.l2));
+  float f = g.kd * ex2(d * terms.near);
   if (kBoth) f = fmaf(g.ce, ex2(fmaf(d, plain.near, -g.l2_plain)), f);
   return f;
 }
@@ -240,9 +260,11 @@ __device__ __forceinline__ RowSum join_parts(const float4* part, int parts, cons
 
 // With the list: the student's totals and what both kinds of warps take from them.
 struct RowTotal {
-  float base, rest, lt, l1;  // lt: log of the sum at the temperature, l1: at temperature 1
-  float lr;                  // log of the rest's share
-  bool none, taught;         // nothing is visible; the teacher says something (and the student too)
+  float base, lt, l1;  // lt: log of the sum at the temperature, l1: at temperature 1
+  float lr;            // log of the rest's share
+  float m, rest;       // the rest's largest logit and its sum over that
+  float scale;         // an entry's share of the row over its term of that sum
+  bool none, taught;   // nothing is visible; the teacher says something (and the student too)
 };
 __device__ __forceinline__ RowTotal row_total(const RowSum& s, const float4& list, float list_plain, const Terms& terms, bool both) {
   RowTotal r;
@@ -251,8 +273,11 @@ __device__ __forceinline__ RowTotal row_total(const RowSum& s, const float4& lis
   r.base = base_of(lists ? list.z : s.m);
   const float fall = some ? fminf(s.m, list.z) - r.base : 0.f;  // of the other
   const float e = expf(fall * terms.inv);
-  r.rest = lists ? s.rest * e : s.rest;
-  const float total = r.rest + (lists ? list.w : some ? list.w * e : 0.f);
+  const float down = lists ? e : 1.f, rest = s.rest * down;
+  const float total = rest + (lists ? list.w : some ? list.w * e : 0.f);
+  r.m = base_of(s.m);
+  r.rest = s.rest;
+  r.scale = __fdividef(down, total);
   r.lt = r.l1 = logf(total);
   if (both) {
     const float e1 = expf(fall);
@@ -260,8 +285,19 @@ __device__ __forceinline__ RowTotal row_total(const RowSum& s, const float4& lis
   }
   r.none = total == 0.f;
   r.taught = list.y != -INF_F && !r.none;
-  r.lr = logf(__fdividef(r.rest, total));
+  // (from far below the list by the logarithm of the rest's own sum: its part of the row's vanishes)
+  const bool far = lists && fall * terms.inv < -60.f;
+  r.lr = logf(far ? s.rest : __fdividef(rest, total)) + (far ? fall * terms.inv - r.lt : 0.f);
   return r;
+}
+// The slope of a row whose gradient of kd has the factor kw and of ce cw, with the rest's share of the former.  At
+// temperature 1 the two share their powers.
+template <bool kBoth>
+__device__ __forceinline__ Slope rest_slope(const RowTotal& r, float kw, float cw, float share) {
+  const float l1 = r.l1 + (r.base - r.m);
+  Slope g{r.m, share == 0.f ? 0.f : kw * __fdividef(share, r.rest), cw, l1 * kLog2e + l1 * kLog2eLo};
+  if (!kBoth && cw != 0.f) g.kd += cw * r.scale;
+  return g;
 }
 
 template <typename E, int kG, int kVec, bool kBoth>
@@ -396,18 +432,14 @@ __global__ void __launch_bounds__(kG + 32, kVec > 8 ? 2 : 3) held_kernel(const _
       const float4 list = sh.list[turn];
       const RowTotal r_ = row_total(s, list, sh.list_plain[turn], terms, kBoth);
       // the rest's slope
-      float slope = 0.f, C = 0.f;
+      float C = 0.f;
       if (!forward) meet<3, kAll>();
       if (!forward) C = sh.C;
-      if (r_.taught && !(r_.rest == 0.f)) {
-        const float d = in.tail - list.x * terms.inv - list.y - r_.lr;
-        slope = slope_of(a.opt.kind, a.opt.mix, d) - C;
-      }
       float kw, cw;
       factors(r_, in, s.bad, C, &kw, &cw);
-      // at temperature 1 the two parts of the gradient share their powers
-      Slope g{r_.base, kw != 0.f ? kw * slope : 0.f, r_.lt * kLog2e + r_.lt * kLog2eLo, cw, r_.l1 * kLog2e + r_.l1 * kLog2eLo};
-      if (!kBoth) g.kd += cw;
+      const float share =
+          kw != 0.f && r_.taught ? rest_share(a.opt.kind, a.opt.mix, in.tail - list.x * terms.inv - list.y, r_.lr, C) : 0.f;
+      const Slope g = rest_slope<kBoth>(r_, kw, cw, share);
       E* const out = a.dlogits == nullptr || dead ? nullptr : out_at(t);
       if (out != nullptr) {
         if (g.kd == 0.f && (!kBoth || cw == 0.f)) {
@@ -598,10 +630,9 @@ __global__ void __launch_bounds__(kG + 32, kVec > 8 ? 2 : 3) held_kernel(const _
             out[v] = Elem<E>::put(y);
           }
           if (lane == 0 && label_mine && !label_listed && cw != 0.f) {
-            const float slope =
-                kw != 0.f && r.taught && !(r.rest == 0.f) ? slope_of(a.opt.kind, a.opt.mix, tail_p - tail_q) - C : 0.f;
-            const float x = xl - r.base, q = expf(x * terms.inv - r.lt);
-            out[label] = Elem<E>::put(kw * slope * q + cw * ((kBoth ? expf(x - r.l1) : q) - 1.f));
+            const float share = kw != 0.f && r.taught ? rest_share(a.opt.kind, a.opt.mix, tail_p, tail_q, C) : 0.f;
+            const float x = xl - r.base, part = share == 0.f ? 0.f : share * __fdividef(expf((xl - r.m) * terms.inv), r.rest);
+            out[label] = Elem<E>::put(kw * part + cw * ((kBoth ? expf(x - r.l1) : expf(x * terms.inv - r.lt)) - 1.f));
           }
         }
       }
@@ -847,10 +878,8 @@ __global__ void __launch_bounds__(kT, 1024 / kT) stream_kernel(const __grid_cons
     const float gs = r.none || in.weight == 0.f ? 0.f : a.opt.grad_scale * in.weight;
     const float kw = gs != 0.f && fabsf(C) != INF_F ? gs * a.opt.kd_weight * terms.inv : 0.f;
     const float cw = a.opt.ce_weight > 0.f ? gs * a.opt.ce_weight : 0.f;
-    const float slope =
-        kw != 0.f && r.taught && !(r.rest == 0.f) ? slope_of(a.opt.kind, a.opt.mix, tail_p - tail_q) - C : 0.f;
-    Slope g{r.base, kw != 0.f ? kw * slope : 0.f, r.lt * kLog2e + r.lt * kLog2eLo, cw, r.l1 * kLog2e + r.l1 * kLog2eLo};
-    if (!kBoth) g.kd += cw;
+    const float share = kw != 0.f && r.taught ? rest_share(a.opt.kind, a.opt.mix, tail_p, tail_q, C) : 0.f;
+    const Slope g = rest_slope<kBoth>(r, kw, cw, share);
     if (out != nullptr) {
       if (g.kd == 0.f && (!kBoth || cw == 0.f)) {
         zero_share<E, kT>(c, out, a.V, id);
@@ -905,8 +934,8 @@ __global__ void __launch_bounds__(kT, 1024 / kT) stream_kernel(const __grid_cons
         out[v] = Elem<E>::put(y);
       }
       if (id == kT - 1 && label >= 0 && !label_listed && cw != 0.f) {
-        const float d = xl - r.base, q = expf(d * terms.inv - r.lt);
-        out[label] = Elem<E>::put(kw * slope * q + cw * ((kBoth ? expf(d - r.l1) : q) - 1.f));
+        const float d = xl - r.base, part = share == 0.f ? 0.f : share * __fdividef(expf((xl - r.m) * terms.inv), r.rest);
+        out[label] = Elem<E>::put(kw * part + cw * ((kBoth ? expf(d - r.l1) : expf(d * terms.inv - r.lt)) - 1.f));
       }
     }
     if (warp == kW - 1) {

@@ -93,3 +93,86 @@ def test_absent_parts_of_lists_far_from_zero(T, V, k, kind):
         elif t % 4 == 2:
             values[t] = -np.inf
     check_far(x, ids, values.astype(np.float32), rest.astype(np.float32), labels, kind=kind, mix=0.4, ce_weight=0.25)
+
+
+GAPS = (80, 92, 95, 104, 110, 150, 300, 700)
+
+
+def gapped(T, V, k, temperature, gaps, seed):
+    """Rows with one part far below the others, `gap` temperatures: of the student a listed entry, the rest, the whole
+    list; of the teacher an entry, the rest, the whole list."""
+    rng = np.random.default_rng(seed)
+    n = 6 * len(gaps)
+    x, ids, values, rest, labels = batch(rng, n, V, k, absent=0.0)
+    x, values = x * min(1.0, temperature), values.astype(np.float64) * min(1.0, temperature)
+    top = np.log(np.exp(values / temperature - values.max() / temperature).sum(1)) + values.max() / temperature
+    rest = top - rng.uniform(0.2, 6, n)
+    for t in range(n):
+        gap, part = gaps[t // 6] * temperature, t % 6
+        others = np.ones(V, dtype=bool)
+        others[ids[t]] = False
+        if part == 0:
+            x[t, ids[t, 1]] = x[t].max() - gap
+        elif part == 1:
+            x[t, others] += x[t, ids[t]].max() - x[t, others].max() - gap
+        elif part == 2:
+            x[t, ids[t]] += x[t, others].max() - x[t, ids[t]].max() - gap
+        elif part == 3:
+            values[t, 1] = values[t].max() - gap
+        elif part == 4:
+            rest[t] = top[t] - gap / temperature
+        else:
+            values[t] -= gap + values[t].max() - rest[t] * temperature
+    at = rng.permutation(n)[np.arange(T) % n] if T < n else np.arange(T) % n
+    return x[at], ids[at], values[at].astype(np.float32), rest[at].astype(np.float32), labels[at]
+
+
+@pytest.mark.parametrize("kind", ["forward", "reverse", "jsd"])
+@pytest.mark.parametrize("temperature", [1.0, 0.1, 2.0])
+@pytest.mark.parametrize("T,V,k", [(310, 700, 32), (310, 701, 33), (160, 9000, 33), (96, 3000, 256), (60, 9003, 200), (72, 40001, 40)])
+def test_shares_that_vanish(T, V, k, temperature, kind):
+    """A divergence and a gradient that are numbers stay so where a share is below what fp32 holds."""
+    cuda_or_skip()
+    rows = gapped(T, V, k, temperature, GAPS, T + V)
+    far = max(GAPS) * max(1.0, temperature)
+    check_far(*rows, dtype=F32, far=far, kind=kind, mix=0.4, temperature=temperature)
+    check_far(*rows, dtype=F32, far=far, kind=kind, mix=0.4, temperature=temperature, ce_weight=0.3, kd_weight=0.7)
+    if temperature >= 1.0:
+        check_far(*rows, dtype=BF16, far=far, kind=kind, mix=0.4, temperature=temperature, kd_weight=temperature ** 2)
+
+
+@pytest.mark.parametrize("kind", ["forward", "reverse", "jsd"])
+@pytest.mark.parametrize("gap", [92, 110, 700])
+@pytest.mark.parametrize("T,V,k", [(6, 300001, 40), (6, 40001, 100), (6, 128256, 256)])
+def test_shares_that_vanish_in_long_rows(T, V, k, gap, kind):
+    cuda_or_skip()
+    rows = gapped(T, V, k, 1.0, (gap,), V + gap)
+    for dtype in (F32, BF16):
+        check_far(*rows, dtype=dtype, far=gap, kind=kind, mix=0.4, ce_weight=0.3)
+
+
+@pytest.mark.parametrize("V", [600, 9000, 70000])
+def test_shares_of_less_than_64_bits_hold_are_none(V):
+    """A finite mask over what the teacher lists, or over the rest, or in the teacher's list hides like -inf."""
+    cuda_or_skip()
+    x, ids, values, rest, labels = some(6, V, 8)
+    hidden = x.copy(), values.copy(), rest.copy()
+    for low, (y, w, r) in ((-3000.0, (x, values, rest)), (-np.inf, hidden)):
+        y[0, ids[0, 2]] = low
+        y[1] = np.where(np.isin(np.arange(V), ids[1]), y[1], low)
+        y[2, ids[2]] = low
+        w[3, 5] = low
+        r[4] = low
+        w[5] = low
+    for kind in ("forward", "reverse", "jsd"):
+        for temperature in (1.0, 2.0):
+            kw = dict(kind=kind, temperature=temperature, mix=0.4)
+            a, b = run_loss(x, ids, values, rest, **kw), run_loss(hidden[0], ids, *hidden[1:], **kw)
+            for t in range(6):
+                # an entry that the teacher lists as -inf is of the rest, one at a mask is listed with nothing
+                if t in (3, 5):
+                    continue
+                assert np.array_equal(a[0][t], b[0][t]) and np.array_equal(a[3][t], b[3][t]), (kind, t)
+            want = R.distill(x, ids, values.astype(np.float64), rest, **kw)
+            assert np.array_equal(np.isfinite(a[1]), np.isfinite(want["kd"])), kind
+            assert (a[3][~np.isfinite(a[1]) & (kind == "reverse")] == 0).all()

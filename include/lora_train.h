@@ -146,7 +146,7 @@ lora_status_t lora_policy_loss(const void* logits, int64_t ld, int32_t dtype, co
  * (device fp32 [T], may be NULL; -inf where nothing is left).  Entries of -inf are
  * not listed: their places hold id -1 and value -inf.  labels (may be NULL: every
  * row counts): a row with a negative label lists nothing, its tail is -inf.
- * 1 <= k <= min(V, LORA_TOPK_MAX), temperature > 0.
+ * 1 <= k <= min(V, LORA_TOPK_MAX), temperature > 0.  V above 0x7fff0000 is LORA_ERR_UNSUPPORTED.
  */
 lora_status_t lora_topk_logits(const void* logits, int64_t ld, int32_t dtype, const int32_t* labels, int32_t T,
                                int32_t V, int32_t k, float temperature, int32_t* ids, float* values, float* tail,

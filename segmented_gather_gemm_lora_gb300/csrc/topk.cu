@@ -42,6 +42,8 @@ constexpr int kAhead = kT > 256 ? 2 : 1;  // chunks under way: few rows wait for
 constexpr int kResident = 896;  // threads an SM (4096 x 128256: 234 us; 640 258, 768 243, 1024, which spills, 310)
 constexpr float kLowest = -3.402823466e38f;  // below it only -inf, which is not listed
 
+constexpr int kMostEntries = 0x7fff0000;  // steps over a row end past it by less than 2^16, within 32 bits
+
 struct TopkArgs {
   const void* logits;
   long long ld;
@@ -634,7 +636,7 @@ extern "C" lora_status_t lora_topk_logits(const void* logits, int64_t ld, int32_
   const lora_status_t st = check_logits(logits, ld, dtype, labels != nullptr ? labels : ids, T, V);
   if (st != LORA_OK) return st;
   if (k < 1 || k > V || !(temperature > 0.f) || temperature == INFINITY) return LORA_ERR_INVALID_ARG;
-  if (k > LORA_TOPK_MAX) return LORA_ERR_UNSUPPORTED;
+  if (k > LORA_TOPK_MAX || V > kMostEntries) return LORA_ERR_UNSUPPORTED;
   if (T == 0) return LORA_OK;
   if (!f32_ok(ids) || !f32_ok(values) || !aligned_to(tail, 4)) return LORA_ERR_INVALID_ARG;
   TopkArgs a;

@@ -58,3 +58,21 @@ def test_listed_edges_of_crowded_rows(T, V, k, dtype):
 def test_listed_edges_of_lists_long_for_their_row(T, V, k, dtype):
     cuda_or_skip()
     check(np.random.default_rng(V + k).normal(size=(T, V)) * 3, k, dtype, first=5, pad=0)
+
+
+def test_the_longest_rows():
+    """As many entries as 32-bit steps allow: planted ones at both ends and between, and a row of ties."""
+    cuda_or_skip()
+    V, k = 0x7fff0000, 70
+    x = torch.zeros(1, V, dtype=BF16, device="cuda")
+    at = torch.cat([torch.arange(30), V - 1 - torch.arange(30), torch.tensor([V // 2, V // 3, V // 5])]).cuda()
+    ids, values, tail = torch.empty(1, k, dtype=torch.int32, device="cuda"), torch.empty(1, k, device="cuda"), torch.empty(1, device="cuda")
+    B.lora_topk_logits(x, ids, values, tail)
+    assert torch.equal(ids[0].cpu(), torch.arange(k, dtype=torch.int32)) and bool((values == 0).all())
+    # sums of ones are exact up to 2^24, and their joins round 512 threads' parts: 2^-20; the logarithm 2^-19
+    assert abs(float(tail) - np.log(V - k)) <= 2.0 ** -18
+    x[0, at] = torch.arange(at.numel(), 0, -1, device="cuda").to(BF16)
+    B.lora_topk_logits(x, ids, values, tail)
+    rest = torch.arange(30, 30 + k - at.numel())
+    assert torch.equal(ids[0].cpu().long(), torch.cat([at.cpu(), rest]))
+    assert abs(float(tail) - np.log(V - k)) <= 2.0 ** -18

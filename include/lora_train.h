@@ -146,7 +146,7 @@ lora_status_t lora_policy_loss(const void* logits, int64_t ld, int32_t dtype, co
  * (device fp32 [T], may be NULL; -inf where nothing is left).  Entries of -inf are
  * not listed: their places hold id -1 and value -inf.  labels (may be NULL: every
  * row counts): a row with a negative label lists nothing, its tail is -inf.
- * 1 <= k <= min(V, LORA_TOPK_MAX), temperature > 0.  V above 0x7fff0000 is LORA_ERR_UNSUPPORTED.
+ * 1 <= k <= min(V, LORA_TOPK_MAX), temperature >= 2^-126.  V above 0x7fff0000 is LORA_ERR_UNSUPPORTED.
  */
 lora_status_t lora_topk_logits(const void* logits, int64_t ld, int32_t dtype, const int32_t* labels, int32_t T,
                                int32_t V, int32_t k, float temperature, int32_t* ids, float* values, float* tail,
@@ -159,7 +159,7 @@ lora_status_t lora_topk_logits(const void* logits, int64_t ld, int32_t dtype, co
 
 typedef struct {
   int32_t kind;      /* LORA_DISTILL_* */
-  float temperature; /* > 0, of teacher and student (not of the cross-entropy) */
+  float temperature; /* >= 2^-126, of teacher and student (not of the cross-entropy) */
   float mix;         /* 0 < mix < 1: the teacher's share of LORA_DISTILL_JSD's mixture */
   float kd_weight;   /* >= 0: weight of the divergence (temperature^2 keeps its gradient's size) */
   float ce_weight;   /* >= 0: weight of the labels' cross-entropy; 0: labels only say which rows count */

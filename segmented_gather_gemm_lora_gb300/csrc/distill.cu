@@ -1023,7 +1023,7 @@ lora_status_t lora_distill_loss(const void* logits, int64_t ld, int32_t dtype, c
   if (k > LORA_TOPK_MAX) return LORA_ERR_UNSUPPORTED;
   if (opts->kind != LORA_DISTILL_FORWARD && opts->kind != LORA_DISTILL_REVERSE && opts->kind != LORA_DISTILL_JSD)
     return LORA_ERR_INVALID_ARG;
-  if (!(opts->temperature > 0.f) || opts->temperature == INFINITY) return LORA_ERR_INVALID_ARG;
+  if (!temperature_ok(opts->temperature)) return LORA_ERR_INVALID_ARG;
   if (opts->kind == LORA_DISTILL_JSD && !(opts->mix > 0.f && opts->mix < 1.f)) return LORA_ERR_INVALID_ARG;
   if (!(opts->kd_weight >= 0.f) || !(opts->ce_weight >= 0.f)) return LORA_ERR_INVALID_ARG;
   if ((st = check_grad(logits, ld, dtype, dlogits, ldd, T, V)) != LORA_OK || T == 0) return st;

@@ -305,6 +305,11 @@ __device__ __forceinline__ uint4 without(const uint4& v, uint32_t m, float) {
 
 inline Terms terms_of(float temperature) { return Terms{(float)(1.4426950408889634 / (double)temperature), 1.f / temperature}; }
 
+// A temperature whose factors are finite: a difference of 0 times them stays 0.
+inline bool temperature_ok(float temperature) {
+  return temperature >= 1.1754943508222875e-38f && temperature <= 3.402823466e38f;  // normal numbers
+}
+
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 inline bool f32_ok(const void* p) { return p != nullptr && aligned_to(p, 4); }

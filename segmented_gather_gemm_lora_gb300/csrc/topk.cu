@@ -635,7 +635,7 @@ extern "C" lora_status_t lora_topk_logits(const void* logits, int64_t ld, int32_
   // without labels the ids' address stands for theirs in the check
   const lora_status_t st = check_logits(logits, ld, dtype, labels != nullptr ? labels : ids, T, V);
   if (st != LORA_OK) return st;
-  if (k < 1 || k > V || !(temperature > 0.f) || temperature == INFINITY) return LORA_ERR_INVALID_ARG;
+  if (k < 1 || k > V || !temperature_ok(temperature)) return LORA_ERR_INVALID_ARG;
   if (k > LORA_TOPK_MAX || V > kMostEntries) return LORA_ERR_UNSUPPORTED;
   if (T == 0) return LORA_OK;
   if (!f32_ok(ids) || !f32_ok(values) || !aligned_to(tail, 4)) return LORA_ERR_INVALID_ARG;

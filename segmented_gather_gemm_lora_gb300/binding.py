@@ -779,19 +779,21 @@ def lora_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch
 
 
 def _one_device(stream, first: torch.Tensor, *others: Optional[torch.Tensor]) -> int:
-    """The stream's handle.  Refuses tensors that do not share a CUDA device, or that of the current stream where none
-    is given: the library would read their addresses on the device the call runs on."""
+    """The stream's handle.  Refuses tensors that do not all lie on the current CUDA device, and a stream of another one:
+    the library launches on the current device, and would read their addresses there."""
     d = first.get_device()
     if d < 0:
         raise ValueError("expected tensors on a CUDA device")
     for t in others:
         if t is not None and t.get_device() != d:
             raise ValueError("expected tensors on one CUDA device")
-    if stream is not None:
-        return _handle(stream)
     if d != torch._C._cuda_getDevice():
-        raise ValueError("expected tensors on the current CUDA device (%d), or a stream of theirs" % torch.cuda.current_device())
-    return torch._C._cuda_getCurrentRawStream(d)
+        raise ValueError("expected tensors on the current CUDA device (%d)" % torch.cuda.current_device())
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(d)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != d:
+        raise ValueError("expected a stream of the tensors' device")
+    return _handle(stream)
 
 
 def _err_word(err: Optional[torch.Tensor]) -> int:

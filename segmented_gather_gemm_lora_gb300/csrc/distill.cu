@@ -32,7 +32,8 @@ namespace {
 __device__ __forceinline__ float term(float p, float m, float x, float w) {
   // near 0 by the series of (w - x) / x^2: the next term is 1e-7 of the sum
   const float s = fmaf(x, fmaf(x, fmaf(x, fmaf(x, fmaf(x, 1.f / 5040.f, 1.f / 720.f), 1.f / 120.f), 1.f / 24.f), 1.f / 6.f), 0.5f);
-  const float y = fabsf(x) < 0.35f ? p * (x * x) * s : x < 80.f ? p * (w - x) : m - p * x;
+  // (from x = 16 on without p w, in which a p of few bits would count)
+  const float y = fabsf(x) < 0.35f ? p * (x * x) * s : x < 16.f ? p * (w - x) : m - p * (x + 1.f);
   return p == 0.f ? m : y;
 }
 
@@ -58,7 +59,7 @@ __device__ __forceinline__ Outcome outcome(int kind, float mix, float lp, float 
     const float w = expm1f(-d);  // q / p - 1
     o.kd = lq == -INF_F ? INF_F : term(p, q, -d, w);
     o.mass = 0.f;
-    o.share = p == 0.f || d < -80.f ? q - p : p * w;
+    o.share = d < -16.f ? q - p : p * w;
   } else if (kind == LORA_DISTILL_REVERSE) {
     o.kd = lp == -INF_F ? INF_F : term(q, p, d, expm1f(d));
     o.mass = o.share = lq == -INF_F ? 0.f : lp == -INF_F ? INF_F : q * -d;

@@ -19,9 +19,10 @@ FORMS = [(310, 700, 32), (310, 700, 33), (160, 9000, 33), (160, 9000, 200), (3, 
 
 def check_far(x, ids, values, tail, labels=None, dtype=F32, far=0.0, **kw):
     """Against the plain form.  A logarithm of p or q is off by three roundings of the largest logarithm of the row (the
-    listed entries' and `far`, those of the rest) and of a sum's logarithm below 16, and by the sums' errors (2^-19);
-    kd's derivative with respect to one is p - q, a term's own arithmetic is off by 2^-18 of it; a gradient's parts move
-    by as much of themselves, four of them, and are rounded once."""
+    listed entries' and `far`, those of the rest) and of a sum's logarithm below 16, and by the sums' errors (2^-19): d
+    in all.  kd = sum of p (log p - log q) - p + q moves by q - p with log q, at most 2 d together, and by
+    p (log p - log q) with log p, where those of one sign add up to little more than kd itself: by d of kd; a term's own
+    arithmetic is off by 2^-18 of it.  A gradient's parts move by d of themselves, four of them, and are rounded once."""
     loss, kd, ce, grad = run_loss(x, ids, values, tail, labels, dtype=dtype, **kw)
     x = device(x, dtype)[2]
     want = R.distill(x, ids, values.astype(np.float32).astype(np.float64), tail, labels, **kw)
@@ -31,7 +32,7 @@ def check_far(x, ids, values, tail, labels=None, dtype=F32, far=0.0, **kw):
         with np.errstate(invalid="ignore"):
             assert np.array_equal(got[~np.isfinite(w)], w[~np.isfinite(w)]), (name, got, w)
             scale = kw.get("kd_weight", 1.0) + kw.get("ce_weight", 0.0) if name == "loss" else 1.0
-            tol = scale * 2 * d + 2.0 ** -18 * np.abs(w) + 1e-37
+            tol = scale * 2 * d + (2.0 ** -18 + d) * np.abs(w) + 1e-37
             bad = np.isfinite(w) & ~(np.abs(got - w) <= tol)
         assert not bad.any(), (name, got[bad][:4], w[bad][:4], tol[bad][:4])
     tol = 4 * d[:, None] * want["size"] + np.abs(want["grad"]) * (torch.finfo(dtype).eps / 2) * 1.01 + 2.0 ** -126
@@ -176,3 +177,21 @@ def test_shares_of_less_than_64_bits_hold_are_none(V):
             want = R.distill(x, ids, values.astype(np.float64), rest, **kw)
             assert np.array_equal(np.isfinite(a[1]), np.isfinite(want["kd"])), kind
             assert (a[3][~np.isfinite(a[1]) & (kind == "reverse")] == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["forward", "reverse", "jsd"])
+@pytest.mark.parametrize("T,V,k", [(310, 700, 32), (160, 9000, 200), (6, 40001, 100)])
+def test_gradients_of_entries_with_subnormal_shares(T, V, k, kind):
+    """One side's share of an entry below 2^-126, where fp32 has few bits, the other's not: the entry's gradient is the
+    greater one's, to its last digits."""
+    cuda_or_skip()
+    x, ids, values, rest, labels = some(T, V, k)
+    values = values.astype(np.float64)
+    top = np.log(np.exp(values).sum(1) + np.exp(rest))
+    for t in range(T):
+        for j in range(min(k, 12)):
+            values[t, j] = top[t] - (89, 95, 99, 102.5)[j % 4]
+            x[t, ids[t, j]] = x[t, ids[t, 12:]].max() - (20, 40, 70)[j % 3]
+        if t % 2:  # the other way round
+            values[t, :12], x[t, ids[t, :12]] = top[t] - 30, x[t, ids[t, 12:]].max() - (89 + 3.5 * (np.arange(12) % 4))
+    check_far(x, ids, values.astype(np.float32), rest, dtype=F32, far=110, kind=kind, mix=0.4)

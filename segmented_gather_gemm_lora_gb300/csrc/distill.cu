@@ -975,12 +975,12 @@ lora_status_t launch_stream(DistillArgs& a, cudaStream_t s) {
 // The form of the rows (device times in us on a GB300, 64 listed, forward; streamed with 256 /
 // 512 / 1024 threads a row, 4 / 2 / 1 rows an SM at once):
 //  - held while the rows' clusters of 16 vectors a thread are one wave and a row is more than
-//    64 KB.  16 x 128256 bf16: 8.6, streamed 17.7 / 15.3 / 15.9; 64: 12.5, 21.4 / 16.6 / 16.7;
+//    64 KB.  16 x 128256 bf16: 8.5, streamed 17.7 / 15.3 / 15.9; 64: 12.5, 21.4 / 16.6 / 16.7;
 //    150 (two waves): 27.2, 23.4 / 19.0 / 18.4.  64 x 32000: 8.7, 8.1 / 8.0 / 9.1.
 //  - else streamed, with so many rows at once that L2 holds them.  8192 x 32000 bf16: 216 / 308 /
-//    463 (held 245); 4000 x 50257 with jsd 181 / 224 / 350 (270); 8192 x 128256 929 / 808 / 933
+//    463 (held 245); 4000 x 50257 with jsd 178 / 224 / 350 (270); 8192 x 128256 929 / 806 / 933
 //    (935); 2000 x 151936 fp32 584 / 545 / 509.
-//  - of short rows more at once, 64 / 128 / 256 threads: 8192 x 1000 32 / 50 / 87; 8192 x 5000 56 / 73 /
+//  - of short rows more at once, 64 / 128 / 256 threads: 8192 x 1000 34 / 50 / 87; 8192 x 5000 56 / 73 /
 //    99; 4096 x 10000 41 / 50 / 69; 4096 x 20000 74 / 72 / 88; 4096 x 32000 124 / 113 / 110. Few rows:
 //    600 x 5000 7.6 / 7.6 / 8.8, 300 x 10000 8.4 / 7.3 / 7.5.
 // The last warp has no entries: it works out the rest.

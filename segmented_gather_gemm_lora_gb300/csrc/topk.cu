@@ -7,18 +7,23 @@
 // entries at or above it, so a slot below it has nothing to list and its sum stands; the
 // others, k and some more, are read again (from L2), what reaches the value is listed and
 // the rest of them summed.  So the sum is of exactly the entries that are not listed, no
-// difference of large sums.  What is listed is put in order in runs of 32; an entry's place
-// is its place in its run and those that a search finds in the others.
+// difference of large sums (but for ties, below).  What is listed is put in order in runs of 32;
+// an entry's place is its place in its run and those that a search finds in the others.
 // Where too many entries tie with the k-th largest (a mask's lowest value, say) those above it
-// are listed so, then the first of the ties.  A row in which too many crowd in few slots
-// takes the slow way: a radix selection of the k best by passes over the row.
+// are listed so, then the first of the ties, which are taken out of the sum: at most half of it.
+// A row in which too many crowd in few slots takes the slow way: a radix selection of the k best
+// by passes over the row.  So do ordinary rows that are short for their list: with two or three
+// vectors a thread, more entries than there is room for reach what k threads' largest do
+// (8192 x 5000 bf16 with 250 listed 930 us, with 64 of 32000 94).
 // Places and orders of sums are fixed: the same inputs give the same bits.
 //
 // Keys are the values' bits made to order as integers; composite keys order as the
 // listing does, no two alike.
 //
-// What bounds it: of long rows memory and the exponentials (4096 x 128256 bf16, 64 listed: 237 us,
-// 4.4 TB/s; without tail 211); of short ones what is done once a row, about ten barriers.
+// What bounds it: of long rows latency (4096 x 128256 bf16, 64 listed: 236 us, 4.4 TB/s; without
+// tail 211): half of the issue slots are used and warps wait for loads, of which only one or two chunks
+// are on their way, and one of the next row while a row is finished; of short ones what is done once a
+// row, about ten barriers.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -595,7 +600,7 @@ lora_status_t launch(TopkArgs& a, cudaStream_t s) {
 }
 
 // The threads of a row (device times in us on a GB300, rows that fill the GPU unless
-// said, 768 threads an SM):
+// said; measured with 768 threads an SM, kResident 896 since):
 //  - the fewer, the more rows are under way and the less a row's fixed part costs: 8192 x 1000
 //    bf16 with 20 listed and 32 / 64 / 128 / 256 threads 28 / 44 / 63 / 145; 4096 x 20000 with 60
 //    listed - / 69 / 72 / 92;
